@@ -1,0 +1,109 @@
+/*
+ * awq_a8.h -- C ABI of libawq for 8-bit activations: the producers of a quantized layer's input
+ * (RMS norm with the residual's addition, gated activation), with an output in 8 bits and a
+ * scale per row, and the product of such activations with the packed 4-bit weight.
+ *
+ * The conventions of awq.h hold (device memory owned by the caller, argument errors returned
+ * synchronously, every call asynchronous on `stream`, nothing allocated, no state kept).  These
+ * calls carry no data-error flags: a row of the input that holds NaN or Inf gets the scale NaN,
+ * so every product that reads it is NaN (its codes are undefined); in a 16- or 32-bit output
+ * the row's own NaN or Inf shows.
+ */
+#ifndef AWQ_A8_H
+#define AWQ_A8_H
+
+#include "awq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of 8-bit activations, beside awq_dtype's F32 and BF16. */
+#define AWQ_DTYPE_I8 2   /* int8, codes -127 .. 127 */
+#define AWQ_DTYPE_E4M3 3 /* e4m3 without infinities (OCP), |code| <= 448 */
+
+/* Activations of awq_act_mul, beside awq.h's AWQ_ACT_GELU and AWQ_ACT_SILU. */
+#define AWQ_ACT_NONE 2
+
+/* ---------------------------------------------------------------------------------------
+ * The norm in front of a quantized layer (its gamma is where awq_fold_rows leaves 1/s):
+ *   h = x + r (h = x without R);   y = h / sqrt(mean_k h[k]^2 + eps) * gamma[k]
+ * h and y are formed in fp32, the mean from h before its rounding.
+ *   X      [M, K] of x_dtype (F32, BF16), row stride ldx
+ *   R      [M, K] of r_dtype (F32, BF16), row stride ldr, or NULL (no residual)
+ *   H      [M, K] of r_dtype, row stride ldh: h rounded once; may be R itself (ldh = ldr); NULL
+ *          without R, and where h is not wanted
+ *   gamma  [K] of g_dtype (F32, BF16)
+ *   eps    finite and positive
+ *   Y      [M, K] of y_dtype, row stride ldy: F32 or BF16 holds y rounded once; I8 or E4M3 holds
+ *          round(y / scale) to nearest even in the type, with
+ *          scale = max(max_k |y|, 2^-100) / Q,  Q = 127 (I8) or 448 (E4M3)
+ *   scale  fp32 [M] for an 8-bit Y, else ignored
+ * Any K.  H = R aside, outputs overlap no input and not each other.  A row whose sum of squares
+ * is not finite in fp32 (|h| around 1e19 and more, NaN, Inf) has y NaN.
+ * ------------------------------------------------------------------------------------- */
+AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const void* R,
+                        int r_dtype, int64_t ldr, void* H, int64_t ldh, const void* gamma, int g_dtype,
+                        float eps, void* Y, int y_dtype, int64_t ldy, float* scale, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The activation in front of a quantized layer:  y[m, k] = act(G[m, k]) * U[m, k] / s[k]
+ *   G, U   [M, K] of x_dtype (F32, BF16), row strides ldg, ldu (the halves of a fused gate/up
+ *          output are two such views); U NULL: no gate's product
+ *   act    AWQ_ACT_NONE, AWQ_ACT_GELU (0.5 x (1 + erf(x / sqrt 2))) or AWQ_ACT_SILU
+ *          (x / (1 + exp(-x)))
+ *   s      fp32 [K] or NULL: the runtime form of 1/s where no producer absorbed it; positive
+ *          (not checked here: the search and the pack did)
+ *   Y, y_dtype, ldy, scale   as awq_rmsnorm
+ * With act NONE and neither U nor s this quantizes given activations.  y is formed in fp32,
+ * within a few fp32 ulps of the exact value.  Any K.  Y may be G or U where it has their type
+ * and row stride, and overlaps them in no other way.
+ * ------------------------------------------------------------------------------------- */
+AWQ_API int awq_act_mul(const void* G, int x_dtype, int64_t M, int64_t K, int64_t ldg, const void* U,
+                        int64_t ldu, const float* s, int act, void* Y, int y_dtype, int64_t ldy,
+                        float* scale, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The artefact of awq_pack laid out for awq_w4a8, once per weight (4.25 bits per weight, N
+ * rounded up to 16, and 4 bytes per channel):
+ *   wt     device memory of at least awq_w4a8_weight_bytes(N, K) bytes, 256-byte aligned, in three
+ *          parts, each starting at a multiple of 256 bytes:
+ *            codes  for column tile c (channels n = 16 c + l % 16) and group g, 16 bytes per
+ *                   l < 64: the codes of k = 128 g + 32 (l / 16) .. + 31, four words of eight;
+ *                   byte b of a word holds code b (low nibble) and code b + 4 (high nibble)
+ *            steps  uint32 [tiles][K/128][16]: fp16 scales * 2^-e (low half), fp16 zeros (high)
+ *            powers fp32 [16 tiles]: 2^e, e per channel such that its largest step lies in
+ *                   [2^10, 2^11)
+ *   qweight, scales, zeros   as written by awq_pack (qweight 16-byte aligned)
+ * awq_w4a8_weight_bytes is 0 for sizes that awq_w4a8_weight rejects.
+ * ------------------------------------------------------------------------------------- */
+AWQ_API size_t awq_w4a8_weight_bytes(int64_t N, int64_t K);
+AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros,
+                            int64_t N, int64_t K, int32_t group, void* wt, size_t wt_bytes,
+                            awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The W4A8 product:
+ *   Y[m, n] = xscale[m] * sum_g scales[n, g] * sum_{k in g} Xq[m, k] (q[n, k] - zeros[n, g])
+ * on the 8-bit matrix cores: a code q is an int8 byte as it stands, and as an e4m3 byte it is
+ * exactly q 2^-9.  I8: the inner sums are exact integers; E4M3: exact products, fp32 sums.  The
+ * steps and the sum over groups are fp32; Y is rounded once.
+ *   Xq      [M, K] of x_dtype I8 or E4M3, row stride ldx, 16-byte aligned rows
+ *   xscale  fp32 [M]
+ *   wt      as written by awq_w4a8_weight for the same N and K
+ *   Y       [M, N] of y_dtype F32 or BF16, row stride ldy >= N
+ *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
+ *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
+ *           the same time need one each
+ * K is a multiple of 128.
+ * ------------------------------------------------------------------------------------- */
+AWQ_API size_t awq_w4a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M, int64_t K, int64_t ldx,
+                     const void* wt, int64_t N, int32_t group, void* Y, int y_dtype, int64_t ldy, void* ws,
+                     size_t ws_bytes, awq_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* AWQ_A8_H */

@@ -8,10 +8,11 @@ reference code rejects non-finite input ("AWQï¼šä¸ºä»€ä¹ˆ 4-bit æƒé‡é‡åŒ–è¦å
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -37,6 +38,7 @@ N_GRID = 20
 N_CLIP = 10
 ACT_GELU = 0
 ACT_SILU = 1
+ACT_NONE = 2
 
 _lib = None
 
@@ -104,6 +106,19 @@ def lib() -> ctypes.CDLL:
         L.awq_w4a16_workspace_bytes.argtypes = [i64, i64, ctypes.c_int]
         L.awq_w4a16_ws.restype = ctypes.c_int
         L.awq_w4a16_ws.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i64, i32, vp, i64, vp, sz, vp]
+        cf, ci = ctypes.c_float, ctypes.c_int
+        L.awq_rmsnorm.restype = ci
+        L.awq_rmsnorm.argtypes = [vp, ci, i64, i64, i64, vp, ci, i64, vp, i64, vp, ci, cf, vp, ci, i64, vp, vp]
+        L.awq_act_mul.restype = ci
+        L.awq_act_mul.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, ci, vp, ci, i64, vp, vp]
+        L.awq_w4a8_weight_bytes.restype = sz
+        L.awq_w4a8_weight_bytes.argtypes = [i64, i64]
+        L.awq_w4a8_weight.restype = ci
+        L.awq_w4a8_weight.argtypes = [vp, vp, vp, i64, i64, i32, vp, sz, vp]
+        L.awq_w4a8_workspace_bytes.restype = sz
+        L.awq_w4a8_workspace_bytes.argtypes = [i64, i64, i64]
+        L.awq_w4a8.restype = ci
+        L.awq_w4a8.argtypes = [vp, ci, vp, i64, i64, i64, vp, i64, i32, vp, ci, i64, vp, sz, vp]
         if L.awq_abi_version() != 8:
             raise ImportError("libawq ABI version mismatch")
         _lib = L
@@ -515,4 +530,199 @@ def w4a16(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, zeros: t
                               zeros.data_ptr(), N, group_size, Y.data_ptr(), Y.stride(0), ws_ptr, ws_bytes,
                               _stream(X.device)),
            "awq_w4a16_ws")
+    return Y
+
+
+# ---- 8-bit activations ----------------------------------------------------------------------
+
+
+class Act8(NamedTuple):
+    """8-bit activations: ``q`` int8 or float8_e4m3fn [M, K], ``scale`` fp32 [M]; row m stands for
+    q[m] * scale[m].  A row of an input that held NaN or Inf has scale NaN."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+_A8_DTYPE = {torch.float32: AWQ_DTYPE_F32, torch.bfloat16: AWQ_DTYPE_BF16, torch.int8: 2, torch.float8_e4m3fn: 3}
+_ACTS = {"gelu": ACT_GELU, "silu": ACT_SILU, "none": ACT_NONE}
+
+
+def _rows(t: torch.Tensor, name: str, dev: torch.device, shape: Optional[Tuple[int, int]] = None) -> int:
+    """Row stride of a 2-D device tensor [M, K] with unit stride along K."""
+    if t.dim() != 2 or t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D tensor on {dev if dev.type == 'cuda' else 'a GPU'}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # the stride of a single row says nothing
+
+
+def _code(t: torch.dtype, allowed: Tuple[torch.dtype, ...], name: str) -> int:
+    if t not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, not {t}")
+    return _A8_DTYPE[t]
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_CODES = (torch.int8, torch.float8_e4m3fn)
+
+
+def _a8_out(out, dtype: Optional[torch.dtype], M: int, K: int, dev: torch.device):
+    """(result, tensor, its dtype's code, row stride, scale pointer) of a row operator's output."""
+    if out is None:
+        dt = dtype if dtype is not None else torch.bfloat16
+        code = _code(dt, _FLOATS + _CODES, "dtype")
+        y = torch.empty((M, K), dtype=dt, device=dev)
+        if code < 2:
+            return y, y, code, K, None
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        return Act8(y, scale), y, code, K, scale.data_ptr()
+    eight = isinstance(out, tuple)
+    y = out[0] if eight else out
+    code = _code(y.dtype, _CODES if eight else _FLOATS, "out")
+    if dtype is not None and dtype != y.dtype:
+        raise ValueError("dtype and out disagree")
+    ld = _rows(y, "out", dev, (M, K))
+    if not eight:
+        return out, y, code, ld, None
+    scale = _out(out[1], (M,), torch.float32, dev, "out's scale")
+    return Act8(y, scale), y, code, ld, scale.data_ptr()
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _on(dev: torch.device):
+    """The device of the operands made current where it is not (a kernel launches on the current one)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+            dtype: Optional[torch.dtype] = None, out=None, residual_out: Optional[torch.Tensor] = None):
+    """RMS norm with the residual's addition: h = X + residual, y = h / sqrt(mean h^2 + eps) * gamma
+    (X [M, K], gamma [K] fp32 or bf16, residual [M, K] fp32 or bf16).  ``dtype`` is y's: float32,
+    bfloat16 (the default), or int8 / float8_e4m3fn with a scale per row, then y is an ``Act8``.
+    Returns y, or (y, h) with a residual, h rounded to the residual's type.  ``out`` (a tensor, or
+    an Act8) and ``residual_out`` take the results; ``residual_out`` may be ``residual`` itself."""
+    dev = X.device
+    ldx = _rows(X, "X", dev)
+    M, K = X.shape
+    if gamma.shape != (K,) or gamma.device != dev or not gamma.is_contiguous():
+        raise ValueError("gamma must be a contiguous vector of length K on X's device")
+    xc, gc = _code(X.dtype, _FLOATS, "X"), _code(gamma.dtype, _FLOATS, "gamma")
+    rc = ldr = ldh = 0
+    rp = hp = h = None
+    if residual is not None:
+        rc, ldr = _code(residual.dtype, _FLOATS, "residual"), _rows(residual, "residual", dev, (M, K))
+        h = residual_out if residual_out is not None else torch.empty((M, K), dtype=residual.dtype, device=dev)
+        if h.dtype != residual.dtype:
+            raise ValueError("residual_out must have residual's dtype")
+        ldh = _rows(h, "residual_out", dev, (M, K))
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    res, y, yc, ldy, sp = _a8_out(out, dtype, M, K, dev)
+    with _on(dev):
+        st = lib().awq_rmsnorm(X.data_ptr(), xc, M, K, ldx, rp, rc, ldr, hp, ldh, gamma.data_ptr(), gc, eps,
+                               y.data_ptr(), yc, ldy, sp, _raw_stream(dev))
+    _check(st, "awq_rmsnorm")
+    return res if residual is None else (res, h)
+
+
+def act_mul(G: torch.Tensor, U: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, act: str = "silu",
+            *, dtype: Optional[torch.dtype] = None, out=None):
+    """act(G) * U / s (``act`` "silu", "gelu" (exact) or "none"; U [M, K] of G's dtype, s fp32 [K],
+    both optional): the input of a layer behind a gate, or with "none" alone the quantization of
+    given activations.  G and U may be the halves of one gate/up output.  ``dtype`` and ``out`` as in
+    ``rmsnorm``; ``out`` may be G or U where it has their dtype and strides."""
+    dev = G.device
+    ldg = _rows(G, "G", dev)
+    M, K = G.shape
+    xc = _code(G.dtype, _FLOATS, "G")
+    up, ldu = None, 0
+    if U is not None:
+        if U.dtype != G.dtype:
+            raise TypeError("U must have G's dtype")
+        up, ldu = U.data_ptr(), _rows(U, "U", dev, (M, K))
+    if s is not None and (s.shape != (K,) or s.dtype != torch.float32 or s.device != dev or not s.is_contiguous()):
+        raise ValueError("s must be a contiguous fp32 vector of length K on G's device")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}")
+    res, y, yc, ldy, sp = _a8_out(out, dtype, M, K, dev)
+    with _on(dev):
+        st = lib().awq_act_mul(G.data_ptr(), xc, M, K, ldg, up, ldu, s.data_ptr() if s is not None else None,
+                               _ACTS[act], y.data_ptr(), yc, ldy, sp, _raw_stream(dev))
+    _check(st, "awq_act_mul")
+    return res
+
+
+class W4A8Weight(NamedTuple):
+    """A packed weight laid out for ``w4a8`` (``w4a8_weight``): ``data`` uint8, N x K."""
+    data: torch.Tensor
+    N: int
+    K: int
+
+
+def w4a8_weight_bytes(N: int, K: int) -> int:
+    return int(lib().awq_w4a8_weight_bytes(N, K))
+
+
+def w4a8_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = GROUP, *,
+                out: Optional[torch.Tensor] = None) -> W4A8Weight:
+    """The artefact of ``pack`` laid out for ``w4a8``, once per weight.  ``out``: uint8 of at least
+    ``w4a8_weight_bytes`` on the same device, 256-byte aligned."""
+    dev = qweight.device
+    if qweight.dim() != 2 or qweight.dtype != torch.int32 or not qweight.is_contiguous() or not qweight.is_cuda:
+        raise ValueError("qweight must be a contiguous int32 [N, K/8] device tensor")
+    N, K = qweight.shape[0], qweight.shape[1] * 8
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t.shape != (N, K // max(group_size, 1)) or t.dtype != torch.float16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp16 [N, K/group] tensor")
+        _same_device(t, dev, name)
+    wt, wt_bytes = _workspace(out, w4a8_weight_bytes(N, K), dev)
+    with _on(dev):
+        st = lib().awq_w4a8_weight(qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K, group_size,
+                                   wt.data_ptr(), wt_bytes, _raw_stream(dev))
+    _check(st, "awq_w4a8_weight")
+    return W4A8Weight(wt, N, K)
+
+
+def w4a8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().awq_w4a8_workspace_bytes(M, K, N))
+
+
+def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W_hat^T for 8-bit activations (``Act8``: from ``rmsnorm``, ``act_mul``, or the caller's own)
+    and a weight laid out by ``w4a8_weight``.  Y [M, N] is float32 (the default) or bfloat16.
+    ``workspace``: ``w4a8_workspace_bytes`` for (M, K, N), allocated here when not given; calls that may
+    run at the same time (two streams, two graphs) need one each."""
+    q, scale = X
+    data, N, K = weight
+    dev = q.device
+    ldx = _rows(q, "X.q", dev)
+    M = q.shape[0]
+    if q.shape[1] != K:
+        raise ValueError("X and the weight disagree on K")
+    xc = _code(q.dtype, _CODES, "X.q")
+    if scale.shape != (M,) or scale.dtype != torch.float32 or scale.device != dev or not scale.is_contiguous():
+        raise ValueError("X.scale must be a contiguous fp32 vector of length M on X's device")
+    if data.device != dev or data.dtype != torch.uint8 or data.numel() < w4a8_weight_bytes(N, K):
+        raise ValueError("weight must be the result of w4a8_weight on X's device")
+    if out is None:
+        Y = torch.empty((M, N), dtype=dtype if dtype is not None else torch.float32, device=dev)
+        ldy = N
+    else:
+        Y, ldy = out, _rows(out, "out", dev, (M, N))
+        if dtype is not None and dtype != out.dtype:
+            raise ValueError("dtype and out disagree")
+    yc = _code(Y.dtype, _FLOATS, "Y")
+    need = w4a8_workspace_bytes(M, K, N)
+    ws, ws_bytes = _workspace(workspace, need, dev) if need else (None, 0)
+    with _on(dev):
+        st = lib().awq_w4a8(q.data_ptr(), xc, scale.data_ptr(), M, K, ldx, data.data_ptr(), N, GROUP, Y.data_ptr(), yc,
+                            ldy, ws.data_ptr() if need else None, ws_bytes, _raw_stream(dev))
+    _check(st, "awq_w4a8")
     return Y

@@ -1,0 +1,442 @@
+"""GPU tests of the 8-bit activation path against its fp64 definitions.
+
+Tolerances, in units u = 2^-24 (half a step of fp32) of the value:
+- norm: a thread's chain of at most 96 squares and the sums over lanes and waves (22) put at most 118 u
+  on the sum of squares, half of it on 1 / rms, and h, gamma's product, square root, divisions and the
+  last product one or two u each: 72 u.
+- SiLU: the exponential's argument costs |x| u in exp(-x), with an fp32 result nothing; the exponential,
+  reciprocal and products 10 u.  GELU: erfc (16 u) at an argument rounded twice, which erfc amplifies by
+  at most x^2 + 2: 16 u + 2 (x^2 + 2) u.  U, s: 4 u.
+- a stored value adds half a step of its type (bf16 2^-8); a code has to be the rounding of a value within
+  the tolerance of y / scale.
+- product: int8 group sums are exact; each of the G steps of the sum over groups rounds twice, and
+  the sum over waves eight times: (2 G + 16) u of sum_g D (|sum x q| + z |sum x|).  e4m3: the 128 terms of a group are
+  summed in fp32: 136 u of the sum of the absolute terms.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import a8_oracle as a8
+from oracle import awq_oracle as o
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+KIND = {torch.int8: "int8", torch.float8_e4m3fn: "e4m3"}
+F32, BF16, I8, E4M3 = torch.float32, torch.bfloat16, torch.int8, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def awq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from post_weight_quantization_mean_amd import awq as _awq
+    _awq.lib()
+    return _awq
+
+
+def banner(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+
+
+def rand(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def check_stored(y, want, tol):
+    """A 16- or 32-bit output: half a step of its type on top of tol (relative)."""
+    err = np.abs(f64(y) - want)
+    lim = (HALF[y.dtype] + tol) * np.abs(want) + 1e-36
+    assert np.all(err <= lim), (np.argwhere(err > lim)[:4].tolist(), float(np.max(err / lim)))
+
+
+def check_codes(res, want, tol):
+    """An Act8: the scale within tol, each code the rounding of a value within tol of y / scale."""
+    kind = KIND[res.q.dtype]
+    sc = a8.row_scale(want, kind)
+    tol = np.broadcast_to(np.asarray(tol), want.shape)
+    worst = np.max(tol, axis=1)
+    assert res.scale.dtype == F32 and res.scale.shape == (want.shape[0],)
+    assert np.all(np.abs(f64(res.scale) - sc) <= (worst + 4 * U) * sc)
+    v = want / sc[:, None]
+    t = np.abs(v) * (tol + worst[:, None] + 6 * U)
+    q = f64(res.q)
+    lo, hi = a8.round_code(v - t, kind), a8.round_code(v + t, kind)
+    bad = np.argwhere((q < lo) | (q > hi))
+    assert bad.size == 0, (bad[:4].tolist(), [(q[tuple(b)], v[tuple(b)]) for b in bad[:4]])
+
+
+def check(res, want, tol):
+    (check_codes if isinstance(res, tuple) else check_stored)(res, want, tol)
+
+
+# ---- norm ------------------------------------------------------------------------------------
+
+# K: one unit, odd, ragged units of each row layout (one wave, four, sixteen), past the registers
+NORM_SHAPES = [(1, 1), (1, 8), (3, 7), (5, 128), (2, 1000), (300, 1000), (300, 1024), (1, 4096), (301, 4096),
+               (300, 4104), (257, 8192), (2, 11008), (260, 14336), (1, 20000), (258, 20480), (2, 65544), (3, 4097)]
+
+
+@pytest.mark.parametrize("M,K", NORM_SHAPES)
+@pytest.mark.parametrize("xt,rt,out", [(BF16, BF16, E4M3), (BF16, BF16, I8), (F32, F32, BF16), (F32, BF16, F32),
+                                       (BF16, None, I8), (BF16, F32, E4M3), (F32, None, BF16)])
+def test_rmsnorm(awq, M, K, xt, rt, out):
+    banner(f"rmsnorm M={M} K={K} {xt} {rt} {out}")
+    x = rand((M, K), xt, 1, 2.0)
+    r = None if rt is None else rand((M, K), rt, 2, 3.0)
+    g = rand((K,), F32 if K % 2 else BF16, 3) + 1
+    h, y = a8.rmsnorm(f64(x), None if r is None else f64(r), f64(g), 1e-5)
+    res = awq.rmsnorm(x.to(DEV), g.to(DEV), None if r is None else r.to(DEV), eps=1e-5, dtype=out)
+    if rt is not None:
+        res, hh = res
+        assert hh.dtype == rt
+        check_stored(hh, h, 2 * U)
+    # h = x + r rounds relative to h: where x and r cancel, y's error follows h's own, still relative
+    check(res, y, 72 * U)
+
+
+def test_rmsnorm_residual_in_place_and_strided(awq):
+    """Row strides of every operand, the residual updated in place, nothing behind the rows touched."""
+    M, K = 37, 1024
+    X, R = rand((M, K + 24), BF16, 4).to(DEV), rand((M + 2, K + 8), BF16, 5).to(DEV)
+    keep = R.clone()
+    g = (rand((K,), F32, 6) + 1).to(DEV)
+    q, sc = torch.full((M + 2, K + 16), 7, dtype=torch.int8, device=DEV), torch.full((M,), -1.0, device=DEV)
+    h, y = a8.rmsnorm(f64(X[:, :K]), f64(keep[:M, :K]), f64(g), 1e-6)
+    res, hh = awq.rmsnorm(X[:, :K], g, R[:M, :K], out=awq.Act8(q[:M, :K], sc), residual_out=R[:M, :K])
+    check(res, y, 72 * U)
+    check_stored(R[:M, :K], h, 2 * U)
+    assert torch.equal(R[M:], keep[M:]) and torch.equal(R[:, K:], keep[:, K:])
+    assert torch.all(q[M:] == 7) and torch.all(q[:, K:] == 7)
+
+
+@pytest.mark.parametrize("xo,yo", [(1, 0), (0, 3), (3, 1)])
+def test_rmsnorm_unaligned_rows(awq, xo, yo):
+    """Views that start off a 16-byte boundary take single elements, with the same result."""
+    M, K = 5, 512
+    X = rand((M, K + 8), BF16, 7).to(DEV)[:, xo:xo + K]
+    g = (rand((K,), F32, 8) + 1).to(DEV)
+    q, sc = torch.zeros((M, K + 8), dtype=torch.int8, device=DEV), torch.zeros(M, device=DEV)
+    res = awq.rmsnorm(X, g, out=awq.Act8(q[:, yo:yo + K], sc))
+    check(res, a8.rmsnorm(f64(X), None, f64(g), 1e-6)[1], 72 * U)
+
+
+@pytest.mark.parametrize("K", [512, 513])
+@pytest.mark.parametrize("dtype", [I8, E4M3, BF16])
+def test_rows_of_zeros_and_not_finite(awq, K, dtype):
+    """A zero row has codes 0 and the least scale; NaN or Inf in x, r or gamma's products gives that
+    row's scale NaN (its y NaN) and no other's."""
+    M = 6
+    x, r = rand((M, K), BF16, 9), rand((M, K), BF16, 10)
+    x[1], r[1] = 0, 0
+    x[2, 5], r[3, K - 1], x[4, 0] = float("nan"), float("inf"), -float("inf")
+    g = torch.ones(K)
+    res, _ = awq.rmsnorm(x.to(DEV), g.to(DEV), r.to(DEV), dtype=dtype)
+    sick = torch.tensor([False, False, True, True, True, False])
+    if dtype == BF16:
+        assert torch.equal(res.cpu().isnan().all(1), sick) and torch.all(res[1] == 0)
+        return
+    assert torch.equal(res.scale.cpu().isnan(), sick)
+    assert torch.all(res.q[1].float() == 0) and 0 < res.scale[1].item() < 1e-29
+    ok = ~sick
+    _, y = a8.rmsnorm(f64(x[ok]), f64(r[ok]), f64(g), 1e-6)
+    check(awq.Act8(res.q.cpu()[ok], res.scale.cpu()[ok]), y, 72 * U)
+    g[7] = float("nan")
+    assert torch.all(awq.rmsnorm(x.to(DEV), g.to(DEV), dtype=dtype).scale.isnan())
+
+
+def test_rmsnorm_is_the_same_in_every_call(awq):
+    x, g = rand((300, 4096), BF16, 11).to(DEV), torch.ones(4096, device=DEV)
+    a, b = awq.rmsnorm(x, g, dtype=I8), awq.rmsnorm(x, g, dtype=I8)
+    assert torch.equal(a.q, b.q) and torch.equal(a.scale, b.scale)
+
+
+# ---- activation ---------------------------------------------------------------------------------
+
+
+def act_tol(g, act, out, u, s):
+    x = np.abs(f64(g))
+    t = {"none": 0.0 * x, "silu": 10.0 + (0.0 if out == F32 else 1.0) * np.minimum(x, 90.0),
+         "gelu": 16.0 + 2.0 * (np.minimum(x, 14.0) ** 2 + 2)}[act]
+    return (t + 8.0) * U
+
+
+@pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (2, 1000), (300, 1024), (8, 14336), (260, 11008), (258, 4104),
+                                 (1, 20480), (3, 2049), (2, 65544)])
+@pytest.mark.parametrize("xt,act,gate,scaled,out", [
+    (BF16, "silu", True, False, E4M3), (BF16, "silu", True, False, I8), (F32, "silu", True, True, F32),
+    (F32, "gelu", False, True, BF16), (BF16, "gelu", True, False, I8), (BF16, "none", False, False, I8),
+    (F32, "none", False, False, E4M3), (BF16, "none", True, True, BF16), (F32, "gelu", True, False, F32)])
+def test_act_mul(awq, M, K, xt, act, gate, scaled, out):
+    banner(f"act_mul M={M} K={K} {xt} {act} {gate} {scaled} {out}")
+    both = rand((M, 2 * K), xt, 12, 3.0)
+    g, u = both[:, :K], both[:, K:] if gate else None
+    s = torch.exp(0.3 * rand((K,), F32, 13)) if scaled else None
+    d = both.to(DEV)
+    res = awq.act_mul(d[:, :K], d[:, K:] if gate else None, None if s is None else s.to(DEV), act, dtype=out)
+    want = a8.act_mul(f64(g), None if u is None else f64(u), None if s is None else f64(s), act)
+    check(res, want, act_tol(g, act, out, u, s))
+
+
+def test_act_mul_far_tails(awq):
+    """Large magnitudes: SiLU and GELU go to 0 and to x, with no NaN where exp overflows."""
+    x = torch.tensor([[-3e38, -1e4, -200.0, -104.0, -90.0, -20.0, -0.0, 0.0, 20.0, 90.0, 1e4, 3e38]])
+    for act in ("silu", "gelu"):
+        y = awq.act_mul(x.to(DEV), None, None, act, dtype=F32)
+        check_stored(y, a8.act_mul(f64(x), None, None, act), act_tol(x, act, F32, None, None))
+
+
+def test_act_mul_in_place(awq):
+    both = rand((9, 512), BF16, 14).to(DEV)
+    g, u = both[:, :256], both[:, 256:]
+    want = a8.act_mul(f64(g), f64(u), None, "silu")
+    awq.act_mul(g, u, out=g)
+    check_stored(g, want, 100 * U)
+
+
+@pytest.mark.parametrize("K", [256, 255])
+def test_act_mul_not_finite(awq, K):
+    x = rand((3, K), F32, 15)
+    x[1, 3] = float("nan")
+    x[2, 4] = float("inf")
+    res = awq.act_mul(x.to(DEV), None, None, "none", dtype=E4M3)
+    assert res.scale.isnan().tolist() == [False, True, True]
+
+
+# ---- product --------------------------------------------------------------------------------------
+
+
+def artefact(N, K, seed):
+    rng = np.random.default_rng(seed)
+    W = (rng.standard_normal((N, K)) / np.sqrt(K)).astype(np.float32)
+    W[:, : K // 2] += 0.5 / np.sqrt(K)  # groups whose range is not centred: other zero points
+    return o.pack(W, np.ones(K, np.float32))
+
+
+def on_gpu(awq, art):
+    q = torch.from_numpy(art["qweight"]).to(DEV)
+    sc = torch.from_numpy(art["scales"].view(np.float16)).to(DEV)
+    z = torch.from_numpy(art["zeros"].view(np.float16)).to(DEV)
+    return awq.w4a8_weight(q, sc, z)
+
+
+def codes(M, K, dtype, seed):
+    rng = np.random.default_rng(seed)
+    v = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32) + 0.3)
+    v = v * 127 / 4.5 if dtype == I8 else v * 448 / 4.5
+    q = (v.round().clamp(-127, 127) if dtype == I8 else v.clamp(-448, 448)).to(dtype)
+    return q, torch.from_numpy(rng.uniform(0.001, 0.01, M).astype(np.float32))
+
+
+def check_product(Y, q, sc, art, label=""):
+    want, mag, absmag = a8.w4a8(f64(q), f64(sc), art)
+    G = q.shape[1] // 128
+    lim = (2 * G + 16) * U * mag + (HALF[Y.dtype] + 4 * U) * np.abs(want) + 1e-36
+    if q.dtype == E4M3:
+        lim = lim + 136 * U * absmag
+    err = np.abs(f64(Y) - want)
+    assert np.all(err <= lim), (label, np.argwhere(~(err <= lim))[:4].tolist(), float(np.nanmax(err / lim)))
+
+
+# tokens: one tile of 16 whole and ragged, several; channels: below a tile, ragged, many; groups 1 .. 86
+W4A8_SHAPES = [(1, 128, 1), (1, 4096, 100), (2, 256, 17), (7, 384, 16), (16, 1024, 33), (17, 5120, 48), (31, 128, 130),
+               (33, 2048, 64), (64, 1152, 257), (65, 4096, 300), (100, 640, 500), (129, 1024, 256), (256, 2048, 200),
+               (257, 896, 513), (300, 4096, 272), (520, 1280, 640), (5, 11008, 40), (270, 11008, 64)]
+
+
+@pytest.mark.parametrize("M,K,N", W4A8_SHAPES)
+@pytest.mark.parametrize("xt,yt", [(I8, F32), (E4M3, F32), (E4M3, BF16)])
+def test_w4a8(awq, M, K, N, xt, yt):
+    banner(f"w4a8 M={M} K={K} N={N} {xt} {yt}")
+    art = artefact(N, K, 20)
+    q, sc = codes(M, K, xt, 21)
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), dtype=yt)
+    check_product(Y, q, sc, art)
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+@pytest.mark.parametrize("xt", [I8, E4M3])
+def test_w4a8_strided(awq, M, xt):
+    """Row strides of the codes and of Y; nothing outside Y's view is written."""
+    K, N = 512, 200
+    art = artefact(N, K, 22)
+    q, sc = codes(M, K, xt, 23)
+    full = torch.zeros((M, K + 48), dtype=xt, device=DEV)
+    full[:, :K] = q.to(DEV)
+    Y = torch.full((M + 3, N + 40), -7.0, device=DEV)
+    awq.w4a8(awq.Act8(full[:, :K], sc.to(DEV)), on_gpu(awq, art), out=Y[:M, :N])
+    check_product(Y[:M, :N], q, sc, art)
+    assert torch.all(Y[:, N:] == -7.0) and torch.all(Y[M:] == -7.0)
+
+
+@pytest.mark.parametrize("M", [4, 80, 260])
+@pytest.mark.parametrize("xt", [I8, E4M3])
+def test_w4a8_extremes(awq, M, xt):
+    """Extreme codes (+-Q with extreme weights), steps over the whole fp16 range, zero points 0 and 15."""
+    K, N = 1024, 48
+    rng = np.random.default_rng(24)
+    G = K // 128
+    scales = np.exp2(rng.uniform(-24, 15.9, (N, G))).astype(np.float16)
+    scales[0] = 2.0 ** -24
+    scales[1] = 65504
+    scales[2] = 0
+    art = dict(qweight=rng.integers(0, 2 ** 32, (N, K // 8), dtype=np.uint64).astype(np.uint32).view(np.int32),
+               scales=scales, zeros=rng.choice([0.0, 15.0], (N, G)).astype(np.float16))
+    art["qweight"][3] = -1
+    q, sc = codes(M, K, xt, 25)
+    top = 127.0 if xt == I8 else 448.0
+    q[0], q[1] = torch.full((K,), top).to(xt), torch.full((K,), -top).to(xt)
+    w = awq.w4a8_weight(torch.from_numpy(art["qweight"]).to(DEV), torch.from_numpy(art["scales"]).to(DEV),
+                        torch.from_numpy(art["zeros"]).to(DEV))
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), w)
+    # steps below 2^-25 of their channel's largest lose bits: half a step of 2^-24 at 2^11 scale
+    want, mag, absmag = a8.w4a8(f64(q), f64(sc), art)
+    ones = dict(art, scales=np.ones_like(scales) * np.float16(1))
+    loss = a8.w4a8(f64(q), f64(sc), ones)[2] * (np.max(scales.astype(np.float64), axis=1) * 2.0 ** -35)[None, :]
+    lim = (2 * G + 16) * U * mag + 5 * U * np.abs(want) + loss + (136 * U * absmag if xt == E4M3 else 0) + 1e-36
+    assert np.all(np.abs(f64(Y) - want) <= lim)
+
+
+@pytest.mark.parametrize("M", [5, 90, 300])
+def test_w4a8_scale_nan_stays_in_its_row(awq, M):
+    art = artefact(64, 256, 26)
+    q, sc = codes(M, 256, I8, 27)
+    sc[M - 2] = float("nan")
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art))
+    assert torch.all(Y[M - 2].isnan())
+    keep = torch.arange(M) != M - 2
+    check_product(Y.cpu()[keep], q[keep], sc[keep], art)
+
+
+def test_w4a8_agrees_with_w4a16(awq):
+    """The same artefact and activations through both products: 8-bit activations put at most half a step
+    per channel on top of the 16-bit product's own error."""
+    M, K, N = 40, 1024, 96
+    art = artefact(N, K, 28)
+    X = rand((M, K), BF16, 29)
+    t = [torch.from_numpy(art["qweight"]).to(DEV)] + [torch.from_numpy(art[k].view(np.float16)).to(DEV)
+                                                      for k in ("scales", "zeros")]
+    Y16 = f64(awq.w4a16(X.to(DEV), *t))
+    a = awq.act_mul(X.to(DEV), None, None, "none", dtype=I8)
+    Y8 = f64(awq.w4a8(a, awq.w4a8_weight(*t)))
+    W = np.abs(o.dequant_artefact(art["qweight"], art["scales"], art["zeros"]).astype(np.float64))
+    lim = 0.5001 * f64(a.scale)[:, None] * W.sum(1)[None, :] + (2.0 ** -8 + K * U) * (np.abs(f64(X)) @ W.T)
+    assert np.all(np.abs(Y8 - Y16) <= lim)
+
+
+@pytest.mark.parametrize("M", [1, 24, 300])
+@pytest.mark.parametrize("xt", [I8, E4M3])
+def test_mlp_block(awq, M, xt):
+    """The operators as a decoder's MLP runs them, every step against the definition applied to the step's
+    own inputs: norm + residual -> gate/up -> SiLU gate -> down -> next norm."""
+    K, I = 512, 896
+    gu, down = artefact(2 * I, K, 30), artefact(K, I, 31)
+    x, r, g = rand((M, K), BF16, 32), rand((M, K), BF16, 33), rand((K,), F32, 34) * 0.1 + 1
+    a, h = awq.rmsnorm(x.to(DEV), g.to(DEV), r.to(DEV), dtype=xt)
+    hr, y = a8.rmsnorm(f64(x), f64(r), f64(g), 1e-6)
+    check_stored(h, hr, 2 * U)
+    check(a, y, 72 * U)
+    z = awq.w4a8(a, on_gpu(awq, gu), dtype=BF16)
+    check_product(z, a.q.cpu(), a.scale.cpu(), gu)
+    b = awq.act_mul(z[:, :I], z[:, I:], dtype=xt)
+    check(b, a8.act_mul(f64(z[:, :I]), f64(z[:, I:]), None, "silu"), act_tol(z[:, :I], "silu", xt, None, None))
+    d = awq.w4a8(b, on_gpu(awq, down), dtype=BF16)
+    check_product(d, b.q.cpu(), b.scale.cpu(), down)
+    y2, h2 = awq.rmsnorm(d, g.to(DEV), h, dtype=BF16, residual_out=h.clone())
+    hr2, yr2 = a8.rmsnorm(f64(d), f64(h), f64(g), 1e-6)
+    check_stored(h2, hr2, 2 * U)
+    check_stored(y2, yr2, 72 * U)
+
+
+@pytest.mark.parametrize("M", [2, 40, 300])
+def test_captured_and_replayed(awq, M):
+    """The chain in a graph, replayed on new inputs between eager calls, equals the eager results."""
+    K, I = 512, 384
+    gu = on_gpu(awq, artefact(2 * I, K, 35))
+    xs = [rand((M, K), BF16, 36 + i).to(DEV) for i in range(3)]
+    g = torch.ones(K, device=DEV)
+
+    def chain(x):
+        z = awq.w4a8(awq.rmsnorm(x, g, dtype=E4M3), gu, dtype=BF16)
+        return awq.act_mul(z[:, :I], z[:, I:], dtype=I8)
+
+    buf = xs[0].clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain(buf)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(buf)
+    for x in xs + xs[:1]:
+        want = chain(x)
+        buf.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.q, want.q) and torch.equal(got.scale, want.scale)
+
+
+def test_two_streams_at_once(awq):
+    """Calls on two streams, each with its own outputs and workspace, do not disturb each other."""
+    art = artefact(256, 1024, 40)
+    w = on_gpu(awq, art)
+    data = [codes(m, 1024, I8, 41 + m) for m in (300, 20)]
+    dev = [awq.Act8(q.to(DEV), sc.to(DEV)) for q, sc in data]
+    want = [awq.w4a8(d, w) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(awq.w4a8(dev[i], w))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in outs[i]:
+            assert torch.equal(y, want[i])
+
+
+def test_refusals(awq):
+    x, g = rand((4, 256), BF16, 50).to(DEV), torch.ones(256, device=DEV)
+    with pytest.raises(ValueError):
+        awq.rmsnorm(x, g[:128])
+    with pytest.raises(TypeError):
+        awq.rmsnorm(x.half(), g)
+    with pytest.raises(ValueError):
+        awq.rmsnorm(x, g, x[:2])
+    with pytest.raises(ValueError):
+        awq.rmsnorm(x, g, residual_out=x)
+    with pytest.raises(awq.AwqError):
+        awq.rmsnorm(x, g, eps=0.0)
+    with pytest.raises(ValueError):
+        awq.rmsnorm(x.t(), torch.ones(4, device=DEV))
+    with pytest.raises(ValueError):
+        awq.rmsnorm(x, g, out=torch.empty(4, 128, device=DEV))
+    with pytest.raises(ValueError):
+        awq.act_mul(x, act="relu")
+    with pytest.raises(TypeError):
+        awq.act_mul(x, x.float())
+    with pytest.raises(TypeError):
+        awq.act_mul(x, dtype=torch.float16)
+    with pytest.raises(awq.AwqError):
+        awq.rmsnorm(x[:0], g)
+    w = on_gpu(awq, artefact(16, 256, 51))
+    a = awq.act_mul(x, act="none", dtype=I8)
+    with pytest.raises(ValueError):
+        awq.w4a8(awq.Act8(a.q[:, :128], a.scale), w)
+    with pytest.raises(ValueError):
+        awq.w4a8(awq.Act8(a.q, a.scale[:2]), w)
+    with pytest.raises(TypeError):
+        awq.w4a8(awq.Act8(x, a.scale), w)
+    with pytest.raises(TypeError):
+        awq.w4a8(a, w, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        awq.w4a8(a, awq.W4A8Weight(w.data[:64], 16, 256))
