@@ -95,7 +95,7 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each
- * K is a multiple of 128.
+ * K is a multiple of 128; 256 rows of Xq and of Y span less than 2^31 bytes each (AWQ_ERR_SHAPE).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_w4a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M, int64_t K, int64_t ldx,

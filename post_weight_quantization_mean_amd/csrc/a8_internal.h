@@ -31,7 +31,7 @@ hipError_t launch_act_mul(const RowArgs& a, int x_type, bool vec, hipStream_t st
 struct W4a8Layout {
   size_t steps, powers, total;  // byte offsets of the parts behind the codes
 };
-inline int64_t w4a8_tiles(int64_t N) { return (N + 15) / 16; }
+__host__ __device__ inline int64_t w4a8_tiles(int64_t N) { return (N + 15) / 16; }
 struct W4a8Args {
   const void* x;
   const float* xscale;
