@@ -127,8 +127,8 @@ __device__ __forceinline__ Operand<KIND> operand(const i32x8 b) {
   return r;
 }
 
-// One group's products of 16 tokens and 16 channels: lane l gets channel l % 16 of tokens 4 (l / 16) + i
-// (fp32; int8: exact integers; e4m3: times 2^-9 with codes as b).
+// One group's products of 16 tokens and 16 channels: lane l gets channel l % 16 of tokens 4 (l / 16) + i,
+// as settled<KIND>(r[i]) (int8: exact integers; e4m3: times 2^-9 with codes as b).
 template <int KIND>
 __device__ __forceinline__ f32x4 group_product(const Operand<KIND>& a, const Operand<KIND>& b) {
   const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -140,14 +140,19 @@ __device__ __forceinline__ f32x4 group_product(const Operand<KIND>& a, const Ope
     for (int s = 1; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[s], b.h[s], r, 0, 0, 0);
     return r;
   } else {
-    const i32x4 zi = {0, 0, 0, 0};
+    // the sums start at the bits of 1.5 2^23: |sum| < 2^22 more is that float plus the sum, so that a
+    // full-rate subtraction stands for the conversion
+    constexpr int kBits = 0x4b400000;
+    const i32x4 zi = {kBits, kBits, kBits, kBits};
     const i32x4 alo = __builtin_shufflevector(a.b, a.b, 0, 1, 2, 3), ahi = __builtin_shufflevector(a.b, a.b, 4, 5, 6, 7);
     const i32x4 blo = __builtin_shufflevector(b.b, b.b, 0, 1, 2, 3), bhi = __builtin_shufflevector(b.b, b.b, 4, 5, 6, 7);
     i32x4 r = __builtin_amdgcn_mfma_i32_16x16x64_i8(alo, blo, zi, 0, 0, 0);
     r = __builtin_amdgcn_mfma_i32_16x16x64_i8(ahi, bhi, r, 0, 0, 0);
-    return (f32x4){(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
+    return __builtin_bit_cast(f32x4, r);
   }
 }
+template <int KIND>
+__device__ __forceinline__ float settled(float r) { return KIND == kInt8 ? r - 12582912.0f : r; }
 
 __device__ __forceinline__ i32x8 join(const u32x4 lo, const u32x4 hi) {
   return (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(64 * kStWaves) void w4a8_stream_kernel(const W4a8Ar
         const float d = h2f(dz[q] & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
         const float z = h2f(dz[q] >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d, fmaf(-z, sx[i], s[i]), tot[t][q][i]);
+        for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d, fmaf(-z, settled<KIND>(sx[i]), settled<KIND>(s[i])), tot[t][q][i]);
       }
     }
   }
@@ -287,36 +292,40 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 }
 
 // A block of eight waves, two per SIMD, computes 32 TM tokens x 256 channels; wave (wm, wn) of 2 x 4 has
-// 16 TM tokens x 64 channels.  One stage is one group: the tokens' bytes (128 per row), the codes of sixteen
-// channel tiles (1 KiB each, as laid out) and their steps.  Three stages in LDS: while group g is multiplied,
-// g + 1 has been requested and g + 2 is requested, by LDS DMA (no registers), behind one barrier per group.
+// 16 TM tokens x 64 channels and takes one group a step.  The tokens' bytes (128 per row and group) and the
+// groups' steps come into LDS by DMA in four stages; the codes, which only two waves share, come
+// straight into registers in operand order, a group ahead.  The barrier of step g says that stages g
+// and g + 1 have landed, so that the last products of a step run beside the reads for the first ones of
+// the next; stage g + 2 is under way and g + 3 is requested.
 // Rows of 128 bytes hold their 16-byte pieces at piece ^ (row % 8) ^ (row / 8 % 2): the reads of sixteen
 // rows' same piece then use every bank once.
 //
-// Per group and 16 x 16 outputs the matrix unit works 32 cycles on the product and the vector unit 16
-// on the four steps' multiply-adds (int8: 32, with the conversions); unpacking adds 12 instructions per
-// channel tile and wave, spread over TM products.  The zero points would cost as many multiply-adds
+// Per group and 16 x 16 outputs the matrix unit works 32 cycles on the product and the vector unit 8
+// on the steps' multiply-adds (int8: 16); unpacking adds 12 instructions per channel tile and wave,
+// spread over TM products.  The zero points would cost as many multiply-adds
 // again; their sum over groups is a product of its own, sum_g sums[m, g] (D z)[n, g], and runs on the matrix
 // cores in fp16 with both operands as high and low parts (sums 22 bits, D z 15: exact), one
 // instruction of 16 cycles for eight groups.
 constexpr int kTileN = 256;
 template <int TM>
-constexpr int kTileStage = 32 * TM * 128 + 16 * 1024 + 1024;
+constexpr int kTileStage = 16 * TM * 128 + 1024;
 
 __device__ __forceinline__ int row_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 #define AWQ_LDS_A8 __attribute__((address_space(3)))
+#define AWQ_INLINE __attribute__((always_inline))
 
 template <int KIND, int TM>
-__global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, const uint32_t* __restrict__ sums,
+__global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, const uint32_t* __restrict__ sums,
                                                            int64_t Gp, int mtiles, int ntiles) {
   constexpr bool E4M3 = KIND != kInt8;
-  constexpr int STAGE = kTileStage<TM>, BOFF = 32 * TM * 128, SOFF = BOFF + 16 * 1024;
-  constexpr int NDMA = TM / 2 + 2 + 1;  // copies per wave and stage
+  constexpr int STAGE = kTileStage<TM>, SOFF = 16 * TM * 128;
+  constexpr int NDMA = TM / 2 + 1;  // copies per wave and stage
   __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st3[STAGE];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = (int)(p.K / kGroup);
   // Blocks go to the eight XCDs in turn; each XCD takes a contiguous run of tiles, which walk bands
   // of four token tiles, so that the 32 tiles in work there are about four by eight and share their
@@ -324,15 +333,15 @@ __global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, con
   const int total = mtiles * ntiles, per = (total + 7) / 8;
   const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
-  const int band = __builtin_amdgcn_readfirstlane(id / (4 * ntiles)), in = id - band * 4 * ntiles;
-  const int bh = mtiles - 4 * band < 4 ? mtiles - 4 * band : 4;
+  const int band = __builtin_amdgcn_readfirstlane(id / (8 * ntiles)), in = id - band * 8 * ntiles;
+  const int bh = mtiles - 8 * band < 8 ? mtiles - 8 * band : 8;
   const int col = __builtin_amdgcn_readfirstlane(in / bh), tile0 = 16 * col;  // first channel tile
-  const int64_t m0 = (int64_t)(4 * band + in - col * bh) * (32 * TM);
+  const int64_t m0 = (int64_t)(8 * band + in - col * bh) * (16 * TM);
   const int tiles = (int)w4a8_tiles(p.N);
   const int nt = tiles - tile0 < 16 ? tiles - tile0 : 16;
-  const int rows = p.M - m0 < 32 * TM ? (int)(p.M - m0) : 32 * TM;
+  const int rows = p.M - m0 < 16 * TM ? (int)(p.M - m0) : 16 * TM;
 
-  // copies: rows and tiles past the end read as zero (the resources end there)
+  // rows and tiles past the end read as zero (the resources end there)
   const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(static_cast<const uint8_t*>(p.x) + m0 * p.ldx), (short)0, (int)((rows - 1) * p.ldx + p.K),
       0x00020000);
@@ -340,26 +349,31 @@ __global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, con
       const_cast<uint32_t*>(p.codes + (int64_t)tile0 * G * 256), (short)0, nt * G * 1024, 0x00020000);
   const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint32_t*>(p.steps + (int64_t)tile0 * G * 16), (short)0, nt * G * 64, 0x00020000);
-  uint32_t xoff[TM / 2], woff[2];
+  uint32_t xoff[TM / 2];
 #pragma unroll
   for (int i = 0; i < TM / 2; ++i) {
-    const int row = 4 * TM * wave + 8 * i + (lane >> 3);
+    const int row = 4 * TM * wn + 8 * i + (lane >> 3);
     xoff[i] = (uint32_t)(row * p.ldx + 16 * ((lane & 7) ^ row_swizzle(row)));
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)((2 * wave + i) * G * 1024 + lane * 16);
   const uint32_t soff = (uint32_t)((4 * wn + j) * G * 64 + c * 4);  // the steps of this wave's own four tiles
-  auto dma = [&](uint8_t* st, int g) __attribute__((always_inline)) {
+  auto dma = [&](uint8_t* st, int g) AWQ_INLINE {
 #pragma unroll
     for (int i = 0; i < TM / 2; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (AWQ_LDS_A8 void*)(st + (4 * TM * wave + 8 * i) * 128), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (AWQ_LDS_A8 void*)(st + (4 * TM * wn + 8 * i) * 128), 16,
                                                (int)xoff[i], g * 128, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (AWQ_LDS_A8 void*)(st + BOFF + (2 * wave + i) * 1024), 16,
-                                               (int)woff[i], g * 1024, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (AWQ_LDS_A8 void*)(st + SOFF + wn * 256), 4, (int)soff, g * 64, 0, 0);
   };
+  u32x4 cw0[4], cw1[4];  // the codes of the next two steps, by parity
+  auto load_codes = [&](u32x4* cw, int g) AWQ_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      cw[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, ((4 * wn + q) * G + g) * 1024, 0));
+  };
+  load_codes(cw0, 0);
+  load_codes(cw1, 1);
+  dma(st0, 0);
+  dma(st1, 1);
+  dma(st2, 2);
   f32x4 tot[TM][4];
 #pragma unroll
   for (int t = 0; t < TM; ++t)
@@ -370,7 +384,7 @@ __global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, con
     const uint32_t* srow[TM];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      const int r = 16 * (TM * wm + t) + c;
+      const int r = 16 * t + c;
       srow[t] = sums + (m0 + (r < rows ? r : rows - 1)) * Gp + 2 * j;
     }
     for (int b = 0; b < (int)Gp / 8; ++b) {
@@ -400,56 +414,93 @@ __global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, con
     }
   }
   // this lane's pieces of row c of a token tile (tiles are 16 rows: the same swizzle in each)
-  const int a0 = (16 * TM * wm + c) * 128 + 16 * ((2 * j) ^ row_swizzle(c));
-  const int a1 = (16 * TM * wm + c) * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
-  auto compute = [&](const uint8_t* st) __attribute__((always_inline)) {
+  const int a0 = c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
+  const int a1 = c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
+  i32x8 an;         // the next token tile's bytes
+  uint32_t dn[4];   // the next step's steps and zero points
+  auto read_a = [&](const uint8_t* st, int t) AWQ_INLINE {
+    an = join(*reinterpret_cast<const u32x4*>(st + a0 + t * 2048), *reinterpret_cast<const u32x4*>(st + a1 + t * 2048));
+  };
+  auto read_d = [&](const uint8_t* st) AWQ_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dn[q] = *reinterpret_cast<const uint32_t*>(st + SOFF + (4 * wn + q) * 64 + c * 4);
+  };
+  // own copies but the newest NDMA landed, own reads of the stage before done; after the barrier that
+  // holds for every wave
+  auto sync = [&] () AWQ_INLINE {
+    __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((NDMA + 4) | (0x7 << 4) | (0xf << 8));  // vmcnt; no wait for LDS and exports
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Step g: stages now (g), next (g + 1) and free (g - 1, then g + 3).  Requests past the last group read
+  // the next row's bytes, the next tile's codes or zeros, which nothing uses.
+  auto step = [&](int g, u32x4* cw, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
     Operand<KIND> w[4];
     float d[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      w[q] = operand<KIND>(unpack_codes(*reinterpret_cast<const u32x4*>(st + BOFF + (4 * wn + q) * 1024 + lane * 16)));
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(st + SOFF + (4 * wn + q) * 64 + c * 4);
-      d[q] = h2f(v & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
+      w[q] = operand<KIND>(unpack_codes(cw[q]));
+      d[q] = h2f(dn[q] & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
+      asm volatile("" : "+v"(d[q]));  // fp32 from here on: v_fmac_f32 in place, not v_fma_mix_f32 from fp16
     }
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      const Operand<KIND> a = operand<KIND>(join(*reinterpret_cast<const u32x4*>(st + a0 + t * 2048),
-                                                 *reinterpret_cast<const u32x4*>(st + a1 + t * 2048)));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 s = group_product<KIND>(a, w[q]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d[q], s[i], tot[t][q][i]);
-      }
-    }
-  };
-  // own copies of a stage landed (the next stage's NDMA may be in flight), own reads of the stage
-  // before done; after the barrier that holds for every wave
-  auto sync = [] {
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(NDMA | (0x7 << 4));  // vmcnt NDMA, lgkmcnt 0, no wait for exports
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  };
-  auto step = [&](int g, uint8_t* now, uint8_t* next2) __attribute__((always_inline)) {
     sync();
+    load_codes(cw, g + 2);
     __builtin_amdgcn_sched_barrier(0);
-    dma(next2, g + 2);  // past the last group: bytes of the buffer or zeros that nothing reads
+    dma(free, g + 3);
     __builtin_amdgcn_sched_barrier(0);
-    compute(now);
-    __builtin_amdgcn_sched_barrier(0);
+    // two products at a time; their multiply-adds run behind the next two
+    f32x4 s[2];
+    auto add = [&](int u) AWQ_INLINE {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tot[u / 2][2 * (u % 2) + h][i] = fmaf(d[2 * (u % 2) + h], settled<KIND>(s[h][i]), tot[u / 2][2 * (u % 2) + h][i]);
+    };
+    Operand<KIND> a;
+#pragma unroll
+    for (int u = 0; u < 2 * TM; ++u) {
+      const int t = u / 2;
+      if (u % 2 == 0) {
+        a = operand<KIND>(an);
+        if (t + 1 < TM) {
+          read_a(now, t + 1);
+        } else {
+          read_a(next, 0);
+          read_d(next);
+        }
+      }
+      f32x4 r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) r[h] = group_product<KIND>(a, w[2 * (u % 2) + h]);
+      if (u > 0) add(u - 1);
+      s[0] = r[0], s[1] = r[1];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(2 * TM - 1);
   };
-  dma(st0, 0);
-  dma(st1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt((2 * NDMA) | (0x7 << 4) | (0xf << 8));  // stage 0
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+  read_a(st0, 0);
+  read_d(st0);
   int g = 0;
-  for (; g + 3 <= G; g += 3) {
-    step(g, st0, st2);
-    step(g + 1, st1, st0);
-    step(g + 2, st2, st1);
+  for (; g + 4 <= G; g += 4) {
+    step(g, cw0, st0, st1, st3);
+    step(g + 1, cw1, st1, st2, st0);
+    step(g + 2, cw0, st2, st3, st1);
+    step(g + 3, cw1, st3, st0, st2);
   }
-  if (g < G) step(g, st0, st2);
-  if (g + 1 < G) step(g + 1, st1, st0);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: no copy outlives the block
+  if (g < G) step(g, cw0, st0, st1, st3);
+  if (g + 1 < G) step(g + 1, cw1, st1, st2, st0);
+  if (g + 2 < G) step(g + 2, cw0, st2, st3, st1);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt and lgkmcnt 0: no copy or load outlives the block
   // stores through a resource that ends with the last row's last channel: rows past M are dropped there,
   // channels past N by the lane mask (256 rows of Y span less than 2^31 bytes: host-checked)
   const int n0 = tile0 * 16;
@@ -459,7 +510,7 @@ __global__ __launch_bounds__(512, 2) void w4a8_tile_kernel(const W4a8Args p, con
       0x00020000);
   const __amdgpu_buffer_rsrc_t mr =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.xscale + m0), (short)0, rows * 4, 0x00020000);
-  const int r0 = 16 * TM * wm + 4 * j, ldyb = (int)p.ldy * es;
+  const int r0 = 4 * j, ldyb = (int)p.ldy * es;
 #pragma unroll
   for (int t = 0; t < TM; ++t)
 #pragma unroll
@@ -503,12 +554,12 @@ hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
   const int64_t nt = (a.N + kTileN - 1) / kTileN;
 #define AWQ_TILE(TMV)                                                                                 \
   do {                                                                                                \
-    const int64_t mt = (a.M + 32 * TMV - 1) / (32 * TMV);                                             \
+    const int64_t mt = (a.M + 16 * TMV - 1) / (16 * TMV);                                             \
     if (mt * nt > 0x7ffffff) return hipErrorInvalidValue;                                             \
-    w4a8_tile_kernel<KIND, TMV><<<(unsigned)((mt * nt + 7) / 8 * 8), 512, 0, st>>>(a, sums, Gp, (int)mt, (int)nt); \
+    w4a8_tile_kernel<KIND, TMV><<<(unsigned)((mt * nt + 7) / 8 * 8), 256, 0, st>>>(a, sums, Gp, (int)mt, (int)nt); \
   } while (0)
   if constexpr (KIND != kE4m3Wide) {  // the converted operands leave no registers for eight token tiles
-    if ((a.M + 255) / 256 * nt >= 256) {
+    if ((a.M + 127) / 128 * nt >= 512) {
       AWQ_TILE(8);
       return hipGetLastError();
     }
