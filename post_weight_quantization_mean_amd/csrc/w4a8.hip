@@ -21,6 +21,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -369,8 +370,30 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
     for (int q = 0; q < 4; ++q)
       cw[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, ((4 * wn + q) * G + g) * 1024, 0));
   };
-  load_codes(cw0, 0);
-  load_codes(cw1, 1);
+  // the zero points' operands of eight groups: row sums (past the last row: zero) and steps (past the last
+  // group, whose sum is zero: the last one's)
+  const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint32_t*>(sums + m0 * Gp), (short)0, (int)(rows * Gp * 4), 0x00020000);
+  struct Zero {
+    u32x2 sum[TM];
+    uint32_t step[4][2];
+  } z0, z1;
+  auto load_zero = [&](Zero& z, int b) AWQ_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int g = 8 * b + 2 * j + h;
+        z.step[q][h] = __builtin_amdgcn_raw_buffer_load_b32(sr, ((4 * wn + q) * G + (g < G ? g : G - 1)) * 64 + c * 4, 0, 0);
+      }
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+      z.sum[t] = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(zr, (int)((16 * t + c) * Gp + 8 * b + 2 * j) * 4, 0, 0));
+  };
+  load_zero(z0, 0);
+  load_zero(z1, 1);
+  __builtin_amdgcn_sched_barrier(0);
   dma(st0, 0);
   dma(st1, 1);
   dma(st2, 2);
@@ -379,40 +402,34 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   for (int t = 0; t < TM; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  // minus the zero points' part: lane quarter j holds groups 8 b + 2 j and + 1
-  {
-    const uint32_t* srow[TM];
+  // minus the zero points' part: lane quarter j multiplies groups 8 b + 2 j and + 1, four products each.
+  // The operands of eight groups are requested two rounds ahead, the first ones before the stages' copies.
+  for (int b = 0; b < (int)Gp / 8; ++b) {
+    f16x8 zq[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      u32x4 w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v = z0.step[q][h];
+        const float dz = -h2f(v & 0xffffu) * h2f(v >> 16);
+        const uint32_t hi = f2h(dz), lo = f2h(dz - h2f(hi));
+        w[2 * h] = hi | hi << 16;
+        w[2 * h + 1] = lo | lo << 16;
+      }
+      zq[q] = __builtin_bit_cast(f16x8, w);
+    }
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      const int r = 16 * t + c;
-      srow[t] = sums + (m0 + (r < rows ? r : rows - 1)) * Gp + 2 * j;
+      const f16x8 a = __builtin_bit_cast(f16x8, (u32x4){z0.sum[t][0], z0.sum[t][0], z0.sum[t][1], z0.sum[t][1]});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tot[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, zq[q], tot[t][q], 0, 0, 0);
     }
-    for (int b = 0; b < (int)Gp / 8; ++b) {
-      f16x8 zq[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int tl = 4 * wn + q < nt ? 4 * wn + q : nt - 1;
-        u32x4 w;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int g = 8 * b + 2 * j + h;  // past the last group (its sum is 0): the last one's step
-          const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(sr, (tl * G + (g < G ? g : G - 1)) * 64 + c * 4, 0, 0);
-          const float dz = -h2f(v & 0xffffu) * h2f(v >> 16);
-          const uint32_t hi = f2h(dz), lo = f2h(dz - h2f(hi));
-          w[2 * h] = hi | hi << 16;
-          w[2 * h + 1] = lo | lo << 16;
-        }
-        zq[q] = __builtin_bit_cast(f16x8, w);
-      }
-#pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        const uint2 v = *reinterpret_cast<const uint2*>(srow[t] + 8 * b);
-        const f16x8 a = __builtin_bit_cast(f16x8, (u32x4){v.x, v.x, v.y, v.y});
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tot[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, zq[q], tot[t][q], 0, 0, 0);
-      }
-    }
+    z0 = z1;
+    load_zero(z1, b + 2);
   }
+  load_codes(cw0, 0);
+  load_codes(cw1, 1);
   // this lane's pieces of row c of a token tile (tiles are 16 rows: the same swizzle in each)
   const int a0 = c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
   const int a1 = c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
@@ -484,7 +501,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   };
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt((2 * NDMA) | (0x7 << 4) | (0xf << 8));  // stage 0
+  constexpr int NEWER0 = 2 * NDMA + 8;
+  __builtin_amdgcn_s_waitcnt((NEWER0 & 15) | ((NEWER0 >> 4) << 14) | (0x7 << 4) | (0xf << 8));  // stage 0
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_sched_barrier(0);
@@ -510,34 +528,65 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
       0x00020000);
   const __amdgpu_buffer_rsrc_t mr =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.xscale + m0), (short)0, rows * 4, 0x00020000);
-  const int r0 = 4 * j, ldyb = (int)p.ldy * es;
+  const int ldyb = (int)p.ldy * es;
 #pragma unroll
   for (int t = 0; t < TM; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float xs =
-          __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mr, (r0 + 16 * t + i) * 4, 0, 0));  // 0 past M
+      const float xs = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mr, (16 * t + 4 * j + i) * 4, 0, 0));  // 0 past M
 #pragma unroll
       for (int q = 0; q < 4; ++q) tot[t][q][i] *= xs;
     }
+  float pw[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int nc = (4 * wn + q) * 16 + c;
-    if (n0 + nc < p.N) {
-      const float pw = p.powers[n0 + nc];
-      const int yo = r0 * ldyb + nc * es;
-      if (p.ybf16) {
+    const int n = n0 + (4 * wn + q) * 16 + c;
+    pw[q] = p.powers[n < tiles * 16 ? n : tiles * 16 - 1];
+  }
+  if (p.ybf16) {
+    // through LDS, so that a wave stores whole rows of 256 channels (written from the products' layout,
+    // a store would fill 32 bytes of a line); rows of 528 bytes keep the writes free of bank conflicts
+    constexpr int ROW = 528, RPS = 4 * TM;  // bytes of a row, rows per stage buffer
+    static_assert(RPS * ROW <= STAGE, "a stage buffer holds a quarter of the tile");
+    uint8_t* const pool[4] = {st0, st1, st2, st3};
+    __syncthreads();  // every wave is done with the stages
 #pragma unroll
-        for (int t = 0; t < TM; ++t)
+    for (int t = 0; t < TM; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b16(to_bf16(tot[t][q][i] * pw), yr, yo, (16 * t + i) * ldyb, 0);
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint16_t*>(pool[16 * t / RPS] + (16 * t % RPS + 4 * j + i) * ROW + (64 * wn + 16 * q + c) * 2) =
+              to_bf16(tot[t][q][i] * pw[q]);
+    __syncthreads();
+    // 32 lanes a row; 16-byte stores where every row of Y starts at a multiple of 16 bytes
+    const int cb = (lane & 31) * 8;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)ldyb) & 15u) == 0 && n0 + cb + 8 <= p.N;
+#pragma unroll
+    for (int r = 0; r < 2 * TM; ++r) {
+      const int row = 2 * wn + (lane >> 5);  // of eight
+      const u32x4 v = *reinterpret_cast<const u32x4*>(pool[8 * r / RPS] + (8 * r % RPS + row) * ROW + cb * 2);
+      const int yo = (8 * r + row) * ldyb + cb * 2;
+      if (wide) {
+        __builtin_amdgcn_raw_buffer_store_b128(v, yr, yo, 0, 0);
       } else {
 #pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n0 + cb + e < p.N)
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[e / 2] >> (16 * (e & 1))), yr, yo + 2 * e, 0, 0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int nc = (4 * wn + q) * 16 + c;
+      if (n0 + nc < p.N) {
+        const int yo = 4 * j * ldyb + nc * 4;
+#pragma unroll
         for (int t = 0; t < TM; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i] * pw), yr, yo, (16 * t + i) * ldyb, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i] * pw[q]), yr, yo, (16 * t + i) * ldyb, 0);
       }
     }
   }
