@@ -8,7 +8,6 @@ reference code rejects non-finite input ("AWQï¼šä¸ºä»€ä¹ˆ 4-bit æƒé‡é‡åŒ–è¦å
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -39,6 +38,8 @@ N_CLIP = 10
 ACT_GELU = 0
 ACT_SILU = 1
 ACT_NONE = 2
+AWQ_DTYPE_I8 = 2
+AWQ_DTYPE_E4M3 = 3
 
 _lib = None
 
@@ -543,60 +544,81 @@ class Act8(NamedTuple):
     scale: torch.Tensor
 
 
-_A8_DTYPE = {torch.float32: AWQ_DTYPE_F32, torch.bfloat16: AWQ_DTYPE_BF16, torch.int8: 2, torch.float8_e4m3fn: 3}
+_FLOATS = {torch.float32: AWQ_DTYPE_F32, torch.bfloat16: AWQ_DTYPE_BF16}
+_CODES = {torch.int8: AWQ_DTYPE_I8, torch.float8_e4m3fn: AWQ_DTYPE_E4M3}
+_STORED = {**_FLOATS, **_CODES}
 _ACTS = {"gelu": ACT_GELU, "silu": ACT_SILU, "none": ACT_NONE}
 
+# These calls run once per layer and token, so their host side is kept short: a few attribute reads per
+# operand, and the library's own checks (sizes, strides, alignment) are not repeated here.
 
-def _rows(t: torch.Tensor, name: str, dev: torch.device, shape: Optional[Tuple[int, int]] = None) -> int:
-    """Row stride of a 2-D device tensor [M, K] with unit stride along K."""
-    if t.dim() != 2 or t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D tensor on {dev if dev.type == 'cuda' else 'a GPU'}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+
+def _rows(t: torch.Tensor, name: str, dev: torch.device, shape: Tuple[int, ...]) -> int:
+    """Row stride of a tensor of the given 2-D shape on ``dev`` with unit stride along its rows."""
+    if t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be a tensor of shape {list(shape)} on {dev}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # the stride of a single row says nothing
+    return ld if shape[0] > 1 else shape[1]  # the stride of a single row says nothing
 
 
-def _code(t: torch.dtype, allowed: Tuple[torch.dtype, ...], name: str) -> int:
-    if t not in allowed:
+def _first(t: torch.Tensor, name: str) -> Tuple[torch.device, Tuple[int, ...]]:
+    """Device and shape of the operand that the others have to agree with."""
+    dev, shape = t.device, t.shape
+    if dev.type != "cuda" or len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D device tensor")
+    return dev, shape
+
+
+def _code(t: torch.dtype, allowed, name: str) -> int:
+    code = allowed.get(t)
+    if code is None:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, not {t}")
-    return _A8_DTYPE[t]
+    return code
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
-_CODES = (torch.int8, torch.float8_e4m3fn)
+def _vector(t: torch.Tensor, n: int, dev: torch.device, name: str) -> int:
+    """Address of a contiguous vector of length n on dev."""
+    if t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of length {n} on {dev}")
+    return t.data_ptr()
 
 
-def _a8_out(out, dtype: Optional[torch.dtype], M: int, K: int, dev: torch.device):
-    """(result, tensor, its dtype's code, row stride, scale pointer) of a row operator's output."""
+def _a8_out(out, dtype: Optional[torch.dtype], shape: Tuple[int, ...], dev: torch.device):
+    """(result, address, its dtype's code, row stride, scale address) of a row operator's output."""
     if out is None:
         dt = dtype if dtype is not None else torch.bfloat16
-        code = _code(dt, _FLOATS + _CODES, "dtype")
-        y = torch.empty((M, K), dtype=dt, device=dev)
-        if code < 2:
-            return y, y, code, K, None
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
-        return Act8(y, scale), y, code, K, scale.data_ptr()
+        code = _code(dt, _STORED, "dtype")
+        y = torch.empty(shape, dtype=dt, device=dev)
+        if code < AWQ_DTYPE_I8:
+            return y, y.data_ptr(), code, shape[1], None
+        scale = torch.empty(shape[:1], dtype=torch.float32, device=dev)
+        return Act8(y, scale), y.data_ptr(), code, shape[1], scale.data_ptr()
     eight = isinstance(out, tuple)
     y = out[0] if eight else out
     code = _code(y.dtype, _CODES if eight else _FLOATS, "out")
     if dtype is not None and dtype != y.dtype:
         raise ValueError("dtype and out disagree")
-    ld = _rows(y, "out", dev, (M, K))
+    ld = _rows(y, "out", dev, shape)
     if not eight:
-        return out, y, code, ld, None
-    scale = _out(out[1], (M,), torch.float32, dev, "out's scale")
-    return Act8(y, scale), y, code, ld, scale.data_ptr()
+        return out, y.data_ptr(), code, ld, None
+    if out[1].dtype != torch.float32:
+        raise TypeError("out's scale must be float32")
+    return out, y.data_ptr(), code, ld, _vector(out[1], shape[0], dev, "out's scale")
 
 
-def _raw_stream(dev: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _on(dev: torch.device):
-    """The device of the operands made current where it is not (a kernel launches on the current one)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Queue a library call on dev's current stream, with dev current (kernels launch on the current device)."""
+    fn = getattr(_lib or lib(), name)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        raise AwqError(st, name)
 
 
 def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -606,28 +628,26 @@ def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tenso
     bfloat16 (the default), or int8 / float8_e4m3fn with a scale per row, then y is an ``Act8``.
     Returns y, or (y, h) with a residual, h rounded to the residual's type.  ``out`` (a tensor, or
     an Act8) and ``residual_out`` take the results; ``residual_out`` may be ``residual`` itself."""
-    dev = X.device
-    ldx = _rows(X, "X", dev)
-    M, K = X.shape
-    if gamma.shape != (K,) or gamma.device != dev or not gamma.is_contiguous():
-        raise ValueError("gamma must be a contiguous vector of length K on X's device")
+    dev, shape = _first(X, "X")
+    M, K = shape
+    ldx = _rows(X, "X", dev, shape)
     xc, gc = _code(X.dtype, _FLOATS, "X"), _code(gamma.dtype, _FLOATS, "gamma")
-    rc = ldr = ldh = 0
-    rp = hp = h = None
+    gp = _vector(gamma, K, dev, "gamma")
     if residual is not None:
-        rc, ldr = _code(residual.dtype, _FLOATS, "residual"), _rows(residual, "residual", dev, (M, K))
-        h = residual_out if residual_out is not None else torch.empty((M, K), dtype=residual.dtype, device=dev)
-        if h.dtype != residual.dtype:
-            raise ValueError("residual_out must have residual's dtype")
-        ldh = _rows(h, "residual_out", dev, (M, K))
+        rc, ldr = _code(residual.dtype, _FLOATS, "residual"), _rows(residual, "residual", dev, shape)
+        if residual_out is None:
+            h, ldh = torch.empty(shape, dtype=residual.dtype, device=dev), K
+        else:
+            h, ldh = residual_out, _rows(residual_out, "residual_out", dev, shape)
+            if h.dtype != residual.dtype:
+                raise ValueError("residual_out must have residual's dtype")
         rp, hp = residual.data_ptr(), h.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    res, y, yc, ldy, sp = _a8_out(out, dtype, M, K, dev)
-    with _on(dev):
-        st = lib().awq_rmsnorm(X.data_ptr(), xc, M, K, ldx, rp, rc, ldr, hp, ldh, gamma.data_ptr(), gc, eps,
-                               y.data_ptr(), yc, ldy, sp, _raw_stream(dev))
-    _check(st, "awq_rmsnorm")
+    else:
+        rp, rc, ldr, hp, ldh = None, 0, 0, None, 0
+    res, yp, yc, ldy, sp = _a8_out(out, dtype, shape, dev)
+    _call("awq_rmsnorm", dev, X.data_ptr(), xc, M, K, ldx, rp, rc, ldr, hp, ldh, gp, gc, eps, yp, yc, ldy, sp)
     return res if residual is None else (res, h)
 
 
@@ -637,29 +657,28 @@ def act_mul(G: torch.Tensor, U: Optional[torch.Tensor] = None, s: Optional[torch
     both optional): the input of a layer behind a gate, or with "none" alone the quantization of
     given activations.  G and U may be the halves of one gate/up output.  ``dtype`` and ``out`` as in
     ``rmsnorm``; ``out`` may be G or U where it has their dtype and strides."""
-    dev = G.device
-    ldg = _rows(G, "G", dev)
-    M, K = G.shape
+    dev, shape = _first(G, "G")
+    M, K = shape
+    ldg = _rows(G, "G", dev, shape)
     xc = _code(G.dtype, _FLOATS, "G")
-    up, ldu = None, 0
+    up, ldu, sp = None, 0, None
     if U is not None:
         if U.dtype != G.dtype:
             raise TypeError("U must have G's dtype")
-        up, ldu = U.data_ptr(), _rows(U, "U", dev, (M, K))
-    if s is not None and (s.shape != (K,) or s.dtype != torch.float32 or s.device != dev or not s.is_contiguous()):
-        raise ValueError("s must be a contiguous fp32 vector of length K on G's device")
+        up, ldu = U.data_ptr(), _rows(U, "U", dev, shape)
+    if s is not None:
+        if s.dtype != torch.float32:
+            raise TypeError("s must be float32")
+        sp = _vector(s, K, dev, "s")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}")
-    res, y, yc, ldy, sp = _a8_out(out, dtype, M, K, dev)
-    with _on(dev):
-        st = lib().awq_act_mul(G.data_ptr(), xc, M, K, ldg, up, ldu, s.data_ptr() if s is not None else None,
-                               _ACTS[act], y.data_ptr(), yc, ldy, sp, _raw_stream(dev))
-    _check(st, "awq_act_mul")
+    res, yp, yc, ldy, scp = _a8_out(out, dtype, shape, dev)
+    _call("awq_act_mul", dev, G.data_ptr(), xc, M, K, ldg, up, ldu, sp, _ACTS[act], yp, yc, ldy, scp)
     return res
 
 
 class W4A8Weight(NamedTuple):
-    """A packed weight laid out for ``w4a8`` (``w4a8_weight``): ``data`` uint8, N x K."""
+    """A packed weight laid out for ``w4a8`` (by ``w4a8_weight``): ``data`` uint8, N x K."""
     data: torch.Tensor
     N: int
     K: int
@@ -673,19 +692,19 @@ def w4a8_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
                 out: Optional[torch.Tensor] = None) -> W4A8Weight:
     """The artefact of ``pack`` laid out for ``w4a8``, once per weight.  ``out``: uint8 of at least
     ``w4a8_weight_bytes`` on the same device, 256-byte aligned."""
-    dev = qweight.device
-    if qweight.dim() != 2 or qweight.dtype != torch.int32 or not qweight.is_contiguous() or not qweight.is_cuda:
+    dev, shape = _first(qweight, "qweight")
+    if qweight.dtype != torch.int32 or not qweight.is_contiguous():
         raise ValueError("qweight must be a contiguous int32 [N, K/8] device tensor")
-    N, K = qweight.shape[0], qweight.shape[1] * 8
+    N, K = shape[0], shape[1] * 8
     for t, name in ((scales, "scales"), (zeros, "zeros")):
         if t.shape != (N, K // max(group_size, 1)) or t.dtype != torch.float16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp16 [N, K/group] tensor")
         _same_device(t, dev, name)
+    if out is not None and out.dtype != torch.uint8:
+        raise TypeError("out must be uint8")
     wt, wt_bytes = _workspace(out, w4a8_weight_bytes(N, K), dev)
-    with _on(dev):
-        st = lib().awq_w4a8_weight(qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K, group_size,
-                                   wt.data_ptr(), wt_bytes, _raw_stream(dev))
-    _check(st, "awq_w4a8_weight")
+    _call("awq_w4a8_weight", dev, qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K, group_size,
+          wt.data_ptr(), wt_bytes)
     return W4A8Weight(wt, N, K)
 
 
@@ -701,28 +720,27 @@ def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, ou
     run at the same time (two streams, two graphs) need one each."""
     q, scale = X
     data, N, K = weight
-    dev = q.device
-    ldx = _rows(q, "X.q", dev)
-    M = q.shape[0]
-    if q.shape[1] != K:
-        raise ValueError("X and the weight disagree on K")
+    dev, shape = _first(q, "X.q")
+    M = shape[0]
+    ldx = _rows(q, "X.q", dev, (M, K))
     xc = _code(q.dtype, _CODES, "X.q")
-    if scale.shape != (M,) or scale.dtype != torch.float32 or scale.device != dev or not scale.is_contiguous():
-        raise ValueError("X.scale must be a contiguous fp32 vector of length M on X's device")
+    if scale.dtype != torch.float32:
+        raise TypeError("X.scale must be float32")
+    scp = _vector(scale, M, dev, "X.scale")
     if data.device != dev or data.dtype != torch.uint8 or data.numel() < w4a8_weight_bytes(N, K):
-        raise ValueError("weight must be the result of w4a8_weight on X's device")
+        raise ValueError(f"weight must be the result of w4a8_weight on {dev}")
     if out is None:
-        Y = torch.empty((M, N), dtype=dtype if dtype is not None else torch.float32, device=dev)
-        ldy = N
+        dt = dtype if dtype is not None else torch.float32
+        yc = _code(dt, _FLOATS, "dtype")
+        Y, ldy = torch.empty((M, N), dtype=dt, device=dev), N
     else:
-        Y, ldy = out, _rows(out, "out", dev, (M, N))
+        Y, ldy, yc = out, _rows(out, "out", dev, (M, N)), _code(out.dtype, _FLOATS, "out")
         if dtype is not None and dtype != out.dtype:
             raise ValueError("dtype and out disagree")
-    yc = _code(Y.dtype, _FLOATS, "Y")
-    need = w4a8_workspace_bytes(M, K, N)
-    ws, ws_bytes = _workspace(workspace, need, dev) if need else (None, 0)
-    with _on(dev):
-        st = lib().awq_w4a8(q.data_ptr(), xc, scale.data_ptr(), M, K, ldx, data.data_ptr(), N, GROUP, Y.data_ptr(), yc,
-                            ldy, ws.data_ptr() if need else None, ws_bytes, _raw_stream(dev))
-    _check(st, "awq_w4a8")
+    ws, ws_bytes = None, _lib.awq_w4a8_workspace_bytes(M, K, N)
+    if ws_bytes:
+        workspace, ws_bytes = _workspace(workspace, ws_bytes, dev)
+        ws = workspace.data_ptr()
+    _call("awq_w4a8", dev, q.data_ptr(), xc, scp, M, K, ldx, data.data_ptr(), N, GROUP, Y.data_ptr(), yc, ldy, ws,
+          ws_bytes)
     return Y
