@@ -80,6 +80,8 @@ __global__ __launch_bounds__(256) void w4a8_steps_kernel(const uint16_t* __restr
   powers[n] = ldexpf(1.0f, e);
 }
 
+#define AWQ_INLINE __attribute__((always_inline))
+
 // ---- operand pieces ---------------------------------------------------------------------------------
 // eight operand words (32 channels) of a lane from its four words of codes
 __device__ __forceinline__ i32x8 unpack_codes(const u32x4 w) {
@@ -160,18 +162,17 @@ __device__ __forceinline__ i32x8 join(const u32x4 lo, const u32x4 hi) {
 }
 
 // ---- few tokens: the weight as a stream ----------------------------------------------------------------
-// A block computes CT tiles of 16 channels for up to 16 TT tokens over all of K.  Its eight waves take the
-// groups in turn, each with its own fp32 sums, which meet in LDS at the end in wave order.  Sum x per
-// token and group is one more product, with ones, in the layout of the sums it corrects.  Rows past the
-// last token repeat it and are not stored.
-constexpr int kStWaves = 8;
-
-template <int KIND, int TT, int CT>
-__global__ __launch_bounds__(64 * kStWaves) void w4a8_stream_kernel(const W4a8Args p) {
-  __shared__ float part[kStWaves][TT * CT * 256];
+// A block computes CT tiles of 16 channels for up to 16 TT tokens over all of K.  Its WV waves take the
+// groups in turn, D of them in flight in each wave, with fp32 sums of their own, which meet in LDS at the
+// end in wave order.  Sum x per token and group is one more product, with ones, in the layout of the
+// sums it corrects.  Rows past the last token repeat it and are not stored.
+template <int KIND, int TT, int CT, int WV, int D>
+__global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) {
+  __shared__ float part[WV][CT * 256];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t G = p.K / kGroup, tiles = (p.N + 15) / 16;
+  const int G = (int)(p.K / kGroup);
+  const int64_t tiles = (p.N + 15) / 16;
   const int64_t t0 = (int64_t)blockIdx.x * CT, m0 = (int64_t)blockIdx.y * (16 * TT);
   const uint8_t* xrow[TT];
 #pragma unroll
@@ -195,50 +196,81 @@ __global__ __launch_bounds__(64 * kStWaves) void w4a8_stream_kernel(const W4a8Ar
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int q = 0; q < CT; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-  for (int64_t g = wave; g < G; g += kStWaves) {
-    u32x4 w[CT], xa[TT][2];
+  struct Group {
+    u32x4 w[CT], x[TT][2];
     uint32_t dz[CT];
+  } buf[D];
+  auto fetch = [&](Group& b, int i) AWQ_INLINE {  // this wave's i-th group
+    const int64_t g = wave + i * WV;
 #pragma unroll
     for (int q = 0; q < CT; ++q) {
-      w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[q] + g * 256));
-      dz[q] = srow[q][g * 16];
+      b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[q] + g * 256));
+      b.dz[q] = srow[q][g * 16];
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) b.x[t][h] = *reinterpret_cast<const u32x4*>(xrow[t] + g * kGroup + 16 * h);
+  };
+  auto use = [&](const Group& b) AWQ_INLINE {
+    Operand<KIND> w[CT];
+    float d[CT], z[CT];
+#pragma unroll
+    for (int q = 0; q < CT; ++q) {
+      w[q] = operand<KIND>(unpack_codes(b.w[q]));
+      d[q] = h2f(b.dz[q] & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
+      z[q] = h2f(b.dz[q] >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      xa[t][0] = *reinterpret_cast<const u32x4*>(xrow[t] + g * kGroup);
-      xa[t][1] = *reinterpret_cast<const u32x4*>(xrow[t] + g * kGroup + 16);
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const Operand<KIND> a = operand<KIND>(join(xa[t][0], xa[t][1]));
+      const Operand<KIND> a = operand<KIND>(join(b.x[t][0], b.x[t][1]));
       const f32x4 sx = group_product<KIND>(a, ones);
 #pragma unroll
       for (int q = 0; q < CT; ++q) {
-        const f32x4 s = group_product<KIND>(a, operand<KIND>(unpack_codes(w[q])));
-        const float d = h2f(dz[q] & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
-        const float z = h2f(dz[q] >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
+        const f32x4 s = group_product<KIND>(a, w[q]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d, fmaf(-z, settled<KIND>(sx[i]), settled<KIND>(s[i])), tot[t][q][i]);
+        for (int i = 0; i < 4; ++i)
+          tot[t][q][i] = fmaf(d[q], fmaf(-z[q], settled<KIND>(sx[i]), settled<KIND>(s[i])), tot[t][q][i]);
       }
     }
+  };
+  const int n = (G - wave + WV - 1) / WV;  // this wave's groups (none or fewer where G < wave)
+#pragma unroll
+  for (int i = 0; i < D; ++i)
+    if (i < n) fetch(buf[i], i);
+  int i0 = 0;
+  for (; i0 + 2 * D <= n; i0 += D)
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      use(buf[i]);
+      fetch(buf[i], i0 + i + D);
+    }
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    if (i0 + i < n) use(buf[i]);
+    if (i0 + i + D < n) fetch(buf[i], i0 + i + D);
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+  for (int i = 0; i < D; ++i)
+    if (i0 + i + D < n) use(buf[i]);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    if (t > 0) __syncthreads();
 #pragma unroll
     for (int q = 0; q < CT; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][((t * 16 + 4 * j + i) * CT + q) * 16 + c] = tot[t][q][i];
-  __syncthreads();
-  for (int o = threadIdx.x; o < TT * CT * 256; o += 64 * kStWaves) {
-    const int64_t m = m0 + o / (16 * CT), n = t0 * 16 + o % (16 * CT);
-    float s = 0.0f;
+      for (int i = 0; i < 4; ++i) part[wave][((4 * j + i) * CT + q) * 16 + c] = tot[t][q][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < CT * 256; o += 64 * WV) {
+      const int64_t m = m0 + 16 * t + o / (16 * CT), nn = t0 * 16 + o % (16 * CT);
+      float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kStWaves; ++w) s += part[w][o];
-    if (m < p.M && n < p.N) {
-      const float y = s * (p.xscale[m] * p.powers[n]);
-      if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = to_bf16(y);
-      else static_cast<float*>(p.y)[m * p.ldy + n] = y;
+      for (int w = 0; w < WV; ++w) s += part[w][o];
+      if (m < p.M && nn < p.N) {
+        const float y = s * (p.xscale[m] * p.powers[nn]);
+        if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + nn] = to_bf16(y);
+        else static_cast<float*>(p.y)[m * p.ldy + nn] = y;
+      }
     }
   }
 }
@@ -246,14 +278,10 @@ __global__ __launch_bounds__(64 * kStWaves) void w4a8_stream_kernel(const W4a8Ar
 template <int KIND>
 hipError_t launch_stream(const W4a8Args& a, hipStream_t st) {
   const int64_t tiles = w4a8_tiles(a.N);
-#define AWQ_ST(TTV, CTV)                                                                            \
-  w4a8_stream_kernel<KIND, TTV, CTV>                                                                \
-      <<<dim3((unsigned)((tiles + CTV - 1) / CTV), (unsigned)((a.M + 16 * TTV - 1) / (16 * TTV))),  \
-         64 * kStWaves, 0, st>>>(a)
-  if (a.M <= 16) AWQ_ST(1, 1);
-  else if (a.M <= 32) AWQ_ST(2, 1);
-  else AWQ_ST(4, 1);
-#undef AWQ_ST
+  // two channel tiles per block halve the reads of X where that still leaves more blocks than CUs
+  // (16 tokens x 4096 -> 28672: 15.0 us against 20.4; 5 x 14336 -> 4096: 10.6 against 8.8)
+  if (tiles >= 320) w4a8_stream_kernel<KIND, 1, 2, 8, 2><<<(unsigned)((tiles + 1) / 2), 512, 0, st>>>(a);
+  else w4a8_stream_kernel<KIND, 1, 1, 16, 2><<<(unsigned)tiles, 1024, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -313,7 +341,6 @@ constexpr int kTileStage = 16 * TM * 128 + 1024;
 
 __device__ __forceinline__ int row_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 #define AWQ_LDS_A8 __attribute__((address_space(3)))
-#define AWQ_INLINE __attribute__((always_inline))
 
 template <int KIND, int TM>
 __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, const uint32_t* __restrict__ sums,
@@ -357,7 +384,10 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
     xoff[i] = (uint32_t)(row * p.ldx + 16 * ((lane & 7) ^ row_swizzle(row)));
   }
   const uint32_t soff = (uint32_t)((4 * wn + j) * G * 64 + c * 4);  // the steps of this wave's own four tiles
+  // A request past the last group repeats the last one (nothing uses it): scalar offsets stay below the
+  // resources' ends, and rows past the last are out of range by their vector offset.
   auto dma = [&](uint8_t* st, int g) AWQ_INLINE {
+    g = g < G ? g : G - 1;
 #pragma unroll
     for (int i = 0; i < TM / 2; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (AWQ_LDS_A8 void*)(st + (4 * TM * wn + 8 * i) * 128), 16,
@@ -366,9 +396,12 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   };
   u32x4 cw0[4], cw1[4];  // the codes of the next two steps, by parity
   auto load_codes = [&](u32x4* cw, int g) AWQ_INLINE {
+    g = g < G ? g : G - 1;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      cw[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, ((4 * wn + q) * G + g) * 1024, 0));
+    for (int q = 0; q < 4; ++q) {
+      const int tl = 4 * wn + q < nt ? 4 * wn + q : nt - 1;  // past the last tile: loaded again, not stored
+      cw[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, (tl * G + g) * 1024, 0));
+    }
   };
   // the zero points' operands of eight groups: row sums (past the last row: zero) and steps (past the last
   // group, whose sum is zero: the last one's)
@@ -452,8 +485,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Step g: stages now (g), next (g + 1) and free (g - 1, then g + 3).  Requests past the last group read
-  // the next row's bytes, the next tile's codes or zeros, which nothing uses.
+  // Step g: stages now (g), next (g + 1) and free (g - 1, then g + 3).
   auto step = [&](int g, u32x4* cw, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
     Operand<KIND> w[4];
     float d[4];
@@ -586,36 +618,271 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
         for (int t = 0; t < TM; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i] * pw[q]), yr, yo, (16 * t + i) * ldyb, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i] * pw[q]), yr, yo + (16 * t + i) * ldyb, 0, 0);
       }
     }
   }
 }
 
-int64_t padded_groups(int64_t K) { return (K / kGroup + 7) / 8 * 8; }
+// ---- some tokens: tiles that share their groups among blocks ----------------------------------------------
+// Where 16 TM x 256 tiles are fewer than CUs, each tile's groups are divided among blocks: block
+// (column, split, row) sums groups split n .. split n + n - 1 into fp32 parts that a second kernel adds in
+// split order (one split: straight into Y).  A block has few groups, so what it takes is latency, the
+// memory's and that of a product behind whose result its multiply-adds wait: two sets of four waves take
+// the even and the odd groups of the block (their sums meet in LDS at the end), each from its own ring of
+// three stages that LDS DMA fills with a group's tokens, codes and steps, two stages ahead.
+// The zero points come off per group, with the rows' sums from one more product with ones.
+template <int TM>
+constexpr int kSplitStage = 16 * TM * 128 + 16 * 1024 + 1024;
 
-template <int KIND>
-hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
-  const int64_t G = a.K / kGroup, Gp = padded_groups(a.K), pieces = a.M * Gp * 8;
-  if ((pieces + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
-  w4a8_sums_kernel<KIND != kInt8><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
-      static_cast<const uint8_t*>(a.x), a.M, a.ldx, G, Gp, sums);
-  const int64_t nt = (a.N + kTileN - 1) / kTileN;
-#define AWQ_TILE(TMV)                                                                                 \
-  do {                                                                                                \
-    const int64_t mt = (a.M + 16 * TMV - 1) / (16 * TMV);                                             \
-    if (mt * nt > 0x7ffffff) return hipErrorInvalidValue;                                             \
-    w4a8_tile_kernel<KIND, TMV><<<(unsigned)((mt * nt + 7) / 8 * 8), 256, 0, st>>>(a, sums, Gp, (int)mt, (int)nt); \
-  } while (0)
-  if constexpr (KIND != kE4m3Wide) {  // the converted operands leave no registers for eight token tiles
-    if ((a.M + 127) / 128 * nt >= 512) {
-      AWQ_TILE(8);
-      return hipGetLastError();
+template <int KIND, int TM>
+__global__ __launch_bounds__(512, 2) void w4a8_split_kernel(const W4a8Args p, float* __restrict__ parts, int mtiles,
+                                                            int ntiles, int splits, int per_split) {
+  constexpr bool E4M3 = KIND != kInt8;
+  constexpr int STAGE = kSplitStage<TM>, BOFF = 16 * TM * 128, SOFF = BOFF + 16 * 1024;
+  constexpr int NDMA = TM / 2 + 4 + 1;  // copies per wave and stage
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * STAGE], st1[2 * STAGE], st2[2 * STAGE];
+  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave & 3, set = wave >> 2;
+  const int G = (int)(p.K / kGroup);
+  // each XCD (blocks go to the eight in turn) takes a contiguous run: the rows of one column and split, which
+  // share their codes, then the next split, then the next column
+  const int total = mtiles * ntiles * splits, per = (total + 7) / 8;
+  const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
+  const int cs = __builtin_amdgcn_readfirstlane(id / mtiles);
+  const int col = __builtin_amdgcn_readfirstlane(cs / splits), split = cs - col * splits;
+  const int tile0 = 16 * col;
+  const int64_t m0 = (int64_t)(id - cs * mtiles) * (16 * TM);
+  const int tiles = (int)w4a8_tiles(p.N);
+  const int nt = tiles - tile0 < 16 ? tiles - tile0 : 16;
+  const int rows = p.M - m0 < 16 * TM ? (int)(p.M - m0) : 16 * TM;
+  const int g0 = split * per_split, n = G - g0 < per_split ? G - g0 : per_split;  // this block's groups, at least one
+
+  const int base = set * STAGE;  // this set's half of a stage buffer
+  uint32_t xoff[TM / 2], woff[4];
+#pragma unroll
+  for (int i = 0; i < TM / 2; ++i) {
+    const int row = 4 * TM * wn + 8 * i + (lane >> 3);
+    xoff[i] = (uint32_t)(row * p.ldx + 16 * ((lane & 7) ^ row_swizzle(row)));
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) woff[q] = (uint32_t)((4 * wn + q) * G * 1024 + lane * 16);
+  const uint32_t soff = (uint32_t)((4 * wn + j) * G * 64 + c * 4);
+  // Rows and tiles past the end read as zero (the resources end there); past the block's last group the
+  // resources are empty, so that every step has the same number of copies and none reads for nothing.
+  auto dma = [&](uint8_t* st, int i) AWQ_INLINE {
+    const bool in = 2 * i + set < n;
+    const int g = in ? g0 + 2 * i + set : 0;
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(p.x) + m0 * p.ldx), (short)0,
+        in ? (int)((rows - 1) * p.ldx + p.K) : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint32_t*>(p.codes + (int64_t)tile0 * G * 256), (short)0, in ? nt * G * 1024 : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint32_t*>(p.steps + (int64_t)tile0 * G * 16), (short)0, in ? nt * G * 64 : 0, 0x00020000);
+#pragma unroll
+    for (int k = 0; k < TM / 2; ++k)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (AWQ_LDS_A8 void*)(st + (base + (4 * TM * wn + 8 * k) * 128)), 16,
+                                               (int)xoff[k], g * 128, 0, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (AWQ_LDS_A8 void*)(st + (base + BOFF + (4 * wn + q) * 1024)), 16,
+                                               (int)woff[q], g * 1024, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (AWQ_LDS_A8 void*)(st + (base + SOFF + wn * 256)), 4, (int)soff, g * 64, 0, 0);
+  };
+  dma(st0, 0);
+  dma(st1, 1);
+  f32x4 tot[TM][4];
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int kOne = E4M3 ? 0x38383838 : 0x01010101;
+  const Operand<KIND> ones = operand<KIND>((i32x8){kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne});
+  const int a0 = base + c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
+  const int a1 = base + c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
+  auto step = [&](const uint8_t* now, uint8_t* free, int i) AWQ_INLINE {
+    static_assert(NDMA < 16, "the low four bits of vmcnt");
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    // stage i landed, own reads of stage i - 1 done; behind the barrier, everybody's
+    __builtin_amdgcn_s_waitcnt(NDMA | (0x7 << 4));
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    dma(free, i + 2);
+
+    __builtin_amdgcn_sched_barrier(0);
+    Operand<KIND> w[4];
+    float d[4], z[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      w[q] = operand<KIND>(unpack_codes(*reinterpret_cast<const u32x4*>(now + (base + BOFF + (4 * wn + q) * 1024 + lane * 16))));
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(now + (base + SOFF + (4 * wn + q) * 64 + c * 4));
+      d[q] = h2f(v & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
+      z[q] = h2f(v >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
+      asm volatile("" : "+v"(d[q]), "+v"(z[q]));  // fp32 from here on: v_fmac_f32 in place
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const Operand<KIND> a = operand<KIND>(join(*reinterpret_cast<const u32x4*>(now + (a0 + t * 2048)),
+                                                 *reinterpret_cast<const u32x4*>(now + (a1 + t * 2048))));
+      const f32x4 sx = group_product<KIND>(a, ones);
+      f32x4 r[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = group_product<KIND>(a, w[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tot[t][q][e] = fmaf(d[q], fmaf(-z[q], settled<KIND>(sx[e]), settled<KIND>(r[q][e])), tot[t][q][e]);
+      if (t % 2) __builtin_amdgcn_sched_barrier(0);  // two token tiles at a time keep the registers below 256
+    }
+  };
+  const int pairs = (n + 1) / 2;
+  int i = 0;
+  for (; i + 3 <= pairs; i += 3) {
+    step(st0, st2, i);
+    step(st1, st0, i + 1);
+    step(st2, st1, i + 2);
+  }
+  if (i < pairs) step(st0, st2, i);
+  if (i + 1 < pairs) step(st1, st0, i + 1);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt and lgkmcnt 0: no copy outlives the block
+  // the odd groups' sums through LDS to the even groups' waves: a tile's 16 values a lane, lane by lane
+  __syncthreads();
+  static_assert(TM * 16384 <= 2 * 2 * STAGE && TM * 8192 <= 2 * STAGE, "two stage buffers hold the sums");
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f32x4* at = reinterpret_cast<f32x4*>((t < TM / 2 ? st0 : st1) + ((t % (TM / 2) * 4 + wn) * 4 + q) * 1024) + lane;
+      if (set == 1) *at = tot[t][q];
+    }
+  __syncthreads();
+  if (set == 1) return;
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      tot[t][q] += *(reinterpret_cast<const f32x4*>((t < TM / 2 ? st0 : st1) + ((t % (TM / 2) * 4 + wn) * 4 + q) * 1024) + lane);
+  const int64_t np = (int64_t)tiles * 16;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (4 * wn + q >= nt) continue;
+    const int64_t nn = (int64_t)(tile0 + 4 * wn + q) * 16 + c;
+    if (splits > 1) {
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * t + 4 * j + e;
+          if (r < rows) parts[((int64_t)split * p.M + m0 + r) * np + nn] = tot[t][q][e];
+        }
+    } else if (nn < p.N) {
+      const float pw = p.powers[nn];
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * t + 4 * j + e;
+          if (r < rows) {
+            const float y = tot[t][q][e] * (p.xscale[m0 + r] * pw);
+            if (p.ybf16) static_cast<uint16_t*>(p.y)[(m0 + r) * p.ldy + nn] = to_bf16(y);
+            else static_cast<float*>(p.y)[(m0 + r) * p.ldy + nn] = y;
+          }
+        }
     }
   }
-  AWQ_TILE(4);
-#undef AWQ_TILE
+}
+
+// Y = xscale 2^e (the parts in split order); four channels per thread.
+__global__ __launch_bounds__(256) void w4a8_join_kernel(const W4a8Args p, const float* __restrict__ parts, int splits) {
+  const int64_t np = w4a8_tiles(p.N) * 16, quads = np / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.M * quads) return;
+  const int64_t m = i / quads, n = 4 * (i - m * quads);
+  const float* src = parts + m * np + n;
+  f32x4 s = *reinterpret_cast<const f32x4*>(src);
+  for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(src + (int64_t)k * p.M * np);
+  const float xs = p.xscale[m];
+  const f32x4 pw = *reinterpret_cast<const f32x4*>(p.powers + n);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < p.N) {
+      const float y = s[e] * (xs * pw[e]);
+      if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n + e] = to_bf16(y);
+      else static_cast<float*>(p.y)[m * p.ldy + n + e] = y;
+    }
+}
+
+int64_t padded_groups(int64_t K) { return (K / kGroup + 7) / 8 * 8; }
+
+// How a product runs, by its sizes alone (so that the workspace's size can be told before).
+constexpr int kStream = 0, kSplit = 1, kTile = 2;
+struct Plan {
+  int path;
+  int tm;               // token tiles of 16 per block (split, tile)
+  int splits, per_split;  // split: blocks and groups per tile
+};
+Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
+  const int64_t G = K / kGroup, nt = (N + kTileN - 1) / kTileN;
+  Plan pl{kStream, 0, 1, 0};
+  if (M <= 16) return pl;
+  const int64_t t64 = (M + 63) / 64 * nt, t128 = (M + 127) / 128 * nt;
+  if (t64 >= 256) {
+    pl.path = kTile;
+    pl.tm = t128 >= 512 ? 8 : 4;
+    return pl;
+  }
+  pl.path = kSplit;
+  pl.tm = M <= 32 ? 2 : 4;
+  const int64_t tiles = (M + 16 * pl.tm - 1) / (16 * pl.tm) * nt;
+  int64_t s = 256 / tiles;
+  if (s > G / 2) s = G / 2;
+  if (s < 1) s = 1;
+  pl.per_split = (int)((G + s - 1) / s);
+  pl.splits = (int)((G + pl.per_split - 1) / pl.per_split);
+  return pl;
+}
+
+template <int KIND, int TM>
+hipError_t launch_split(const W4a8Args& a, const Plan& pl, float* parts, hipStream_t st) {
+  const int64_t mt = (a.M + 16 * TM - 1) / (16 * TM), nt = (a.N + kTileN - 1) / kTileN, blocks = mt * nt * pl.splits;
+  w4a8_split_kernel<KIND, TM><<<(unsigned)((blocks + 7) / 8 * 8), 512, 0, st>>>(a, parts, (int)mt, (int)nt, pl.splits,
+                                                                              pl.per_split);
+  if (pl.splits > 1) {
+    const int64_t quads = a.M * w4a8_tiles(a.N) * 4;
+    w4a8_join_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, st>>>(a, parts, pl.splits);
+  }
   return hipGetLastError();
+}
+
+template <int KIND, int TM>
+hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
+  const int64_t G = a.K / kGroup, Gp = padded_groups(a.K), pieces = a.M * Gp * 8;
+  const int64_t mt = (a.M + 16 * TM - 1) / (16 * TM), nt = (a.N + kTileN - 1) / kTileN;
+  if ((pieces + 255) / 256 > 0x7fffffff || mt * nt > 0x7ffffff) return hipErrorInvalidValue;
+  w4a8_sums_kernel<KIND != kInt8><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
+      static_cast<const uint8_t*>(a.x), a.M, a.ldx, G, Gp, sums);
+  w4a8_tile_kernel<KIND, TM><<<(unsigned)((mt * nt + 7) / 8 * 8), 256, 0, st>>>(a, sums, Gp, (int)mt, (int)nt);
+  return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_kind(const W4a8Args& a, void* ws, hipStream_t st) {
+  const Plan pl = w4a8_plan(a.M, a.K, a.N);
+  if (pl.path == kStream) return launch_stream<KIND>(a, st);
+  if (pl.path == kSplit) {
+    float* parts = static_cast<float*>(ws);
+    return pl.tm == 2 ? launch_split<KIND, 2>(a, pl, parts, st) : launch_split<KIND, 4>(a, pl, parts, st);
+  }
+  uint32_t* sums = static_cast<uint32_t*>(ws);
+  if constexpr (KIND != kE4m3Wide) {  // the converted operands leave no registers for eight token tiles
+    if (pl.tm == 8) return launch_tile<KIND, 8>(a, sums, st);
+  }
+  return launch_tile<KIND, 4>(a, sums, st);
 }
 
 }  // namespace
@@ -630,22 +897,15 @@ hipError_t launch_w4a8_weight(const int32_t* qweight, const uint16_t* scales, co
   return hipGetLastError();
 }
 
-// above this many tokens the tile kernel runs
-constexpr int64_t kStreamMax = 64;
-
 size_t w4a8_workspace(int64_t M, int64_t K, int64_t N) {
-  return M > kStreamMax ? (size_t)(M * padded_groups(K) * 4) : 0;
+  const Plan pl = w4a8_plan(M, K, N);
+  if (pl.path == kTile) return (size_t)(M * padded_groups(K) * 4);
+  return pl.splits > 1 ? (size_t)(pl.splits * M * w4a8_tiles(N) * 16 * 4) : 0;
 }
 
 hipError_t launch_w4a8(const W4a8Args& a, void* ws, hipStream_t st) {
-  const int kind = !a.e4m3 ? kInt8 : a.ybf16 ? kE4m3Fast : kE4m3Wide;
-  if (a.M > kStreamMax) {
-    uint32_t* sums = static_cast<uint32_t*>(ws);
-    if (kind == kInt8) return launch_tile<kInt8>(a, sums, st);
-    return kind == kE4m3Fast ? launch_tile<kE4m3Fast>(a, sums, st) : launch_tile<kE4m3Wide>(a, sums, st);
-  }
-  if (kind == kInt8) return launch_stream<kInt8>(a, st);
-  return kind == kE4m3Fast ? launch_stream<kE4m3Fast>(a, st) : launch_stream<kE4m3Wide>(a, st);
+  if (!a.e4m3) return launch_kind<kInt8>(a, ws, st);
+  return a.ybf16 ? launch_kind<kE4m3Fast>(a, ws, st) : launch_kind<kE4m3Wide>(a, ws, st);
 }
 
 }  // namespace awq
