@@ -831,11 +831,16 @@ Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
   Plan pl{kStream, 0, 1, 0};
   if (M <= 16) return pl;
   const int64_t t64 = (M + 63) / 64 * nt, t128 = (M + 127) / 128 * nt;
-  if (t64 >= 256) {
+  if (t64 > 128) {
+    // 128-token tiles do a token's work in 0.77 of the time but leave whole rounds of 512 blocks (two per CU)
+    // emptier: they run where the last round is five sixths full or there are many (K = 4096, e4m3, us, 64- against
+    // 128-token tiles: 448 of the latter 73 / 68, 384 66 / 68, 560 98 / 103, 896 135 / 132)
     pl.path = kTile;
-    pl.tm = t128 >= 512 ? 8 : 4;
+    pl.tm = t128 >= 1024 || t128 * 6 >= (t128 + 511) / 512 * 512 * 5 ? 8 : 4;
     return pl;
   }
+  // few tiles: split (256 x 14336 -> 4096, 64 tiles: 37 us against 93 unsplit; at 128 tiles and more a split is
+  // one block per tile and loses to the tile kernel's two per CU: 41 against 33 at 224)
   pl.path = kSplit;
   pl.tm = M <= 32 ? 2 : 4;
   const int64_t tiles = (M + 16 * pl.tm - 1) / (16 * pl.tm) * nt;
