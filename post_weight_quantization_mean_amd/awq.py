@@ -42,6 +42,7 @@ AWQ_DTYPE_I8 = 2
 AWQ_DTYPE_E4M3 = 3
 
 _lib = None
+_a8 = None  # the native binding of the 8-bit activation calls, once the library is loaded
 
 
 class AwqError(RuntimeError):
@@ -122,8 +123,23 @@ def lib() -> ctypes.CDLL:
         L.awq_w4a8.argtypes = [vp, ci, vp, i64, i64, i64, vp, i64, i32, vp, ci, i64, vp, sz, vp]
         if L.awq_abi_version() != 8:
             raise ImportError("libawq ABI version mismatch")
+        _bind(L)
         _lib = L
     return _lib
+
+
+def _bind(L: ctypes.CDLL) -> None:
+    """Load the native binding of the calls that run once per layer and token and hand it L's functions."""
+    global _a8
+    from . import _a8 as binding
+    names = ("awq_rmsnorm", "awq_act_mul", "awq_w4a8", "awq_w4a8_weight_bytes", "awq_w4a8_workspace_bytes")
+    binding.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Act8, AwqError)
+    _a8 = binding
+
+
+def _bound():
+    lib()
+    return _a8
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -544,81 +560,19 @@ class Act8(NamedTuple):
     scale: torch.Tensor
 
 
-_FLOATS = {torch.float32: AWQ_DTYPE_F32, torch.bfloat16: AWQ_DTYPE_BF16}
-_CODES = {torch.int8: AWQ_DTYPE_I8, torch.float8_e4m3fn: AWQ_DTYPE_E4M3}
-_STORED = {**_FLOATS, **_CODES}
 _ACTS = {"gelu": ACT_GELU, "silu": ACT_SILU, "none": ACT_NONE}
 
-# These calls run once per layer and token, so their host side is kept short: a few attribute reads per
-# operand, and the library's own checks (sizes, strides, alignment) are not repeated here.
 
-
-def _rows(t: torch.Tensor, name: str, dev: torch.device, shape: Tuple[int, ...]) -> int:
-    """Row stride of a tensor of the given 2-D shape on ``dev`` with unit stride along its rows."""
-    if t.shape != shape or t.device != dev:
-        raise ValueError(f"{name} must be a tensor of shape {list(shape)} on {dev}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have unit stride along its last axis")
-    return ld if shape[0] > 1 else shape[1]  # the stride of a single row says nothing
-
-
-def _first(t: torch.Tensor, name: str) -> Tuple[torch.device, Tuple[int, ...]]:
-    """Device and shape of the operand that the others have to agree with."""
-    dev, shape = t.device, t.shape
-    if dev.type != "cuda" or len(shape) != 2:
-        raise ValueError(f"{name} must be a 2-D device tensor")
-    return dev, shape
-
-
-def _code(t: torch.dtype, allowed, name: str) -> int:
-    code = allowed.get(t)
-    if code is None:
-        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, not {t}")
-    return code
-
-
-def _vector(t: torch.Tensor, n: int, dev: torch.device, name: str) -> int:
-    """Address of a contiguous vector of length n on dev."""
-    if t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of length {n} on {dev}")
-    return t.data_ptr()
-
-
-def _a8_out(out, dtype: Optional[torch.dtype], shape: Tuple[int, ...], dev: torch.device):
-    """(result, address, its dtype's code, row stride, scale address) of a row operator's output."""
-    if out is None:
-        dt = dtype if dtype is not None else torch.bfloat16
-        code = _code(dt, _STORED, "dtype")
-        y = torch.empty(shape, dtype=dt, device=dev)
-        if code < AWQ_DTYPE_I8:
-            return y, y.data_ptr(), code, shape[1], None
-        scale = torch.empty(shape[:1], dtype=torch.float32, device=dev)
-        return Act8(y, scale), y.data_ptr(), code, shape[1], scale.data_ptr()
-    eight = isinstance(out, tuple)
-    y = out[0] if eight else out
-    code = _code(y.dtype, _CODES if eight else _FLOATS, "out")
-    if dtype is not None and dtype != y.dtype:
-        raise ValueError("dtype and out disagree")
-    ld = _rows(y, "out", dev, shape)
-    if not eight:
-        return out, y.data_ptr(), code, ld, None
-    if out[1].dtype != torch.float32:
-        raise TypeError("out's scale must be float32")
-    return out, y.data_ptr(), code, ld, _vector(out[1], shape[0], dev, "out's scale")
-
-
-def _call(name: str, dev: torch.device, *args) -> None:
-    """Queue a library call on dev's current stream, with dev current (kernels launch on the current device)."""
-    fn = getattr(_lib or lib(), name)
-    index = dev.index
+def _on(t: torch.Tensor, call, *args):
+    """call(*args, stream) on the current stream of t's device, with that device current (kernels launch on
+    the current one).  A host tensor goes through as it is: the call refuses it."""
+    index = t.get_device()
+    if index < 0:
+        return call(*args, 0)
     if torch._C._cuda_getDevice() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st:
-        raise AwqError(st, name)
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -628,27 +582,7 @@ def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tenso
     bfloat16 (the default), or int8 / float8_e4m3fn with a scale per row, then y is an ``Act8``.
     Returns y, or (y, h) with a residual, h rounded to the residual's type.  ``out`` (a tensor, or
     an Act8) and ``residual_out`` take the results; ``residual_out`` may be ``residual`` itself."""
-    dev, shape = _first(X, "X")
-    M, K = shape
-    ldx = _rows(X, "X", dev, shape)
-    xc, gc = _code(X.dtype, _FLOATS, "X"), _code(gamma.dtype, _FLOATS, "gamma")
-    gp = _vector(gamma, K, dev, "gamma")
-    if residual is not None:
-        rc, ldr = _code(residual.dtype, _FLOATS, "residual"), _rows(residual, "residual", dev, shape)
-        if residual_out is None:
-            h, ldh = torch.empty(shape, dtype=residual.dtype, device=dev), K
-        else:
-            h, ldh = residual_out, _rows(residual_out, "residual_out", dev, shape)
-            if h.dtype != residual.dtype:
-                raise ValueError("residual_out must have residual's dtype")
-        rp, hp = residual.data_ptr(), h.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    else:
-        rp, rc, ldr, hp, ldh = None, 0, 0, None, 0
-    res, yp, yc, ldy, sp = _a8_out(out, dtype, shape, dev)
-    _call("awq_rmsnorm", dev, X.data_ptr(), xc, M, K, ldx, rp, rc, ldr, hp, ldh, gp, gc, eps, yp, yc, ldy, sp)
-    return res if residual is None else (res, h)
+    return _on(X, (_a8 or _bound()).rmsnorm, X, gamma, residual, eps, dtype, out, residual_out)
 
 
 def act_mul(G: torch.Tensor, U: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, act: str = "silu",
@@ -657,24 +591,10 @@ def act_mul(G: torch.Tensor, U: Optional[torch.Tensor] = None, s: Optional[torch
     both optional): the input of a layer behind a gate, or with "none" alone the quantization of
     given activations.  G and U may be the halves of one gate/up output.  ``dtype`` and ``out`` as in
     ``rmsnorm``; ``out`` may be G or U where it has their dtype and strides."""
-    dev, shape = _first(G, "G")
-    M, K = shape
-    ldg = _rows(G, "G", dev, shape)
-    xc = _code(G.dtype, _FLOATS, "G")
-    up, ldu, sp = None, 0, None
-    if U is not None:
-        if U.dtype != G.dtype:
-            raise TypeError("U must have G's dtype")
-        up, ldu = U.data_ptr(), _rows(U, "U", dev, shape)
-    if s is not None:
-        if s.dtype != torch.float32:
-            raise TypeError("s must be float32")
-        sp = _vector(s, K, dev, "s")
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}")
-    res, yp, yc, ldy, scp = _a8_out(out, dtype, shape, dev)
-    _call("awq_act_mul", dev, G.data_ptr(), xc, M, K, ldg, up, ldu, sp, _ACTS[act], yp, yc, ldy, scp)
-    return res
+    return _on(G, (_a8 or _bound()).act_mul, G, U, s, code, dtype, out)
 
 
 class W4A8Weight(NamedTuple):
@@ -692,10 +612,9 @@ def w4a8_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
                 out: Optional[torch.Tensor] = None) -> W4A8Weight:
     """The artefact of ``pack`` laid out for ``w4a8``, once per weight.  ``out``: uint8 of at least
     ``w4a8_weight_bytes`` on the same device, 256-byte aligned."""
-    dev, shape = _first(qweight, "qweight")
-    if qweight.dtype != torch.int32 or not qweight.is_contiguous():
+    if qweight.dim() != 2 or qweight.dtype != torch.int32 or not qweight.is_cuda or not qweight.is_contiguous():
         raise ValueError("qweight must be a contiguous int32 [N, K/8] device tensor")
-    N, K = shape[0], shape[1] * 8
+    N, K, dev = qweight.shape[0], qweight.shape[1] * 8, qweight.device
     for t, name in ((scales, "scales"), (zeros, "zeros")):
         if t.shape != (N, K // max(group_size, 1)) or t.dtype != torch.float16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp16 [N, K/group] tensor")
@@ -703,8 +622,8 @@ def w4a8_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
     if out is not None and out.dtype != torch.uint8:
         raise TypeError("out must be uint8")
     wt, wt_bytes = _workspace(out, w4a8_weight_bytes(N, K), dev)
-    _call("awq_w4a8_weight", dev, qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K, group_size,
-          wt.data_ptr(), wt_bytes)
+    _check(_on(qweight, lib().awq_w4a8_weight, qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), N, K,
+               group_size, wt.data_ptr(), wt_bytes), "awq_w4a8_weight")
     return W4A8Weight(wt, N, K)
 
 
@@ -720,27 +639,4 @@ def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, ou
     run at the same time (two streams, two graphs) need one each."""
     q, scale = X
     data, N, K = weight
-    dev, shape = _first(q, "X.q")
-    M = shape[0]
-    ldx = _rows(q, "X.q", dev, (M, K))
-    xc = _code(q.dtype, _CODES, "X.q")
-    if scale.dtype != torch.float32:
-        raise TypeError("X.scale must be float32")
-    scp = _vector(scale, M, dev, "X.scale")
-    if data.device != dev or data.dtype != torch.uint8 or data.numel() < w4a8_weight_bytes(N, K):
-        raise ValueError(f"weight must be the result of w4a8_weight on {dev}")
-    if out is None:
-        dt = dtype if dtype is not None else torch.float32
-        yc = _code(dt, _FLOATS, "dtype")
-        Y, ldy = torch.empty((M, N), dtype=dt, device=dev), N
-    else:
-        Y, ldy, yc = out, _rows(out, "out", dev, (M, N)), _code(out.dtype, _FLOATS, "out")
-        if dtype is not None and dtype != out.dtype:
-            raise ValueError("dtype and out disagree")
-    ws, ws_bytes = None, _lib.awq_w4a8_workspace_bytes(M, K, N)
-    if ws_bytes:
-        workspace, ws_bytes = _workspace(workspace, ws_bytes, dev)
-        ws = workspace.data_ptr()
-    _call("awq_w4a8", dev, q.data_ptr(), xc, scp, M, K, ldx, data.data_ptr(), N, GROUP, Y.data_ptr(), yc, ldy, ws,
-          ws_bytes)
-    return Y
+    return _on(q, (_a8 or _bound()).w4a8, q, scale, data, N, K, dtype, out, workspace)

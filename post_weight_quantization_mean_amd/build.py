@@ -1,4 +1,5 @@
-"""Builds libawq.so (all HIP kernels + the C-ABI host code) in-tree for gfx950 with hipcc.
+"""Builds libawq.so (all HIP kernels + the C-ABI host code) in-tree for gfx950 with hipcc, and _a8.so (the
+native Python binding of the 8-bit activation calls: host code, no kernels) with g++.
 
 Usage: python -m post_weight_quantization_mean_amd.build   (or __graft_entry__.build()).
 """
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libawq.so")
+BINDING = os.path.join(PKG, "_a8.so")
 
 SOURCES = ["stats.hip", "scales.hip", "search.hip", "gram.hip", "pack.hip", "clip.hip", "fold.hip", "w4a16.hip",
            "rows8.hip", "w4a8.hip", "awq_api.cpp", "a8_api.cpp"]
@@ -37,8 +39,26 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP toolchain is required to build libawq")
 
 
+def build_binding() -> None:
+    """Compile _a8.so against this interpreter and torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "a8_binding.cpp"), "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on a8_binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libawq.so; always rebuilds.  Returns the library path."""
+    """Compile every source, link libawq.so and build _a8.so; always rebuilds.  Returns the library path."""
     cc = hipcc()
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -58,7 +78,9 @@ def build(verbose: bool = False) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
+        binding = pool.submit(build_binding)
         objs = list(pool.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
