@@ -12,6 +12,8 @@
 //
 // Maxima are taken over the bits of |v| as unsigned integers: the same order as the floats', with NaN
 // above infinity, so that a NaN reaches the row's scale (fmaxf would drop it).
+#include <type_traits>
+
 #include "a8_internal.h"
 
 namespace awq {
@@ -34,15 +36,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // round to n
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
+// The same types for rows that start anywhere: the hardware takes such accesses, at a few extra cycles where
+// one crosses a cache line.
+typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
 // eight consecutive elements as loaded, and as fp32
 template <int T>
 struct Raw8 {
   u32x4 q[T == kF32 ? 2 : 1];
 };
-template <int T>
+// ALIGNED: the elements start at a multiple of 16 bytes, otherwise anywhere.
+template <int T, bool ALIGNED>
 __device__ __forceinline__ Raw8<T> load8(const void* p, int64_t i) {
+  using V = typename std::conditional<ALIGNED, u32x4, u32x4_any>::type;
   Raw8<T> r;
-  const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * esize<T>());
+  const V* s = reinterpret_cast<const V*>(static_cast<const char*>(p) + i * esize<T>());
   r.q[0] = s[0];
   if constexpr (T == kF32) r.q[1] = s[1];
   return r;
@@ -53,14 +62,34 @@ __device__ __forceinline__ float elem8(const Raw8<T>& r, int t) {  // t known at
   const uint32_t w = r.q[0][t / 2];
   return __uint_as_float(t & 1 ? w & 0xffff0000u : w << 16);
 }
+template <bool ALIGNED>
 __device__ __forceinline__ void store8_f32(void* p, int64_t i, const float* v) {
-  float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-  d[0] = make_float4(v[0], v[1], v[2], v[3]);
-  d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  using V = typename std::conditional<ALIGNED, u32x4, u32x4_any>::type;
+  V* d = reinterpret_cast<V*>(static_cast<float*>(p) + i);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    d[h] = (u32x4){__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                   __float_as_uint(v[4 * h + 3])};
 }
+template <bool ALIGNED>
 __device__ __forceinline__ void store8_bf16(void* p, int64_t i, const float* v) {
-  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
+  using V = typename std::conditional<ALIGNED, u32x4, u32x4_any>::type;
+  *reinterpret_cast<V*>(static_cast<uint16_t*>(p) + i) =
       (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void store8_codes(void* p, int64_t i, const u32x2 w) {
+  using V = typename std::conditional<ALIGNED, u32x2, u32x2_any>::type;
+  *reinterpret_cast<V*>(static_cast<uint8_t*>(p) + i) = w;
+}
+template <int XT>
+__device__ __forceinline__ float elem1(const void* p, int64_t i) {
+  if constexpr (XT == kF32) return static_cast<const float*>(p)[i];
+  else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+__device__ __forceinline__ void store1(void* p, int64_t i, float v, int type) {
+  if (type == kF32) static_cast<float*>(p)[i] = v;
+  else static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16(v, v);
 }
 
 // four codes rne(v c) in one word.  int8: v c + 1.5 2^23 leaves the rounded integer, two's complement,
@@ -90,7 +119,22 @@ __device__ __forceinline__ float activate(float x, int act, bool fine) {
     }
     return x * __builtin_amdgcn_rcpf(1.0f + e);
   }
-  if (act == kActGelu) return 0.5f * x * erfcf(-x * 0.70710678118654752f);
+  if (act == kActGelu) {
+    // erfc(z) = exp(-z^2) p(1 / (1 + 0.43 z)) for z = |x| / sqrt 2: p of degree 8 fitted to exp(z^2) erfc(z) with
+    // relative error 2^-23.4 up to z = 10.5 (above it the product underflows), halved here
+    const float a = fabsf(x), t = __builtin_amdgcn_rcpf(fmaf(a, 0.30405592918395996f, 1.0f));
+    float p = 0.03716862201690674f;
+    p = fmaf(p, t, -0.15669101476669312f);
+    p = fmaf(p, t, 0.19490274786949158f);
+    p = fmaf(p, t, -0.0462779626250267f);
+    p = fmaf(p, t, 0.12572525441646576f);
+    p = fmaf(p, t, 0.10152062773704529f);
+    p = fmaf(p, t, 0.12242478877305984f);
+    p = fmaf(p, t, 0.12122516334056854f);
+    p = fmaf(p, t, 1.818873215597705e-06f);
+    const float e = p * __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2e));  // erfc(z) / 2
+    return x < 0.0f ? x * e : fmaf(-x, e, x);
+  }
   return x;
 }
 
@@ -155,33 +199,54 @@ __device__ __forceinline__ RowFactors row_factors(const RowArgs& a, float sum, u
 }
 
 // ---- a row in registers -------------------------------------------------------------------------
-// W waves per row (W = 1: four rows per block), U units of eight elements per lane.
-template <int OP, int XT, int BT, int W, int U>
+// W waves per row (W = 1: four rows per block), U units of eight elements per lane.  ALIGNED: every row of
+// every operand starts at a multiple of 16 bytes (8-bit outputs: 8) and K is a multiple of 8; otherwise the
+// first K % 8 threads of a row take one of its last elements each.
+template <int OP, int XT, int BT, int W, int U, bool ALIGNED>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowArgs a) {
   constexpr int T = 64 * W, RPB = W == 1 ? 4 : 1;
   __shared__ float2 red[2][W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t = W == 1 ? lane : threadIdx.x;
   const int units = (int)(a.K / 8);
+  const bool tail = !ALIGNED && t < (int)(a.K % 8);
+  const int kt = 8 * units + t;
   const int ytype = a.y_type, col_type = a.col_type;
   int parity = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + (W == 1 ? wave : 0); row < a.M; row += (int64_t)gridDim.x * RPB) {
-    // units past the row's end load its last one again and count for nothing
+    // units past the row's end load its first one again and count for nothing
     int k[U];
     Raw8<XT> x[U];
     Raw8<BT == kNoOperand ? kBf16 : BT> b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int unit = u * T + t;
-      k[u] = 8 * (unit < units ? unit : units - 1);
-      x[u] = load8<XT>(a.x, row * a.ldx + k[u]);
+      k[u] = unit < units ? 8 * unit : 0;
+      if (!ALIGNED && units == 0) continue;
+      x[u] = load8<XT, ALIGNED>(a.x, row * a.ldx + k[u]);
     }
     if constexpr (BT != kNoOperand) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) b[u] = load8<BT>(a.b, row * a.ldb + k[u]);
+      for (int u = 0; u < U; ++u)
+        if (ALIGNED || units > 0) b[u] = load8<BT, ALIGNED>(a.b, row * a.ldb + k[u]);
     }
-    float v[U][8], sum = 0.0f;
-    uint32_t top = 0;
+    float vt = 0.0f, ht = 0.0f;  // the tail element's value, and its h
+    if (tail) {
+      ht = elem1<XT>(a.x, row * a.ldx + kt);
+      const float bt = BT != kNoOperand ? elem1<BT == kNoOperand ? kBf16 : BT>(a.b, row * a.ldb + kt) : 0.0f;
+      const float ct = col_type == kF32 ? elem1<kF32>(a.col, kt) : col_type == kBf16 ? elem1<kBf16>(a.col, kt) : 1.0f;
+      if (OP == kOpNorm) {
+        if (BT != kNoOperand) ht += bt;
+        vt = ht * ct;
+        if (BT != kNoOperand && a.h != nullptr) store1(a.h, row * a.ldh + kt, ht, BT);
+      } else {
+        vt = activate(ht, a.act, ytype == kF32);
+        if (BT != kNoOperand) vt *= bt;
+        if (col_type == kF32) vt *= __builtin_amdgcn_rcpf(ct);
+      }
+    }
+    float v[U][8], sum = ht * ht;
+    uint32_t top = abs_bits(vt);
     if constexpr (OP == kOpNorm) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -196,22 +261,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
         sum += in ? sq : 0.0f;
         if constexpr (BT != kNoOperand) {
           if (in && a.h != nullptr) {
-            if constexpr (BT == kF32) store8_f32(a.h, row * a.ldh + k[u], v[u]);
-            else store8_bf16(a.h, row * a.ldh + k[u], v[u]);
+            if constexpr (BT == kF32) store8_f32<ALIGNED>(a.h, row * a.ldh + k[u], v[u]);
+            else store8_bf16<ALIGNED>(a.h, row * a.ldh + k[u], v[u]);
           }
         }
       }
-      if (col_type == kF32) {
+      if (!ALIGNED && units == 0) {
+      } else if (col_type == kF32) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const Raw8<kF32> g = load8<kF32>(a.col, k[u]);
+          const Raw8<kF32> g = load8<kF32, ALIGNED>(a.col, k[u]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] *= elem8(g, e);
         }
       } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const Raw8<kBf16> g = load8<kBf16>(a.col, k[u]);
+          const Raw8<kBf16> g = load8<kBf16, ALIGNED>(a.col, k[u]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] *= elem8(g, e);
         }
@@ -224,10 +290,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
           v[u][e] = activate(elem8(x[u], e), a.act, ytype == kF32);
           if constexpr (BT != kNoOperand) v[u][e] *= elem8(b[u], e);
         }
-      if (col_type == kF32) {
+      if (col_type == kF32 && (ALIGNED || units > 0)) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const Raw8<kF32> s = load8<kF32>(a.col, k[u]);
+          const Raw8<kF32> s = load8<kF32, ALIGNED>(a.col, k[u]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[u][e] *= __builtin_amdgcn_rcpf(elem8(s, e));
         }
@@ -249,10 +315,15 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (u * T + t < units)
-          *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.y) + row * a.ldy + k[u]) =
-              (u32x2){codes4(v[u], f.code, ytype == kE4m3), codes4(v[u] + 4, f.code, ytype == kE4m3)};
+          store8_codes<ALIGNED>(a.y, row * a.ldy + k[u],
+                                (u32x2){codes4(v[u], f.code, ytype == kE4m3), codes4(v[u] + 4, f.code, ytype == kE4m3)});
+      if (tail) {
+        const float w[4] = {vt, vt, vt, vt};
+        static_cast<uint8_t*>(a.y)[row * a.ldy + kt] = (uint8_t)codes4(w, f.code, ytype == kE4m3);
+      }
       if (t == 0) a.scale[row] = f.scale;
     } else {
+      if (tail) store1(a.y, row * a.ldy + kt, OP == kOpNorm ? vt * f.mul : vt, ytype);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (OP == kOpNorm) {
@@ -260,8 +331,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
           for (int e = 0; e < 8; ++e) v[u][e] *= f.mul;
         }
         if (u * T + t < units) {
-          if (ytype == kF32) store8_f32(a.y, row * a.ldy + k[u], v[u]);
-          else store8_bf16(a.y, row * a.ldy + k[u], v[u]);
+          if (ytype == kF32) store8_f32<ALIGNED>(a.y, row * a.ldy + k[u], v[u]);
+          else store8_bf16<ALIGNED>(a.y, row * a.ldy + k[u], v[u]);
         }
       }
     }
@@ -269,18 +340,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
 }
 
 // ---- any row: two passes ------------------------------------------------------------------------
-// Rows longer than the registers of a block, rows that are not 16-byte aligned and odd K: single
-// elements, read again for the store (the second read comes from the caches for all but the longest).
-template <int XT>
-__device__ __forceinline__ float elem1(const void* p, int64_t i) {
-  if constexpr (XT == kF32) return static_cast<const float*>(p)[i];
-  else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
-__device__ __forceinline__ void store1(void* p, int64_t i, float v, int type) {
-  if (type == kF32) static_cast<float*>(p)[i] = v;
-  else static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16(v, v);
-}
-
+// Rows longer than the registers of a block (65536 elements): single elements, read again for the store.
 template <int OP, int XT, int BT>
 __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
   constexpr int W = 16;
@@ -328,12 +388,12 @@ __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
 
 unsigned grid_of(int64_t rows) { return (unsigned)(rows < 0x40000000 ? rows : 0x40000000); }
 
-template <int OP, int XT, int BT>
-hipError_t launch_rows(const RowArgs& a, bool vec, hipStream_t st) {
+template <int OP, int XT, int BT, bool ALIGNED>
+void launch_rows_as(const RowArgs& a, hipStream_t st) {
   const int64_t units = a.K / 8;
-#define AWQ_ROWS(WV, UV)                                                                               \
-  rows_kernel<OP, XT, BT, WV, UV><<<grid_of(WV == 1 ? (a.M + 3) / 4 : a.M), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
-  if (!vec || units > 16 * 64 * 8) {
+#define AWQ_ROWS(WV, UV) \
+  rows_kernel<OP, XT, BT, WV, UV, ALIGNED><<<grid_of(WV == 1 ? (a.M + 3) / 4 : a.M), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
+  if (units > 16 * 64 * 8) {
     rows_any_kernel<OP, XT, BT><<<grid_of(a.M), 1024, 0, st>>>(a);
   } else if (a.M <= 256 && units > 128) {
     // fewer rows than CUs: spread each over sixteen waves
@@ -352,6 +412,11 @@ hipError_t launch_rows(const RowArgs& a, bool vec, hipStream_t st) {
     AWQ_ROWS(16, 8);
   }
 #undef AWQ_ROWS
+}
+template <int OP, int XT, int BT>
+hipError_t launch_rows(const RowArgs& a, bool aligned, hipStream_t st) {
+  if (aligned) launch_rows_as<OP, XT, BT, true>(a, st);
+  else launch_rows_as<OP, XT, BT, false>(a, st);
   return hipGetLastError();
 }
 
