@@ -702,96 +702,152 @@ __global__ __launch_bounds__(512, 2) void w4a8_split_kernel(const W4a8Args p, fl
   const Operand<KIND> ones = operand<KIND>((i32x8){kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne});
   const int a0 = base + c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
   const int a1 = base + c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
-  auto step = [&](const uint8_t* now, uint8_t* free, int i) AWQ_INLINE {
-    static_assert(NDMA < 16, "the low four bits of vmcnt");
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  i32x8 an;                // the next token tile's bytes
+  u32x4 cw[4];             // the next step's codes
+  uint32_t dn[4];          // and its steps and zero points
+  auto read_a = [&](const uint8_t* st, int t) AWQ_INLINE {
+    an = join(*reinterpret_cast<const u32x4*>(st + (a0 + t * 2048)), *reinterpret_cast<const u32x4*>(st + (a1 + t * 2048)));
+  };
+  auto read_w = [&](const uint8_t* st) AWQ_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      cw[q] = *reinterpret_cast<const u32x4*>(st + (base + BOFF + (4 * wn + q) * 1024 + lane * 16));
+      dn[q] = *reinterpret_cast<const uint32_t*>(st + (base + SOFF + (4 * wn + q) * 64 + c * 4));
+    }
+  };
+  auto sync = [&](auto newer) AWQ_INLINE {  // own copies but the newest landed, own reads done; then everybody's
+    constexpr int NEWER = decltype(newer)::value;
+    static_assert(NEWER < 16, "the low four bits of vmcnt");
     __builtin_amdgcn_sched_barrier(0);
-    // stage i landed, own reads of stage i - 1 done; behind the barrier, everybody's
-    __builtin_amdgcn_s_waitcnt(NDMA | (0x7 << 4));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(NEWER | (0x7 << 4));
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
-    dma(free, i + 2);
-
-    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Step i: stages now (i), next (i + 1) and free (i - 1, then i + 2).  The barrier is in the middle: it
+  // says that stage i + 1 has landed, whose first operands the second half reads, and that nobody reads
+  // stage i - 1 any more.
+  auto step = [&](const uint8_t* now, const uint8_t* next, uint8_t* free, int i) AWQ_INLINE {
     Operand<KIND> w[4];
     float d[4], z[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      w[q] = operand<KIND>(unpack_codes(*reinterpret_cast<const u32x4*>(now + (base + BOFF + (4 * wn + q) * 1024 + lane * 16))));
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(now + (base + SOFF + (4 * wn + q) * 64 + c * 4));
-      d[q] = h2f(v & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
-      z[q] = h2f(v >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
+      w[q] = operand<KIND>(unpack_codes(cw[q]));
+      d[q] = h2f(dn[q] & 0xffffu);
+      z[q] = d[q] * h2f(dn[q] >> 16);  // step times zero point
+      if (E4M3) d[q] *= 1.0f / kE4m3Unit;
       asm volatile("" : "+v"(d[q]), "+v"(z[q]));  // fp32 from here on: v_fmac_f32 in place
     }
+    // a token tile's multiply-adds run behind the next tile's products
+    f32x4 sx, r[4];
+    auto add = [&](int t) AWQ_INLINE {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = settled<KIND>(sx[e]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tot[t][q][e] = fmaf(d[q], settled<KIND>(r[q][e]), fmaf(-z[q], x, tot[t][q][e]));
+      }
+    };
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      const Operand<KIND> a = operand<KIND>(join(*reinterpret_cast<const u32x4*>(now + (a0 + t * 2048)),
-                                                 *reinterpret_cast<const u32x4*>(now + (a1 + t * 2048))));
-      const f32x4 sx = group_product<KIND>(a, ones);
-      f32x4 r[4];
+      const Operand<KIND> a = operand<KIND>(an);
+      if (t == TM / 2) {
+        sync(std::integral_constant<int, 0>{});
+        dma(free, i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (t + 1 < TM) {
+        read_a(now, t + 1);
+      } else {
+        read_a(next, 0);
+        read_w(next);
+      }
+      const f32x4 nx = group_product<KIND>(a, ones);
+      f32x4 nr[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) r[q] = group_product<KIND>(a, w[q]);
+      for (int q = 0; q < 4; ++q) nr[q] = group_product<KIND>(a, w[q]);
+      if (t > 0) add(t - 1);
+      sx = nx;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          tot[t][q][e] = fmaf(d[q], fmaf(-z[q], settled<KIND>(sx[e]), settled<KIND>(r[q][e])), tot[t][q][e]);
-      if (t % 2) __builtin_amdgcn_sched_barrier(0);  // two token tiles at a time keep the registers below 256
+      for (int q = 0; q < 4; ++q) r[q] = nr[q];
+      __builtin_amdgcn_sched_barrier(0);
     }
+    add(TM - 1);
+    __builtin_amdgcn_sched_barrier(0);
   };
+  sync(std::integral_constant<int, NDMA>{});
+  read_a(st0, 0);
+  read_w(st0);
   const int pairs = (n + 1) / 2;
   int i = 0;
   for (; i + 3 <= pairs; i += 3) {
-    step(st0, st2, i);
-    step(st1, st0, i + 1);
-    step(st2, st1, i + 2);
+    step(st0, st1, st2, i);
+    step(st1, st2, st0, i + 1);
+    step(st2, st0, st1, i + 2);
   }
-  if (i < pairs) step(st0, st2, i);
-  if (i + 1 < pairs) step(st1, st0, i + 1);
+  if (i < pairs) step(st0, st1, st2, i);
+  if (i + 1 < pairs) step(st1, st2, st0, i + 1);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt and lgkmcnt 0: no copy outlives the block
-  // the odd groups' sums through LDS to the even groups' waves: a tile's 16 values a lane, lane by lane
+  // each set gives the other the sums of half the token tiles through LDS (a tile's four values a lane, lane by
+  // lane) and finishes the other half
   __syncthreads();
-  static_assert(TM * 16384 <= 2 * 2 * STAGE && TM * 8192 <= 2 * STAGE, "two stage buffers hold the sums");
+  static_assert(TM * 8192 <= 2 * STAGE, "a stage buffer holds half the sums of one set");
+  auto slot = [&](uint8_t* st, int t, int q) AWQ_INLINE {
+    return reinterpret_cast<f32x4*>(st + ((t * 4 + wn) * 4 + q) * 1024 + lane * 16);
+  };
+  constexpr int H = TM / 2;
+  if (set == 0) {
 #pragma unroll
-  for (int t = 0; t < TM; ++t)
+    for (int t = 0; t < H; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f32x4* at = reinterpret_cast<f32x4*>((t < TM / 2 ? st0 : st1) + ((t % (TM / 2) * 4 + wn) * 4 + q) * 1024) + lane;
-      if (set == 1) *at = tot[t][q];
-    }
+      for (int q = 0; q < 4; ++q) *slot(st0, t, q) = tot[H + t][q];
+  } else {
+#pragma unroll
+    for (int t = 0; t < H; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *slot(st1, t, q) = tot[t][q];
+  }
   __syncthreads();
-  if (set == 1) return;
+  // (the even groups' sums first in both halves)
+  f32x4 fin[H][4];
 #pragma unroll
-  for (int t = 0; t < TM; ++t)
+  for (int t = 0; t < H; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      tot[t][q] += *(reinterpret_cast<const f32x4*>((t < TM / 2 ? st0 : st1) + ((t % (TM / 2) * 4 + wn) * 4 + q) * 1024) + lane);
+    for (int q = 0; q < 4; ++q) fin[t][q] = set == 0 ? tot[t][q] + *slot(st1, t, q) : *slot(st0, t, q) + tot[H + t][q];
+  const int r0 = 16 * H * set + 4 * j;  // this lane's first row
   const int64_t np = (int64_t)tiles * 16;
+  const bool part = splits > 1;
+  const int es = !part && p.ybf16 ? 2 : 4;
+  const int64_t ld = part ? np : p.ldy;
+  char* out = part ? reinterpret_cast<char*>(parts + ((int64_t)split * p.M + m0) * np) : static_cast<char*>(p.y) + m0 * p.ldy * es;
+  const int64_t cols = part ? np : p.N;
+  // the resource ends with the last row's last channel: rows past M are dropped there
+  const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(
+      out + (int64_t)tile0 * 16 * es, (short)0, (int)(((rows - 1) * ld + cols - tile0 * 16) * es), 0x00020000);
+  float xs[H][4];
+  const __amdgpu_buffer_rsrc_t mr =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.xscale + m0), (short)0, rows * 4, 0x00020000);
+#pragma unroll
+  for (int t = 0; t < H; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      xs[t][e] = part ? 1.0f : __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mr, (r0 + 16 * t + e) * 4, 0, 0));
+  const int ldb = (int)ld * es;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (4 * wn + q >= nt) continue;
-    const int64_t nn = (int64_t)(tile0 + 4 * wn + q) * 16 + c;
-    if (splits > 1) {
+    const int nc = (4 * wn + q) * 16 + c;
+    if (tile0 * 16 + nc < cols) {
+      const float pw = part ? 1.0f : p.powers[tile0 * 16 + nc];
 #pragma unroll
-      for (int t = 0; t < TM; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * t + 4 * j + e;
-          if (r < rows) parts[((int64_t)split * p.M + m0 + r) * np + nn] = tot[t][q][e];
-        }
-    } else if (nn < p.N) {
-      const float pw = p.powers[nn];
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
+      for (int t = 0; t < H; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * t + 4 * j + e;
-          if (r < rows) {
-            const float y = tot[t][q][e] * (p.xscale[m0 + r] * pw);
-            if (p.ybf16) static_cast<uint16_t*>(p.y)[(m0 + r) * p.ldy + nn] = to_bf16(y);
-            else static_cast<float*>(p.y)[(m0 + r) * p.ldy + nn] = y;
-          }
+          const float y = fin[t][q][e] * (xs[t][e] * pw);
+          const int yo = (r0 + 16 * t + e) * ldb + nc * es;
+          if (es == 2) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(y), yr, yo, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), yr, yo, 0, 0);
         }
     }
   }
@@ -828,7 +884,7 @@ struct Plan {
 };
 Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
   const int64_t G = K / kGroup, nt = (N + kTileN - 1) / kTileN;
-  Plan pl{kStream, 0, 1, 0};
+  Plan pl{kStream, 0, 1, (int)G};
   if (M <= 16) return pl;
   const int64_t t64 = (M + 63) / 64 * nt, t128 = (M + 127) / 128 * nt;
   if (t64 > 128) {
@@ -839,16 +895,30 @@ Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
     pl.tm = t128 >= 1024 || t128 * 6 >= (t128 + 511) / 512 * 512 * 5 ? 8 : 4;
     return pl;
   }
-  // few tiles: split (256 x 14336 -> 4096, 64 tiles: 37 us against 93 unsplit; at 128 tiles and more a split is
-  // one block per tile and loses to the tile kernel's two per CU: 41 against 33 at 224)
+  // Few tiles: split.  What a choice takes, in us, fitted to measurements at K = 4096 and 14336, 17 to 256
+  // tokens: 1.18 (32-token tiles) or 1.86 (64) per two groups of a block, and with more than one split the second
+  // kernel and its parts, written and read at 4 TB/s.  (101 x 4096 -> 6144: 18.4 us with 32-token tiles and two
+  // splits, 21.6 with 64 and five; 256 x 14336 -> 4096: 40.0 and two, 34.4 and four.  At more than 128 64-token
+  // tiles a split is one block per tile and loses to the tile kernel's two per CU.)
   pl.path = kSplit;
-  pl.tm = M <= 32 ? 2 : 4;
-  const int64_t tiles = (M + 16 * pl.tm - 1) / (16 * pl.tm) * nt;
-  int64_t s = 256 / tiles;
-  if (s > G / 2) s = G / 2;
-  if (s < 1) s = 1;
-  pl.per_split = (int)((G + s - 1) / s);
-  pl.splits = (int)((G + pl.per_split - 1) / pl.per_split);
+  float best = 0.0f;
+  for (int tm = 2; tm <= (M <= 32 ? 2 : 4); tm += 2) {
+    const int64_t tiles = (M + 16 * tm - 1) / (16 * tm) * nt;
+    int64_t most = 256 / tiles;
+    if (most > G / 2) most = G / 2;
+    if (most < 1) most = 1;
+    for (int64_t want = most; want >= 1; want /= 2) {
+      const int64_t per = (G + want - 1) / want, splits = (G + per - 1) / per;
+      float us = (float)((per + 1) / 2) * (tm == 2 ? 1.18f : 1.86f);
+      if (splits > 1) us += 2.5f + (float)(splits * M * N) * 2e-6f;
+      if (pl.tm == 0 || us < best) {
+        best = us;
+        pl.tm = tm;
+        pl.per_split = (int)per;
+        pl.splits = (int)splits;
+      }
+    }
+  }
   return pl;
 }
 
