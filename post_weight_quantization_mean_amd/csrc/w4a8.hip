@@ -276,11 +276,13 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
 }
 
 template <int KIND>
-hipError_t launch_stream(const W4a8Args& a, hipStream_t st) {
+hipError_t launch_stream(const W4a8Args& a, int tt, hipStream_t st) {
   const int64_t tiles = w4a8_tiles(a.N);
+  const unsigned pairs = (unsigned)((tiles + 1) / 2);
   // two channel tiles per block halve the reads of X where that still leaves more blocks than CUs
   // (16 tokens x 4096 -> 28672: 15.0 us against 20.4; 5 x 14336 -> 4096: 10.6 against 8.8)
-  if (tiles >= 320) w4a8_stream_kernel<KIND, 1, 2, 8, 2><<<(unsigned)((tiles + 1) / 2), 512, 0, st>>>(a);
+  if (tt == 2) w4a8_stream_kernel<KIND, 2, 2, 8, 1><<<dim3(pairs, (unsigned)((a.M + 31) / 32)), 512, 0, st>>>(a);
+  else if (tiles >= 320) w4a8_stream_kernel<KIND, 1, 2, 8, 2><<<pairs, 512, 0, st>>>(a);
   else w4a8_stream_kernel<KIND, 1, 1, 16, 2><<<(unsigned)tiles, 1024, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -879,46 +881,55 @@ int64_t padded_groups(int64_t K) { return (K / kGroup + 7) / 8 * 8; }
 constexpr int kStream = 0, kSplit = 1, kTile = 2;
 struct Plan {
   int path;
-  int tm;               // token tiles of 16 per block (split, tile)
+  int tm;               // token tiles of 16 per block
   int splits, per_split;  // split: blocks and groups per tile
 };
+// The costs are microseconds fitted to measurements (int8 and e4m3, K = 4096 and 14336, N = 4096 to 28672, 17 to
+// 640 tokens, weights from memory); what each path measured at the crossovers stands behind its line.
 Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
   const int64_t G = K / kGroup, nt = (N + kTileN - 1) / kTileN;
-  Plan pl{kStream, 0, 1, (int)G};
+  Plan pl{kStream, 1, 1, (int)G};
   if (M <= 16) return pl;
   const int64_t t64 = (M + 63) / 64 * nt, t128 = (M + 127) / 128 * nt;
+  float best;
   if (t64 > 128) {
-    // 128-token tiles do a token's work in 0.77 of the time but leave whole rounds of 512 blocks (two per CU)
-    // emptier: they run where the last round is five sixths full or there are many (K = 4096, e4m3, us, 64- against
-    // 128-token tiles: 448 of the latter 73 / 68, 384 66 / 68, 560 98 / 103, 896 135 / 132)
+    // Tiles.  128-token tiles do a token's work in 0.77 of the time but leave whole rounds of 512 blocks (two per
+    // CU) emptier: they run where the last round is five sixths full or there are many (K = 4096, e4m3, us,
+    // 64- against 128-token tiles: 448 of the latter 73 / 68, 384 66 / 68, 560 98 / 103, 896 135 / 132).
     pl.path = kTile;
     pl.tm = t128 >= 1024 || t128 * 6 >= (t128 + 511) / 512 * 512 * 5 ? 8 : 4;
-    return pl;
-  }
-  // Few tiles: split.  What a choice takes, in us, fitted to measurements at K = 4096 and 14336, 17 to 256
-  // tokens: 1.18 (32-token tiles) or 1.86 (64) per two groups of a block, and with more than one split the second
-  // kernel and its parts, written and read at 4 TB/s.  (101 x 4096 -> 6144: 18.4 us with 32-token tiles and two
-  // splits, 21.6 with 64 and five; 256 x 14336 -> 4096: 40.0 and two, 34.4 and four.  At more than 128 64-token
-  // tiles a split is one block per tile and loses to the tile kernel's two per CU.)
-  pl.path = kSplit;
-  float best = 0.0f;
-  for (int tm = 2; tm <= (M <= 32 ? 2 : 4); tm += 2) {
-    const int64_t tiles = (M + 16 * tm - 1) / (16 * tm) * nt;
-    int64_t most = 256 / tiles;
-    if (most > G / 2) most = G / 2;
-    if (most < 1) most = 1;
-    for (int64_t want = most; want >= 1; want /= 2) {
-      const int64_t per = (G + want - 1) / want, splits = (G + per - 1) / per;
-      float us = (float)((per + 1) / 2) * (tm == 2 ? 1.18f : 1.86f);
-      if (splits > 1) us += 2.5f + (float)(splits * M * N) * 2e-6f;
-      if (pl.tm == 0 || us < best) {
-        best = us;
-        pl.tm = tm;
-        pl.per_split = (int)per;
-        pl.splits = (int)splits;
+    best = 3.0f + 0.95f * (float)G * (t64 <= 256 ? 1.0f : 1.4f * (float)t64 / 512.0f);
+  } else {
+    // Few tiles: split.  Per two groups of a block 1.18 (32-token tiles) or 1.86 (64); with more than one split the
+    // second kernel, and the parts written and read at 4 TB/s.  (101 x 4096 -> 6144: 18.4 us with 32-token tiles and
+    // two splits, 21.6 with 64 and five; 256 x 14336 -> 4096: 40.0 and two, 34.4 and four.  At more than 128
+    // 64-token tiles a split is one block per tile and loses to the tile kernel's two per CU: 41 / 33 at 224.)
+    pl.path = kSplit;
+    pl.tm = 0;
+    best = 0.0f;
+    for (int tm = 2; tm <= (M <= 32 ? 2 : 4); tm += 2) {
+      const int64_t tiles = (M + 16 * tm - 1) / (16 * tm) * nt;
+      int64_t most = 256 / tiles;
+      if (most > G / 2) most = G / 2;
+      if (most < 1) most = 1;
+      for (int64_t want = most; want >= 1; want /= 2) {
+        const int64_t per = (G + want - 1) / want, splits = (G + per - 1) / per;
+        float us = 5.0f + (float)((per + 1) / 2) * (tm == 2 ? 1.18f : 1.86f);
+        if (splits > 1) us += 2.5f + (float)(splits * M * N) * 2e-6f;
+        if (pl.tm == 0 || us < best) {
+          best = us;
+          pl.tm = tm;
+          pl.per_split = (int)per;
+          pl.splits = (int)splits;
+        }
       }
     }
   }
+  // The stream, 32 tokens and 32 channels per block (32 x 4096 -> 6144: 7.6 us against 14.7 split; 64 tokens 12.3
+  // against 16.7; 64 x 4096 -> 28672: 37 against 25.7).
+  const float blocks = (float)((N + 31) / 32) * (float)((M + 31) / 32);
+  if (M <= 256 && 3.2f + 0.134f * (float)G * (blocks <= 256.0f ? 1.0f : 1.15f * blocks / 256.0f) < best)
+    pl = Plan{kStream, 2, 1, (int)G};
   return pl;
 }
 
@@ -948,7 +959,7 @@ hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
 template <int KIND>
 hipError_t launch_kind(const W4a8Args& a, void* ws, hipStream_t st) {
   const Plan pl = w4a8_plan(a.M, a.K, a.N);
-  if (pl.path == kStream) return launch_stream<KIND>(a, st);
+  if (pl.path == kStream) return launch_stream<KIND>(a, pl.tm, st);
   if (pl.path == kSplit) {
     float* parts = static_cast<float*>(ws);
     return pl.tm == 2 ? launch_split<KIND, 2>(a, pl, parts, st) : launch_split<KIND, 4>(a, pl, parts, st);
