@@ -56,7 +56,9 @@ AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_
  *          (not checked here: the search and the pack did)
  *   Y, y_dtype, ldy, scale   as awq_rmsnorm
  * With act NONE and neither U nor s this quantizes given activations.  y is formed in fp32,
- * within a few fp32 ulps of the exact value.  Any K.  Y may be G or U where it has their type
+ * with a relative error of at most, in units of 2^-24: NONE 8; SILU 18, and |x| more where Y is not
+ * F32; GELU 28 + 2 x^2 (its tail is that ill-conditioned; a result below 2^-126 may be 0).
+ * Any K.  Y may be G or U where it has their type
  * and row stride, and overlaps them in no other way.
  * ------------------------------------------------------------------------------------- */
 AWQ_API int awq_act_mul(const void* G, int x_dtype, int64_t M, int64_t K, int64_t ldg, const void* U,
@@ -86,8 +88,10 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  * The W4A8 product:
  *   Y[m, n] = xscale[m] * sum_g scales[n, g] * sum_{k in g} Xq[m, k] (q[n, k] - zeros[n, g])
  * on the 8-bit matrix cores: a code q is an int8 byte as it stands, and as an e4m3 byte it is
- * exactly q 2^-9.  I8: the inner sums are exact integers; E4M3: exact products, fp32 sums.  The
- * steps and the sum over groups are fp32; Y is rounded once.
+ * exactly q 2^-9.  I8: the inner sums are exact integers.  E4M3: the products are exact; for an F32 Y
+ * they are summed in fp32, for a BF16 Y sixteen at a time to 14 bits of the largest of them (the matrix
+ * unit's own sum: at most 2^-9 of the sum of their magnitudes, 2^-13 and less as a rule) and
+ * then in fp32.  The steps and the sum over groups are fp32; Y is rounded once.
  *   Xq      [M, K] of x_dtype I8 or E4M3, row stride ldx, 16-byte aligned rows
  *   xscale  fp32 [M]
  *   wt      as written by awq_w4a8_weight for the same N and K
@@ -95,7 +99,7 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each
- * K is a multiple of 128; 256 rows of Xq and of Y span less than 2^31 bytes each (AWQ_ERR_SHAPE).
+ * K is a multiple of 128; 128 rows of Xq and of Y span less than 2^31 bytes each (AWQ_ERR_SHAPE).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_w4a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M, int64_t K, int64_t ldx,

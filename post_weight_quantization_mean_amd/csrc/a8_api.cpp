@@ -153,7 +153,7 @@ AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M
   if (st == AWQ_OK) st = check_rows(Y, y_dtype, M, N, ldy);
   if (st != AWQ_OK) return st;
   if (!rows_aligned(Xq, x_dtype, ldx, 16) || !aligned(xscale, 4) || !aligned(wt, kAlign)) return AWQ_ERR_INVALID_ARG;
-  // tiles of up to 256 tokens use 32-bit offsets within their rows of Xq and of Y
+  // tiles of up to 128 tokens use 32-bit offsets within their rows of Xq and of Y
   const int64_t xspan = mul3(awq::kW4a8TileM, ldx, 1), yspan = mul3(awq::kW4a8TileM, ldy, dsize(y_dtype));
   if (xspan < 0 || xspan >= (int64_t)INT32_MAX || yspan < 0 || yspan >= (int64_t)INT32_MAX) return AWQ_ERR_SHAPE;
   const size_t need = awq_w4a8_workspace_bytes(M, K, N);

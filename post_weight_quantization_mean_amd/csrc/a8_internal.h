@@ -44,7 +44,7 @@ struct W4a8Args {
 };
 hipError_t launch_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros, int64_t N,
                               int64_t K, uint32_t* codes, uint32_t* steps, float* powers, hipStream_t st);
-constexpr int kW4a8TileM = 256;  // tokens of the largest tile
+constexpr int kW4a8TileM = 128;  // tokens of the largest tile
 size_t w4a8_workspace(int64_t M, int64_t K, int64_t N);
 hipError_t launch_w4a8(const W4a8Args& a, void* ws, hipStream_t st);
 

@@ -7,7 +7,9 @@
 // the subnormals b 2^-9 and the first normal binade, which continues them) exactly q 2^-9.  A word of eight
 // codes becomes two operand words with three instructions.  The zero point is taken out of the sums:
 //   sum x (q - z) = sum x q - z sum x.
-// int8 sums are exact integers below 2^18; e4m3 products are exact in fp32 and their sums round as fp32's.
+// int8 sums are exact integers below 2^18; e4m3 products are exact, their sums as kE4m3Fast and kE4m3Wide say.
+// A result is (sum 2^e) xscale: the first product is exact (e in -35 .. 6 and |sum| far from both ends), so a row
+// whose scale is at either end of fp32 loses nothing.
 //
 // The weight is laid out once (awq_w4a8_weight): the 16 bytes of lane l for one tile of 16 channels and one
 // group are contiguous over the lanes, so a tile's group is one 1 KiB load of a wave, in operand order.
@@ -99,7 +101,7 @@ constexpr float kE4m3Unit = 0x1p-9f;  // an e4m3 byte b < 16 is b times this
 // How a group's products are formed.  The e4m3 matrix instruction adds 16 products at a time after
 // shifting them to the largest one's exponent and keeps 14 bits there (measured; the sums of 16 then add in
 // fp32): about 2^-13 of the largest product, well below a bf16 result's half step but not an fp32 one's.
-// kE4m3 is taken for bf16 results; kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32,
+// kE4m3Fast is taken for bf16 results; kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32,
 // at half the matrix rate, for fp32 results.
 constexpr int kInt8 = 0, kE4m3Fast = 1, kE4m3Wide = 2;
 
@@ -131,28 +133,41 @@ __device__ __forceinline__ Operand<KIND> operand(const i32x8 b) {
 }
 
 // One group's products of 16 tokens and 16 channels: lane l gets channel l % 16 of tokens 4 (l / 16) + i,
-// as settled<KIND>(r[i]) (int8: exact integers; e4m3: times 2^-9 with codes as b).
+// as settled<KIND>(r[i]) (int8: exact integers; e4m3: times 2^-9 with codes as b).  In two parts, the second of
+// which continues the first's sums (kE4m3Fast: all in the first).
 template <int KIND>
-__device__ __forceinline__ f32x4 group_product(const Operand<KIND>& a, const Operand<KIND>& b) {
+__device__ __forceinline__ f32x4 product_begin(const Operand<KIND>& a, const Operand<KIND>& b) {
   const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (KIND == kE4m3Fast) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.b, b.b, z, 0, 0, 0, 0, 0, 0);
   } else if constexpr (KIND == kE4m3Wide) {
-    f32x4 r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[0], b.h[0], z, 0, 0, 0);
-#pragma unroll
-    for (int s = 1; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[s], b.h[s], r, 0, 0, 0);
-    return r;
+    const f32x4 r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[0], b.h[0], z, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[1], b.h[1], r, 0, 0, 0);
   } else {
     // the sums start at the bits of 1.5 2^23: |sum| < 2^22 more is that float plus the sum, so that a
     // full-rate subtraction stands for the conversion
     constexpr int kBits = 0x4b400000;
     const i32x4 zi = {kBits, kBits, kBits, kBits};
-    const i32x4 alo = __builtin_shufflevector(a.b, a.b, 0, 1, 2, 3), ahi = __builtin_shufflevector(a.b, a.b, 4, 5, 6, 7);
-    const i32x4 blo = __builtin_shufflevector(b.b, b.b, 0, 1, 2, 3), bhi = __builtin_shufflevector(b.b, b.b, 4, 5, 6, 7);
-    i32x4 r = __builtin_amdgcn_mfma_i32_16x16x64_i8(alo, blo, zi, 0, 0, 0);
-    r = __builtin_amdgcn_mfma_i32_16x16x64_i8(ahi, bhi, r, 0, 0, 0);
-    return __builtin_bit_cast(f32x4, r);
+    const i32x4 alo = __builtin_shufflevector(a.b, a.b, 0, 1, 2, 3), blo = __builtin_shufflevector(b.b, b.b, 0, 1, 2, 3);
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(alo, blo, zi, 0, 0, 0));
   }
+}
+template <int KIND>
+__device__ __forceinline__ f32x4 product_end(const Operand<KIND>& a, const Operand<KIND>& b, const f32x4 r) {
+  if constexpr (KIND == kE4m3Fast) {
+    return r;
+  } else if constexpr (KIND == kE4m3Wide) {
+    const f32x4 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[2], b.h[2], r, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[3], b.h[3], s, 0, 0, 0);
+  } else {
+    const i32x4 ahi = __builtin_shufflevector(a.b, a.b, 4, 5, 6, 7), bhi = __builtin_shufflevector(b.b, b.b, 4, 5, 6, 7);
+    return __builtin_bit_cast(
+        f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(ahi, bhi, __builtin_bit_cast(i32x4, r), 0, 0, 0));
+  }
+}
+template <int KIND>
+__device__ __forceinline__ f32x4 group_product(const Operand<KIND>& a, const Operand<KIND>& b) {
+  return product_end<KIND>(a, b, product_begin<KIND>(a, b));
 }
 template <int KIND>
 __device__ __forceinline__ float settled(float r) { return KIND == kInt8 ? r - 12582912.0f : r; }
@@ -267,7 +282,7 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
 #pragma unroll
       for (int w = 0; w < WV; ++w) s += part[w][o];
       if (m < p.M && nn < p.N) {
-        const float y = s * (p.xscale[m] * p.powers[nn]);
+        const float y = s * p.powers[nn] * p.xscale[m];
         if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + nn] = to_bf16(y);
         else static_cast<float*>(p.y)[m * p.ldy + nn] = y;
       }
@@ -322,10 +337,10 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
   }
 }
 
-// A block of eight waves, two per SIMD, computes 32 TM tokens x 256 channels; wave (wm, wn) of 2 x 4 has
-// 16 TM tokens x 64 channels and takes one group a step.  The tokens' bytes (128 per row and group) and the
-// groups' steps come into LDS by DMA in four stages; the codes, which only two waves share, come
-// straight into registers in operand order, a group ahead.  The barrier of step g says that stages g
+// A block of four waves, one per SIMD, computes 16 TM tokens x 256 channels, and two blocks share a CU; wave wn has
+// all the tokens and 64 of the channels and takes one group a step.  The tokens' bytes (128 per row and group)
+// and the groups' steps come into LDS by DMA in four stages; the codes, which no other wave of the block needs,
+// come straight into registers in operand order, a group ahead.  The barrier of step g says that stages g
 // and g + 1 have landed, so that the last products of a step run beside the reads for the first ones of
 // the next; stage g + 2 is under way and g + 3 is requested.
 // Rows of 128 bytes hold their 16-byte pieces at piece ^ (row % 8) ^ (row / 8 % 2): the reads of sixteen
@@ -337,6 +352,12 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 // again; their sum over groups is a product of its own, sum_g sums[m, g] (D z)[n, g], and runs on the matrix
 // cores in fp16 with both operands as high and low parts (sums 22 bits, D z 15: exact), one
 // instruction of 16 cycles for eight groups.
+//
+// 4096 x 4096 -> 28672: e4m3 436 us (2.2 PFLOP/s), int8 480 (2.0).  A loop of nothing but such products and
+// multiply-adds runs at 4.0 (e4m3) and 2.9 (int8), a library product without steps at 3.1 and 2.55.  The clock is
+// down to 1.7 .. 2.0 GHz under this load; per cycle the matrix unit is busy 0.55, and without any copies or loads
+// 0.62: neither barriers nor LDS reads nor unpacking bound it (each left out alone: no change), but the
+// products' own latency beside their multiply-adds at two waves per SIMD.
 constexpr int kTileN = 256;
 template <int TM>
 constexpr int kTileStage = 16 * TM * 128 + 1024;
@@ -396,8 +417,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
                                                (int)xoff[i], g * 128, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (AWQ_LDS_A8 void*)(st + SOFF + wn * 256), 4, (int)soff, g * 64, 0, 0);
   };
-  u32x4 cw0[4], cw1[4];  // the codes of the next two steps, by parity
-  auto load_codes = [&](u32x4* cw, int g) AWQ_INLINE {
+  u32x4 cw[4];  // the codes of the next step
+  auto load_codes = [&](int g) AWQ_INLINE {
     g = g < G ? g : G - 1;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -463,8 +484,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
     z0 = z1;
     load_zero(z1, b + 2);
   }
-  load_codes(cw0, 0);
-  load_codes(cw1, 1);
+  load_codes(0);
   // this lane's pieces of row c of a token tile (tiles are 16 rows: the same swizzle in each)
   const int a0 = c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
   const int a1 = c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
@@ -482,13 +502,13 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   auto sync = [&] () AWQ_INLINE {
     __builtin_amdgcn_sched_barrier(0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt((NDMA + 4) | (0x7 << 4) | (0xf << 8));  // vmcnt; no wait for LDS and exports
+    __builtin_amdgcn_s_waitcnt(NDMA | (0x7 << 4) | (0xf << 8));  // vmcnt; no wait for LDS and exports
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
   };
   // Step g: stages now (g), next (g + 1) and free (g - 1, then g + 3).
-  auto step = [&](int g, u32x4* cw, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
+  auto step = [&](int g, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
     Operand<KIND> w[4];
     float d[4];
 #pragma unroll
@@ -498,44 +518,51 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
       asm volatile("" : "+v"(d[q]));  // fp32 from here on: v_fmac_f32 in place, not v_fma_mix_f32 from fp16
     }
     sync();
-    load_codes(cw, g + 2);
+    load_codes(g + 1);
     __builtin_amdgcn_sched_barrier(0);
     dma(free, g + 3);
     __builtin_amdgcn_sched_barrier(0);
-    // two products at a time; their multiply-adds run behind the next two
-    f32x4 s[2];
-    auto add = [&](int u) AWQ_INLINE {
+    // a token tile's multiply-adds run between the next tile's products, so that no product is waited for
+    f32x4 s[4];
+    auto add = [&](int t, int q) AWQ_INLINE {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tot[u / 2][2 * (u % 2) + h][i] = fmaf(d[2 * (u % 2) + h], settled<KIND>(s[h][i]), tot[u / 2][2 * (u % 2) + h][i]);
+      for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d[q], settled<KIND>(s[q][i]), tot[t][q][i]);
     };
-    Operand<KIND> a;
 #pragma unroll
-    for (int u = 0; u < 2 * TM; ++u) {
-      const int t = u / 2;
-      if (u % 2 == 0) {
-        a = operand<KIND>(an);
-        if (t + 1 < TM) {
-          read_a(now, t + 1);
-        } else {
-          read_a(next, 0);
-          read_d(next);
+    for (int t = 0; t < TM; ++t) {
+      const Operand<KIND> a = operand<KIND>(an);
+      f32x4 r[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        r[q] = product_begin<KIND>(a, w[q]);
+        if (q == 0) {
+          if (t + 1 < TM) {
+            read_a(now, t + 1);
+          } else {
+            read_a(next, 0);
+            read_d(next);
+          }
+        }
+        if (t > 0 && (KIND == kE4m3Fast || q < 2)) add(t - 1, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (KIND != kE4m3Fast) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          r[q] = product_end<KIND>(a, w[q], r[q]);
+          if (t > 0 && q < 2) add(t - 1, 2 + q);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      f32x4 r[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) r[h] = group_product<KIND>(a, w[2 * (u % 2) + h]);
-      if (u > 0) add(u - 1);
-      s[0] = r[0], s[1] = r[1];
-      __builtin_amdgcn_sched_barrier(0);
+      for (int q = 0; q < 4; ++q) s[q] = r[q];
     }
-    add(2 * TM - 1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) add(TM - 1, q);
   };
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  constexpr int NEWER0 = 2 * NDMA + 8;
+  constexpr int NEWER0 = 2 * NDMA + 4;
   __builtin_amdgcn_s_waitcnt((NEWER0 & 15) | ((NEWER0 >> 4) << 14) | (0x7 << 4) | (0xf << 8));  // stage 0
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -544,17 +571,17 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   read_d(st0);
   int g = 0;
   for (; g + 4 <= G; g += 4) {
-    step(g, cw0, st0, st1, st3);
-    step(g + 1, cw1, st1, st2, st0);
-    step(g + 2, cw0, st2, st3, st1);
-    step(g + 3, cw1, st3, st0, st2);
+    step(g, st0, st1, st3);
+    step(g + 1, st1, st2, st0);
+    step(g + 2, st2, st3, st1);
+    step(g + 3, st3, st0, st2);
   }
-  if (g < G) step(g, cw0, st0, st1, st3);
-  if (g + 1 < G) step(g + 1, cw1, st1, st2, st0);
-  if (g + 2 < G) step(g + 2, cw0, st2, st3, st1);
+  if (g < G) step(g, st0, st1, st3);
+  if (g + 1 < G) step(g + 1, st1, st2, st0);
+  if (g + 2 < G) step(g + 2, st2, st3, st1);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt and lgkmcnt 0: no copy or load outlives the block
   // stores through a resource that ends with the last row's last channel: rows past M are dropped there,
-  // channels past N by the lane mask (256 rows of Y span less than 2^31 bytes: host-checked)
+  // channels past N by the lane mask (128 rows of Y span less than 2^31 bytes: host-checked)
   const int n0 = tile0 * 16;
   const int es = p.ybf16 ? 2 : 4;
   const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(
@@ -563,20 +590,20 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   const __amdgpu_buffer_rsrc_t mr =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.xscale + m0), (short)0, rows * 4, 0x00020000);
   const int ldyb = (int)p.ldy * es;
-#pragma unroll
-  for (int t = 0; t < TM; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float xs = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mr, (16 * t + 4 * j + i) * 4, 0, 0));  // 0 past M
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tot[t][q][i] *= xs;
-    }
   float pw[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int n = n0 + (4 * wn + q) * 16 + c;
     pw[q] = p.powers[n < tiles * 16 ? n : tiles * 16 - 1];
   }
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float xs = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(mr, (16 * t + 4 * j + i) * 4, 0, 0));  // 0 past M
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tot[t][q][i] = tot[t][q][i] * pw[q] * xs;
+    }
   if (p.ybf16) {
     // through LDS, so that a wave stores whole rows of 256 channels (written from the products' layout,
     // a store would fill 32 bytes of a line); rows of 528 bytes keep the writes free of bank conflicts
@@ -591,7 +618,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint16_t*>(pool[16 * t / RPS] + (16 * t % RPS + 4 * j + i) * ROW + (64 * wn + 16 * q + c) * 2) =
-              to_bf16(tot[t][q][i] * pw[q]);
+              to_bf16(tot[t][q][i]);
     __syncthreads();
     // 32 lanes a row; 16-byte stores where every row of Y starts at a multiple of 16 bytes
     const int cb = (lane & 31) * 8;
@@ -620,7 +647,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
         for (int t = 0; t < TM; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i] * pw[q]), yr, yo + (16 * t + i) * ldyb, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tot[t][q][i]), yr, yo + (16 * t + i) * ldyb, 0, 0);
       }
     }
   }
@@ -846,7 +873,7 @@ __global__ __launch_bounds__(512, 2) void w4a8_split_kernel(const W4a8Args p, fl
       for (int t = 0; t < H; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = fin[t][q][e] * (xs[t][e] * pw);
+          const float y = fin[t][q][e] * pw * xs[t][e];
           const int yo = (r0 + 16 * t + e) * ldb + nc * es;
           if (es == 2) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(y), yr, yo, 0, 0);
           else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), yr, yo, 0, 0);
@@ -869,7 +896,7 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(const W4a8Args p, const 
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (n + e < p.N) {
-      const float y = s[e] * (xs * pw[e]);
+      const float y = s[e] * pw[e] * xs;
       if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n + e] = to_bf16(y);
       else static_cast<float*>(p.y)[m * p.ldy + n + e] = y;
     }

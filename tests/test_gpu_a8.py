@@ -315,6 +315,132 @@ def test_w4a8_scale_nan_stays_in_its_row(awq, M):
     check_product(Y.cpu()[keep], q[keep], sc[keep], art)
 
 
+def check_tile(Y, q, sc, art):
+    """check_product for a bf16 result of e4m3 codes also where few groups leave little to cancel.  The matrix
+    unit shifts sixteen products to the largest one's exponent and keeps 14 bits there: each loses at most 2^-13
+    of the largest, the sixteen together 2^-9 of it, which is at most 2^-9 of the sum of their magnitudes."""
+    if q.dtype != E4M3 or Y.dtype != BF16:
+        return check_product(Y, q, sc, art)
+    want, mag, absmag = a8.w4a8(f64(q), f64(sc), art)
+    G = q.shape[1] // 128
+    lim = (2 * G + 16) * U * mag + (HALF[BF16] + 4 * U) * np.abs(want) + (2.0 ** -9 + 136 * U) * absmag + 1e-36
+    assert np.all(np.abs(f64(Y) - want) <= lim)
+
+
+# More than 128 tiles of 64 tokens x 256 channels run as whole tiles.  64-token tiles: one and two column tiles, groups
+# 1 .. 17 (a multiple of four and each remainder); 128-token tiles, by the last round of 512 blocks: 435 and 1029.
+TILE_SHAPES = [(8257, 128, 40), (8200, 1152, 17), (4100, 1280, 300), (16391, 256, 16), (8321, 1408, 33),
+               (8200, 2176, 1), (18521, 384, 520), (131700, 128, 5), (55553, 640, 24)]
+
+
+@pytest.mark.parametrize("M,K,N", TILE_SHAPES)
+@pytest.mark.parametrize("xt,yt", [(I8, F32), (I8, BF16), (E4M3, F32), (E4M3, BF16)])
+def test_w4a8_tiles(awq, M, K, N, xt, yt):
+    banner(f"w4a8 tiles M={M} K={K} N={N} {xt} {yt}")
+    art = artefact(N, K, 60)
+    q, sc = codes(M, K, xt, 61)
+    Y = torch.full((M + 2, N), -7.0, dtype=yt, device=DEV)
+    awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), out=Y[:M])
+    check_tile(Y[:M], q, sc, art)
+    assert torch.all(Y[M:] == -7.0)
+
+
+@pytest.mark.parametrize("M,N", [(8250, 200), (18521, 516)])
+@pytest.mark.parametrize("pad,first", [(40, 0), (44, 0), (43, 1)])
+@pytest.mark.parametrize("xt", [I8, E4M3])
+def test_w4a8_tiles_strided(awq, M, N, pad, first, xt):
+    """bf16 rows that start at multiples of 16, 8 and 2 bytes; nothing outside Y's view is written."""
+    K = 256
+    art = artefact(N, K, 62)
+    q, sc = codes(M, K, xt, 63)
+    full = torch.zeros((M, K + 48), dtype=xt, device=DEV)
+    full[:, :K] = q.to(DEV)
+    Y = torch.full((M + 3, first + N + pad), -7.0, dtype=BF16, device=DEV)
+    awq.w4a8(awq.Act8(full[:, :K], sc.to(DEV)), on_gpu(awq, art), out=Y[:M, first:first + N])
+    check_tile(Y[:M, first:first + N], q, sc, art)
+    assert torch.all(Y[:, :first] == -7.0) and torch.all(Y[:, first + N:] == -7.0) and torch.all(Y[M:] == -7.0)
+
+
+def test_w4a8_tiles_steps_over_the_whole_range(awq):
+    """Zero points and steps as in the extremes above where the zero points' part is a product of its own."""
+    M, K, N = 8260, 1024, 48
+    rng = np.random.default_rng(64)
+    G = K // 128
+    scales = np.exp2(rng.uniform(-24, 15.9, (N, G))).astype(np.float16)
+    scales[0], scales[1], scales[2] = 2.0 ** -24, 65504, 0
+    art = dict(qweight=rng.integers(0, 2 ** 32, (N, K // 8), dtype=np.uint64).astype(np.uint32).view(np.int32),
+               scales=scales, zeros=rng.choice([0.0, 15.0], (N, G)).astype(np.float16))
+    art["qweight"][3] = -1
+    q, sc = codes(M, K, I8, 65)
+    q[0], q[1] = 127, -127
+    w = awq.w4a8_weight(*[torch.from_numpy(art[k]).to(DEV) for k in ("qweight", "scales", "zeros")])
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), w)
+    want, mag, _ = a8.w4a8(f64(q), f64(sc), art)
+    ones = dict(art, scales=np.ones_like(scales))
+    # steps below 2^-25 of their channel's largest lose bits; the zero points' high and low parts likewise, once more
+    loss = a8.w4a8(f64(q), f64(sc), ones)[2] * (np.max(scales.astype(np.float64), axis=1) * 2.0 ** -34)[None, :]
+    assert np.all(np.abs(f64(Y) - want) <= (2 * G + 16) * U * mag + 5 * U * np.abs(want) + loss + 1e-36)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300, 8260])
+@pytest.mark.parametrize("e", [-107, 80])
+@pytest.mark.parametrize("step", [-24, 14])
+def test_w4a8_row_scales_at_both_ends(awq, M, e, step):
+    """The smallest scale that a producer writes, and a large one, with the smallest and large steps: no product of
+    scale and step on the way leaves fp32's normal range while the result is inside."""
+    K, N = 256, 32
+    art = artefact(N, K, 66)
+    art["scales"] = np.full((N, K // 128), 2.0 ** step, np.float16)
+    q, sc = codes(M, K, I8, 67)
+    sc = sc * 0 + 1.25 * 2.0 ** e
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art))
+    want, mag, _ = a8.w4a8(f64(q), f64(sc), art)
+    lim = (2 * (K // 128) + 16) * U * mag + 5 * U * np.abs(want) + 2.0 ** -148
+    assert np.all(np.abs(f64(Y) - want) <= lim)
+
+
+def test_w4a8_not_finite_codes_stay_in_their_row(awq):
+    """A row of e4m3 NaN codes, as a row that was not finite leaves them: its outputs only."""
+    for M in (5, 40, 300, 8260):
+        art = artefact(32, 256, 68)
+        q, sc = codes(M, 256, E4M3, 69)
+        good = q.clone()
+        q.view(torch.uint8)[M - 3] = 0x7F
+        sc[M - 3] = float("nan")
+        for yt in (F32, BF16):
+            Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), dtype=yt)
+            assert torch.all(Y[M - 3].isnan())
+            keep = torch.arange(M) != M - 3
+            check_tile(Y.cpu()[keep], good[keep], sc[keep], art)
+
+
+@pytest.mark.parametrize("M,N", [(40, 48), (300, 300), (8260, 20), (18521, 516)])
+@pytest.mark.parametrize("xt,yt", [(I8, F32), (E4M3, BF16)])
+def test_w4a8_is_the_same_in_every_call(awq, M, N, xt, yt):
+    """On every path, eager and replayed from two graphs that share a workspace in one stream's order."""
+    K = 640
+    w = on_gpu(awq, artefact(N, K, 70))
+    q, sc = codes(M, K, xt, 71)
+    a = awq.Act8(q.to(DEV), sc.to(DEV))
+    want = awq.w4a8(a, w, dtype=yt)
+    ws = torch.full((max(awq.w4a8_workspace_bytes(M, K, N), 16),), 255, dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(want) for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, y in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            awq.w4a8(a, w, out=y, workspace=ws)
+    for _ in range(3):
+        for y in outs:
+            y.zero_()
+        for g in graphs:
+            g.replay()
+        ws.fill_(255)
+        assert torch.equal(awq.w4a8(a, w, dtype=yt, workspace=ws), want)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 def test_w4a8_agrees_with_w4a16(awq):
     """The same artefact and activations through both products: 8-bit activations put at most half a step
     per channel on top of the 16-bit product's own error."""
