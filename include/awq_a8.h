@@ -71,8 +71,8 @@ AWQ_API int awq_act_mul(const void* G, int x_dtype, int64_t M, int64_t K, int64_
  *   wt     device memory of at least awq_w4a8_weight_bytes(N, K) bytes, 256-byte aligned, in three
  *          parts, each starting at a multiple of 256 bytes:
  *            codes  for column tile c (channels n = 16 c + l % 16) and group g, 16 bytes per
- *                   l < 64: the codes of k = 128 g + 32 (l / 16) .. + 31, four words of eight;
- *                   byte b of a word holds code b (low nibble) and code b + 4 (high nibble)
+ *                   l < 64: the codes of k = 128 g + 16 (l / 16) .. + 15 and 64 further on, four
+ *                   words of eight; byte b of a word holds code b (low nibble) and b + 4 (high)
  *            steps  uint32 [tiles][K/128][16]: fp16 scales * 2^-e (low half), fp16 zeros (high)
  *            powers fp32 [16 tiles]: 2^e, e per channel such that its largest step lies in
  *                   [2^10, 2^11)

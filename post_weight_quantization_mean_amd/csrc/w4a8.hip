@@ -13,7 +13,9 @@
 //
 // The weight is laid out once (awq_w4a8_weight): the 16 bytes of lane l for one tile of 16 channels and one
 // group are contiguous over the lanes, so a tile's group is one 1 KiB load of a wave, in operand order.
-// Within a lane's 32 channels the sum over k runs in the order of the bytes, the same for both operands.
+// Lane l's 32 channels of a group are 16 (l / 16) .. + 15 and the same 64 further on, for both operands: one read of
+// 16 bytes by the lanes of a row then covers 64 whole bytes (16 x 14336 -> 4096: 11.1 us against 12.4 with 32
+// channels in a row per lane).
 #include "a8_internal.h"
 
 namespace awq {
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(256) void w4a8_codes_kernel(const uint32_t* __restr
   if (i >= words) return;
   const int64_t G = K / kGroup, tg = i / 256;
   const int l = (int)(i % 256) / 4, w = (int)(i % 4);
-  const int64_t n = (tg / G) * 16 + l % 16, k = (tg % G) * kGroup + 32 * (l / 16) + 8 * w;
+  const int64_t n = (tg / G) * 16 + l % 16, k = (tg % G) * kGroup + 16 * (l / 16) + 64 * (w / 2) + 8 * (w % 2);
   uint32_t out = 0;
   if (n < N) {
     const uint32_t q = qweight[n * (K / 8) + k / 8];
@@ -179,7 +181,9 @@ __device__ __forceinline__ i32x8 join(const u32x4 lo, const u32x4 hi) {
 // ---- few tokens: the weight as a stream ----------------------------------------------------------------
 // A block computes CT tiles of 16 channels for up to 16 TT tokens over all of K.  Its WV waves take the
 // groups in turn, D of them in flight in each wave, with fp32 sums of their own, which meet in LDS at the
-// end in wave order.  Sum x per token and group is one more product, with ones, in the layout of the
+// end in wave order.  Bound: up to 16 tokens by the weight's bytes and the time until they flow (1 x 4096 -> 28672:
+// 12.5 us, 5.0 TB/s, what a copy reaches; 16 x 14336 -> 4096: 11.1 us, 2.8 TB/s, 256 blocks of seven groups a wave);
+// beyond, by the reads of X and the codes from L2, 4 KiB each per wave and group.  Sum x per token and group is one more product, with ones, in the layout of the
 // sums it corrects.  Rows past the last token repeat it and are not stored.
 template <int KIND, int TT, int CT, int WV, int D>
 __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) {
@@ -189,19 +193,18 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
   const int G = (int)(p.K / kGroup);
   const int64_t tiles = (p.N + 15) / 16;
   const int64_t t0 = (int64_t)blockIdx.x * CT, m0 = (int64_t)blockIdx.y * (16 * TT);
-  const uint8_t* xrow[TT];
+  const uint8_t* xbase = static_cast<const uint8_t*>(p.x) + m0 * p.ldx;
+  uint32_t xoff[TT];  // less than 2^31: host-checked
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t m = m0 + 16 * t + c;
-    xrow[t] = static_cast<const uint8_t*>(p.x) + (m < p.M ? m : p.M - 1) * p.ldx + 32 * j;
-  }
+  for (int t = 0; t < TT; ++t)
+    xoff[t] = (uint32_t)((m0 + 16 * t + c < p.M ? 16 * t + c : (int)(p.M - 1 - m0)) * p.ldx + 16 * j);
   const uint32_t* wrow[CT];
   const uint32_t* srow[CT];
 #pragma unroll
   for (int q = 0; q < CT; ++q) {
     const int64_t tile = t0 + q < tiles ? t0 + q : tiles - 1;  // past the last tile: loaded, not stored
-    wrow[q] = p.codes + tile * G * 256 + 4 * lane;
-    srow[q] = p.steps + tile * G * 16 + c;
+    wrow[q] = p.codes + tile * G * 256;
+    srow[q] = p.steps + tile * G * 16;
   }
   constexpr bool E4M3 = KIND != kInt8;
   constexpr int kOne = E4M3 ? 0x38383838 : 0x01010101;
@@ -219,22 +222,27 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
     const int64_t g = wave + i * WV;
 #pragma unroll
     for (int q = 0; q < CT; ++q) {
-      b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[q] + g * 256));
-      b.dz[q] = srow[q][g * 16];
+      b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[q] + g * 256) + (unsigned)lane);
+      b.dz[q] = (srow[q] + g * 16)[(unsigned)c];
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) b.x[t][h] = *reinterpret_cast<const u32x4*>(xrow[t] + g * kGroup + 16 * h);
+      for (int h = 0; h < 2; ++h) b.x[t][h] = *reinterpret_cast<const u32x4*>(xbase + g * kGroup + 64 * h + xoff[t]);
   };
   auto use = [&](const Group& b) AWQ_INLINE {
     Operand<KIND> w[CT];
     float d[CT], z[CT];
-#pragma unroll
-    for (int q = 0; q < CT; ++q) {
+    auto unpack = [&](int q) AWQ_INLINE {
       w[q] = operand<KIND>(unpack_codes(b.w[q]));
       d[q] = h2f(b.dz[q] & 0xffffu) * (E4M3 ? 1.0f / kE4m3Unit : 1.0f);
       z[q] = h2f(b.dz[q] >> 16) * (E4M3 ? kE4m3Unit : 1.0f);
+    };
+    // one token tile: each channel tile's codes are unpacked just before its product (int8, 1 x 4096 -> 28672: 12.6
+    // us against 13.2); several: all of them first (101 x 4096 -> 6144: 13.7 against 14.0)
+    if constexpr (TT > 1) {
+#pragma unroll
+      for (int q = 0; q < CT; ++q) unpack(q);
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -242,6 +250,7 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
       const f32x4 sx = group_product<KIND>(a, ones);
 #pragma unroll
       for (int q = 0; q < CT; ++q) {
+        if constexpr (TT == 1) unpack(q);
         const f32x4 s = group_product<KIND>(a, w[q]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -290,15 +299,45 @@ __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) 
   }
 }
 
+// Blocks of 32 tokens and ct channel tiles: the fewest channels that leave at most one block of eight waves per CU
+// (more channels read X less often, fewer blocks leave CUs idle); then blocks of four waves, several per CU.
+// K = 4096, us: 192 blocks of 2 tiles 7.5, 256 of 3 8.4, 256 of 4 8.9; 512 of 3 in four waves 13.3 (384 of 4 14.6,
+// 768 of 2 in eight 15.9); 448 of 4 in four waves 16.5 (in eight 17.9; 896 of 2 21.3).  Beyond 512 blocks the split
+// path is as fast or faster (64 x 4096 -> 28672: 30.4 / 26.0; 129 x 8192 -> 8192: 38.2 / 33.9).
+struct StreamShape {
+  int ct, waves;
+  float us;  // estimated
+};
+StreamShape stream_shape(int64_t M, int64_t G, int64_t tiles) {
+  const int64_t rows = (M + 31) / 32;
+  auto blocks = [&](int ct) { return (tiles + ct - 1) / ct * rows; };
+  const float g = (float)G;
+  if (blocks(2) <= 256) return {2, 8, 3.2f + (0.053f + 0.0025f * (float)(M < 32 ? M : 32)) * g};
+  if (blocks(3) <= 256) return {3, 8, 3.2f + 0.163f * g};
+  if (blocks(4) <= 256) return {4, 8, 3.2f + 0.175f * g};
+  if (blocks(3) <= 512) return {3, 4, 3.2f + 0.316f * g};
+  const float b = (float)blocks(4);
+  return {4, 4, 3.2f + 0.356f * g * (b <= 384.0f ? 1.0f : b <= 512.0f ? b / 384.0f : b / 307.0f)};
+}
+
 template <int KIND>
 hipError_t launch_stream(const W4a8Args& a, int tt, hipStream_t st) {
   const int64_t tiles = w4a8_tiles(a.N);
-  const unsigned pairs = (unsigned)((tiles + 1) / 2);
-  // two channel tiles per block halve the reads of X where that still leaves more blocks than CUs
-  // (16 tokens x 4096 -> 28672: 15.0 us against 20.4; 5 x 14336 -> 4096: 10.6 against 8.8)
-  if (tt == 2) w4a8_stream_kernel<KIND, 2, 2, 8, 1><<<dim3(pairs, (unsigned)((a.M + 31) / 32)), 512, 0, st>>>(a);
-  else if (tiles >= 320) w4a8_stream_kernel<KIND, 1, 2, 8, 2><<<pairs, 512, 0, st>>>(a);
-  else w4a8_stream_kernel<KIND, 1, 1, 16, 2><<<(unsigned)tiles, 1024, 0, st>>>(a);
+  if (tt == 2) {
+    const StreamShape s = stream_shape(a.M, a.K / kGroup, tiles);
+    const dim3 grid((unsigned)((tiles + s.ct - 1) / s.ct), (unsigned)((a.M + 31) / 32));
+    if (s.ct == 2) w4a8_stream_kernel<KIND, 2, 2, 8, 1><<<grid, 512, 0, st>>>(a);
+    else if (s.ct == 3 && s.waves == 8) w4a8_stream_kernel<KIND, 2, 3, 8, 1><<<grid, 512, 0, st>>>(a);
+    else if (s.ct == 3) w4a8_stream_kernel<KIND, 2, 3, 4, 1><<<grid, 256, 0, st>>>(a);
+    else if (s.waves == 8) w4a8_stream_kernel<KIND, 2, 4, 8, 1><<<grid, 512, 0, st>>>(a);
+    else w4a8_stream_kernel<KIND, 2, 4, 4, 1><<<grid, 256, 0, st>>>(a);
+  } else if (tiles >= 320) {
+    // two channel tiles per block halve the reads of X where that still leaves more blocks than CUs
+    // (16 tokens x 4096 -> 28672: 15.0 us against 20.4; 5 x 14336 -> 4096: 10.6 against 8.8)
+    w4a8_stream_kernel<KIND, 1, 2, 8, 2><<<(unsigned)((tiles + 1) / 2), 512, 0, st>>>(a);
+  } else {
+    w4a8_stream_kernel<KIND, 1, 1, 16, 2><<<(unsigned)tiles, 1024, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -486,8 +525,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   }
   load_codes(0);
   // this lane's pieces of row c of a token tile (tiles are 16 rows: the same swizzle in each)
-  const int a0 = c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
-  const int a1 = c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
+  const int a0 = c * 128 + 16 * (j ^ row_swizzle(c));
+  const int a1 = c * 128 + 16 * ((j + 4) ^ row_swizzle(c));
   i32x8 an;         // the next token tile's bytes
   uint32_t dn[4];   // the next step's steps and zero points
   auto read_a = [&](const uint8_t* st, int t) AWQ_INLINE {
@@ -729,8 +768,8 @@ __global__ __launch_bounds__(512, 2) void w4a8_split_kernel(const W4a8Args p, fl
     for (int q = 0; q < 4; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   constexpr int kOne = E4M3 ? 0x38383838 : 0x01010101;
   const Operand<KIND> ones = operand<KIND>((i32x8){kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne});
-  const int a0 = base + c * 128 + 16 * ((2 * j) ^ row_swizzle(c));
-  const int a1 = base + c * 128 + 16 * ((2 * j + 1) ^ row_swizzle(c));
+  const int a0 = base + c * 128 + 16 * (j ^ row_swizzle(c));
+  const int a1 = base + c * 128 + 16 * ((j + 4) ^ row_swizzle(c));
   i32x8 an;                // the next token tile's bytes
   u32x4 cw[4];             // the next step's codes
   uint32_t dn[4];          // and its steps and zero points
@@ -952,11 +991,7 @@ Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
       }
     }
   }
-  // The stream, 32 tokens and 32 channels per block (32 x 4096 -> 6144: 7.6 us against 14.7 split; 64 tokens 12.3
-  // against 16.7; 64 x 4096 -> 28672: 37 against 25.7).
-  const float blocks = (float)((N + 31) / 32) * (float)((M + 31) / 32);
-  if (M <= 256 && 3.2f + 0.134f * (float)G * (blocks <= 256.0f ? 1.0f : 1.15f * blocks / 256.0f) < best)
-    pl = Plan{kStream, 2, 1, (int)G};
+  if (M <= 256 && stream_shape(M, G, w4a8_tiles(N)).us < best) pl = Plan{kStream, 2, 1, (int)G};
   return pl;
 }
 

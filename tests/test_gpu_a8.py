@@ -566,3 +566,19 @@ def test_refusals(awq):
         awq.w4a8(a, w, dtype=torch.float16)
     with pytest.raises(ValueError):
         awq.w4a8(a, awq.W4A8Weight(w.data[:64], 16, 256))
+
+
+# 17 to 256 tokens: blocks of two channel tiles, three and four in eight waves, three and four in four waves, each with
+# a ragged last block of tokens and of channels
+@pytest.mark.parametrize("M,K,N", [(33, 1152, 1000), (63, 256, 4100), (96, 256, 3600), (40, 128, 9000), (101, 384, 4500),
+                                   (250, 640, 1025), (32, 256, 20000), (17, 2176, 8200),
+                                   (125, 256, 4090), (31, 384, 28001)])
+@pytest.mark.parametrize("xt,yt", [(I8, F32), (I8, BF16), (E4M3, F32), (E4M3, BF16)])
+def test_w4a8_some_tokens(awq, M, K, N, xt, yt):
+    banner(f"w4a8 some tokens M={M} K={K} N={N} {xt} {yt}")
+    art = artefact(N, K, 80)
+    q, sc = codes(M, K, xt, 81)
+    Y = torch.full((M + 2, N + 8), -7.0, dtype=yt, device=DEV)
+    awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), out=Y[:M, :N])
+    check_tile(Y[:M, :N], q, sc, art)
+    assert torch.all(Y[M:] == -7.0) and torch.all(Y[:, N:] == -7.0)
