@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 // A block of four waves, one per SIMD, computes 16 TM tokens x 256 channels, and two blocks share a CU; wave wn has
 // all the tokens and 64 of the channels and takes one group a step.  The tokens' bytes (128 per row and group)
 // and the groups' steps come into LDS by DMA in four stages; the codes, which no other wave of the block needs,
-// come straight into registers in operand order, a group ahead.  The barrier of step g says that stages g
+// come straight into registers in operand order, one or two groups ahead.  The barrier of step g says that stages g
 // and g + 1 have landed, so that the last products of a step run beside the reads for the first ones of
 // the next; stage g + 2 is under way and g + 3 is requested.
 // Rows of 128 bytes hold their 16-byte pieces at piece ^ (row % 8) ^ (row / 8 % 2): the reads of sixteen
@@ -392,11 +392,11 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 // cores in fp16 with both operands as high and low parts (sums 22 bits, D z 15: exact), one
 // instruction of 16 cycles for eight groups.
 //
-// 4096 x 4096 -> 28672: e4m3 436 us (2.2 PFLOP/s), int8 480 (2.0).  A loop of nothing but such products and
+// 4096 x 4096 -> 28672: e4m3 440 us (2.2 PFLOP/s), int8 484 (2.0).  A loop of nothing but such products and
 // multiply-adds runs at 4.0 (e4m3) and 2.9 (int8), a library product without steps at 3.1 and 2.55.  The clock is
-// down to 1.7 .. 2.0 GHz under this load; per cycle the matrix unit is busy 0.55, and without any copies or loads
-// 0.62: neither barriers nor LDS reads nor unpacking bound it (each left out alone: no change), but the
-// products' own latency beside their multiply-adds at two waves per SIMD.
+// down to 1.7 .. 2.0 GHz under this load.  4096 x 11008 -> 4096, e4m3, 169 us: 149 without the codes' loads, 132
+// without the copies into LDS, 117 without both, 102 without the zero points' part too: what bounds it is the
+// operands' way from L2 (32 KiB a block and step, and the power it takes), then the products.
 constexpr int kTileN = 256;
 template <int TM>
 constexpr int kTileStage = 16 * TM * 128 + 1024;
@@ -410,6 +410,9 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   constexpr bool E4M3 = KIND != kInt8;
   constexpr int STAGE = kTileStage<TM>, SOFF = 16 * TM * 128;
   constexpr int NDMA = TM / 2 + 1;  // copies per wave and stage
+  // groups that the codes are requested ahead: two, but for the case whose registers one fills (256 tiles of 64 tokens, G =
+  // 86: 60.4 us against 62.6; 896 of 128: 439.9 / 442.5; four ahead: no change)
+  constexpr int AHEAD = TM == 8 && KIND == kInt8 ? 1 : 2;
   __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGE];
@@ -456,8 +459,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
                                                (int)xoff[i], g * 128, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (AWQ_LDS_A8 void*)(st + SOFF + wn * 256), 4, (int)soff, g * 64, 0, 0);
   };
-  u32x4 cw[4];  // the codes of the next step
-  auto load_codes = [&](int g) AWQ_INLINE {
+  u32x4 codes[AHEAD][4];  // the codes of the next steps, step g's in codes[g % AHEAD]
+  auto load_codes = [&](u32x4* cw, int g) AWQ_INLINE {
     g = g < G ? g : G - 1;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -523,7 +526,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
     z0 = z1;
     load_zero(z1, b + 2);
   }
-  load_codes(0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load_codes(codes[i], i);
   // this lane's pieces of row c of a token tile (tiles are 16 rows: the same swizzle in each)
   const int a0 = c * 128 + 16 * (j ^ row_swizzle(c));
   const int a1 = c * 128 + 16 * ((j + 4) ^ row_swizzle(c));
@@ -541,13 +545,15 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   auto sync = [&] () AWQ_INLINE {
     __builtin_amdgcn_sched_barrier(0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(NDMA | (0x7 << 4) | (0xf << 8));  // vmcnt; no wait for LDS and exports
+    constexpr int NEWER = NDMA + (AHEAD > 1 ? 4 : 0);
+    static_assert(NEWER < 16, "the low four bits of vmcnt");
+    __builtin_amdgcn_s_waitcnt(NEWER | (0x7 << 4) | (0xf << 8));  // vmcnt; no wait for LDS and exports
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
   };
   // Step g: stages now (g), next (g + 1) and free (g - 1, then g + 3).
-  auto step = [&](int g, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
+  auto step = [&](int g, u32x4* cw, const uint8_t* now, const uint8_t* next, uint8_t* free) AWQ_INLINE {
     Operand<KIND> w[4];
     float d[4];
 #pragma unroll
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
       asm volatile("" : "+v"(d[q]));  // fp32 from here on: v_fmac_f32 in place, not v_fma_mix_f32 from fp16
     }
     sync();
-    load_codes(g + 1);
+    load_codes(cw, g + AHEAD);
     __builtin_amdgcn_sched_barrier(0);
     dma(free, g + 3);
     __builtin_amdgcn_sched_barrier(0);
@@ -601,7 +607,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   };
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  constexpr int NEWER0 = 2 * NDMA + 4;
+  constexpr int NEWER0 = 2 * NDMA + 4 * AHEAD;
   __builtin_amdgcn_s_waitcnt((NEWER0 & 15) | ((NEWER0 >> 4) << 14) | (0x7 << 4) | (0xf << 8));  // stage 0
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -610,14 +616,14 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   read_d(st0);
   int g = 0;
   for (; g + 4 <= G; g += 4) {
-    step(g, st0, st1, st3);
-    step(g + 1, st1, st2, st0);
-    step(g + 2, st2, st3, st1);
-    step(g + 3, st3, st0, st2);
+    step(g, codes[0], st0, st1, st3);
+    step(g + 1, codes[1 % AHEAD], st1, st2, st0);
+    step(g + 2, codes[2 % AHEAD], st2, st3, st1);
+    step(g + 3, codes[3 % AHEAD], st3, st0, st2);
   }
-  if (g < G) step(g, st0, st1, st3);
-  if (g + 1 < G) step(g + 1, st1, st2, st0);
-  if (g + 2 < G) step(g + 2, st2, st3, st1);
+  if (g < G) step(g, codes[0], st0, st1, st3);
+  if (g + 1 < G) step(g + 1, codes[1 % AHEAD], st1, st2, st0);
+  if (g + 2 < G) step(g + 2, codes[2 % AHEAD], st2, st3, st1);
   __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt and lgkmcnt 0: no copy or load outlives the block
   // stores through a resource that ends with the last row's last channel: rows past M are dropped there,
   // channels past N by the lane mask (128 rows of Y span less than 2^31 bytes: host-checked)
