@@ -6,7 +6,8 @@ this package does not load the library; ``stats``/``search``/``pack`` load it on
 and raise if it has not been built.
 """
 
-__all__ = ["stats", "search", "pack", "search_workspace_bytes", "stats_workspace_bytes"]
+__all__ = ["stats", "search", "pack", "search_workspace_bytes", "stats_workspace_bytes", "rmsnorm", "act_mul",
+           "w4a8_weight", "w4a8", "Act8"]
 
 
 def __getattr__(name):
