@@ -181,8 +181,10 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, float2 (*r
 
 // What the row's numbers give: the factor of the stored values (1 / rms, or 1), and for codes the
 // factor that takes v to its code, and the scale.  A row that is not finite gets NaN in all of them.
+// Where a small eps takes the codes' factor past fp32's range (max |v| below 2^-119, a row of zeros among
+// them), a power of two of it, pre, is multiplied to v first; otherwise pre is 1.
 struct RowFactors {
-  float mul, code, scale;
+  float mul, code, scale, pre;
 };
 template <int OP>
 __device__ __forceinline__ RowFactors row_factors(const RowArgs& a, float sum, uint32_t top) {
@@ -195,6 +197,11 @@ __device__ __forceinline__ RowFactors row_factors(const RowArgs& a, float sum, u
   const float mf = m < inf ? fmaxf(m, kFloorMax) : nan;
   f.scale = mf / q;
   f.code = f.mul * (q / mf);
+  f.pre = 1.0f;
+  if (OP == kOpNorm && f.code == inf) {
+    f.pre = 0x1p64f;
+    f.code = f.mul * 0x1p-64f * (q / mf);
+  }
   return f;
 }
 
@@ -312,6 +319,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
     }
     const RowFactors f = row_factors<OP>(a, sum, top);
     if (ytype >= kI8) {
+      if (OP == kOpNorm && f.pre != 1.0f) {
+        vt *= f.pre;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[u][e] *= f.pre;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (u * T + t < units)
@@ -376,7 +390,7 @@ __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
       const float v = value(k);
       if (OP == kOpNorm && BT != kNoOperand && a.h != nullptr) store1(a.h, row * a.ldh + k, h, BT);
       if (a.y_type >= kI8) {
-        const float w[4] = {v, v, v, v};
+        const float c = v * f.pre, w[4] = {c, c, c, c};
         static_cast<uint8_t*>(a.y)[row * a.ldy + k] = (uint8_t)codes4(w, f.code, a.y_type == kE4m3);
       } else {
         store1(a.y, row * a.ldy + k, OP == kOpNorm ? v * f.mul : v, a.y_type);

@@ -582,3 +582,19 @@ def test_w4a8_some_tokens(awq, M, K, N, xt, yt):
     awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), out=Y[:M, :N])
     check_tile(Y[:M, :N], q, sc, art)
     assert torch.all(Y[M:] == -7.0) and torch.all(Y[:, N:] == -7.0)
+
+
+@pytest.mark.parametrize("K", [128, 133, 5000, 65544])
+@pytest.mark.parametrize("eps", [1e-12, 1e-20, 1e-38])
+@pytest.mark.parametrize("dtype", [I8, E4M3])
+def test_rmsnorm_small_eps(awq, K, eps, dtype):
+    """Rows of zeros and of tiny values, where 1 / sqrt(eps) times the codes' factor would pass fp32's range: zeros
+    give codes of zero with the least scale, tiny rows the codes of their values."""
+    x = torch.zeros((5, K))
+    x[1], x[2], x[3] = 2.0 ** -125, -(2.0 ** -112), 2.0 ** -101
+    x[1, K // 2:] = 2.0 ** -126
+    x[4] = rand((K,), F32, 90)
+    res = awq.rmsnorm(x.to(DEV), torch.ones(K, device=DEV), eps=eps, dtype=dtype)
+    _, want = a8.rmsnorm(f64(x), None, np.ones(K), float(np.float32(eps)))
+    assert torch.all(res.q[0].cpu().float() == 0)
+    check(res, want, 72 * U)
