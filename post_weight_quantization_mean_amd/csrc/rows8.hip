@@ -354,7 +354,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rows_kernel(const RowAr
 }
 
 // ---- any row: two passes ------------------------------------------------------------------------
-// Rows longer than the registers of a block (65536 elements): single elements, read again for the store.
+// Rows longer than the registers of a block (32768 elements): single elements, read again for the store (1000 rows of
+// 65536, rmsnorm bf16 -> e4m3: 278 us; eight units a lane spill registers to memory and take 331).
 template <int OP, int XT, int BT>
 __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
   constexpr int W = 16;
@@ -409,8 +410,9 @@ void launch_rows_as(const RowArgs& a, hipStream_t st) {
   rows_kernel<OP, XT, BT, WV, UV, ALIGNED><<<grid_of(WV == 1 ? (a.M + 3) / 4 : a.M), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
   // The fewest registers that hold the row: few units per lane leave more rows in flight, and lanes without a
   // unit read for nothing (4096 rows, silu gate, K = 14336, bf16 -> e4m3: 4 waves x 8 units 68.6 us, 4 x 7 58.7,
-  // 8 x 4 53.9, 16 x 2 53.1; K = 4096, rmsnorm: 1 x 8 22.8 us, 4 x 2 21.2).  Rows of any alignment take the steps that are kept.
-  if (units > 16 * 64 * 8) {
+  // 8 x 4 53.9, 16 x 2 53.1; K = 4096, rmsnorm: 1 x 8 22.8 us, 4 x 2 21.2;
+  // 1000 rows of 20480, rmsnorm: 16 x 4 55.6 us, 16 x 3 32.6).  Rows of any alignment take the steps that are kept.
+  if (units > 16 * 64 * 4) {
     rows_any_kernel<OP, XT, BT><<<grid_of(a.M), 1024, 0, st>>>(a);
   } else if (units <= 128) {
     AWQ_ROWS(1, 2);
@@ -430,8 +432,10 @@ void launch_rows_as(const RowArgs& a, hipStream_t st) {
     if constexpr (ALIGNED) AWQ_ROWS(8, 3);
   } else if (units <= 2048) {
     AWQ_ROWS(16, 2);
+  } else if (units <= 3072) {
+    AWQ_ROWS(16, 3);
   } else {
-    AWQ_ROWS(16, 8);
+    AWQ_ROWS(16, 4);
   }
 #undef AWQ_ROWS
 }

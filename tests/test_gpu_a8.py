@@ -598,3 +598,18 @@ def test_rmsnorm_small_eps(awq, K, eps, dtype):
     _, want = a8.rmsnorm(f64(x), None, np.ones(K), float(np.float32(eps)))
     assert torch.all(res.q[0].cpu().float() == 0)
     check(res, want, 72 * U)
+
+
+@pytest.mark.parametrize("M,K", [(2, 16392), (300, 24576), (2, 24577), (3, 32768), (2, 32775), (2, 32776)])
+@pytest.mark.parametrize("xt,out", [(BF16, E4M3), (F32, BF16), (F32, I8)])
+def test_long_rows(awq, M, K, xt, out):
+    """Rows of three and four units a lane, the longest that stay in registers, and the first that do not."""
+    banner(f"long rows M={M} K={K} {xt} {out}")
+    x, r = rand((M, K), xt, 91), rand((M, K), xt, 92)
+    g = rand((K,), F32, 93) * 0.1 + 1
+    res, h = awq.rmsnorm(x.to(DEV), g.to(DEV), r.to(DEV), dtype=out)
+    hr, want = a8.rmsnorm(f64(x), f64(r), f64(g), 1e-6)
+    check_stored(h, hr, 2 * U)
+    check(res, want, 72 * U)
+    y = awq.act_mul(x.to(DEV), r.to(DEV), dtype=out)
+    check(y, a8.act_mul(f64(x), f64(r), None, "silu"), act_tol(x, "silu", out, r, None))
