@@ -196,11 +196,17 @@ __device__ __forceinline__ RowFactors row_factors(const RowArgs& a, float sum, u
   const float m = __uint_as_float(top) * f.mul;  // max |y|; NaN stays
   const float mf = m < inf ? fmaxf(m, kFloorMax) : nan;
   f.scale = mf / q;
-  f.code = f.mul * (q / mf);
+  f.code = q / mf;
   f.pre = 1.0f;
-  if (OP == kOpNorm && f.code == inf) {
-    f.pre = 0x1p64f;
-    f.code = f.mul * 0x1p-64f * (q / mf);
+  if (OP == kOpNorm) {
+    // Q / max |v|: 1 / rms cancels, and with it its roundings (but where the floor is above max |y|)
+    const float t = __uint_as_float(top);
+    if (m < kFloorMax) f.code = f.mul * (q / kFloorMax);
+    else if (m < inf) f.code = q / t;
+    if (f.code == inf) {
+      f.pre = 0x1p64f;
+      f.code = m < kFloorMax ? f.mul * 0x1p-64f * (q / kFloorMax) : q / (t * 0x1p64f);
+    }
   }
   return f;
 }
