@@ -613,3 +613,35 @@ def test_long_rows(awq, M, K, xt, out):
     check(res, want, 72 * U)
     y = awq.act_mul(x.to(DEV), r.to(DEV), dtype=out)
     check(y, a8.act_mul(f64(x), f64(r), None, "silu"), act_tol(x, "silu", out, r, None))
+
+
+def test_w4a8_refuses_workspaces_and_alignment(awq):
+    """A workspace that is too small, not aligned or not contiguous; codes whose rows start off 16 bytes; a weight of
+    other sizes; and the same arguments once they are right."""
+    M, K, N = 8260, 512, 80  # whole tiles: they need one at any K
+    art = artefact(N, K, 95)
+    w = on_gpu(awq, art)
+    q, sc = codes(M, K, I8, 96)
+    a = awq.Act8(q.to(DEV), sc.to(DEV))
+    need = awq.w4a8_workspace_bytes(M, K, N)
+    assert need > 0 and awq.w4a8_workspace_bytes(4, K, N) == 0
+    buf = torch.empty(2 * need + 64, dtype=torch.uint8, device=DEV)
+    for ws in (buf[:need - 1], buf[8:8 + need]):
+        with pytest.raises(awq.AwqError):
+            awq.w4a8(a, w, workspace=ws)
+    with pytest.raises(ValueError):
+        awq.w4a8(a, w, workspace=buf[::2])
+    with pytest.raises(ValueError):
+        awq.w4a8(a, w, workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        awq.w4a8(a, w, workspace=need)
+    wide = torch.zeros((M, K + 8), dtype=I8, device=DEV)
+    with pytest.raises(awq.AwqError):
+        awq.w4a8(awq.Act8(wide[:, :K], a.scale), w)
+    with pytest.raises(ValueError):
+        awq.w4a8(a, w._replace(K=K + 128))
+    with pytest.raises(ValueError):
+        awq.w4a8(a, w._replace(N=10 * N))
+    with pytest.raises(awq.AwqError):
+        awq.w4a8(awq.Act8(a.q[:1].expand(M, K), a.scale), w)
+    check_product(awq.w4a8(a, w, workspace=buf[:need]), q, sc, art)
