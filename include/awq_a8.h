@@ -22,6 +22,9 @@ extern "C" {
 #define AWQ_DTYPE_I8 2   /* int8, codes -127 .. 127 */
 #define AWQ_DTYPE_E4M3 3 /* e4m3 without infinities (OCP), |code| <= 448 */
 
+/* Or'ed into awq_w4a8's y_dtype: e4m3 codes are summed in fp32 for a BF16 Y too. */
+#define AWQ_W4A8_SUMS_F32 0x100
+
 /* Activations of awq_act_mul, beside awq.h's AWQ_ACT_GELU and AWQ_ACT_SILU. */
 #define AWQ_ACT_NONE 2
 
@@ -90,12 +93,14 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  * on the 8-bit matrix cores: a code q is an int8 byte as it stands, and as an e4m3 byte it is
  * exactly q 2^-9.  I8: the inner sums are exact integers.  E4M3: the products are exact; for an F32 Y
  * they are summed in fp32, for a BF16 Y sixteen at a time to 14 bits of the largest of them (the matrix
- * unit's own sum: at most 2^-9 of the sum of their magnitudes, 2^-13 and less as a rule) and
- * then in fp32.  The steps and the sum over groups are fp32; Y is rounded once.
+ * unit's own sum: at most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more
+ * than a bf16 rounding where one large code with q = z stands beside small ones) and then in fp32.
+ * y_dtype BF16 | AWQ_W4A8_SUMS_F32 sums in fp32 as for an F32 Y, at half the matrix rate; with I8 or an F32 Y
+ * the flag changes nothing.  The steps and the sum over groups are fp32; Y is rounded once.
  *   Xq      [M, K] of x_dtype I8 or E4M3, row stride ldx, 16-byte aligned rows
  *   xscale  fp32 [M]
  *   wt      as written by awq_w4a8_weight for the same N and K
- *   Y       [M, N] of y_dtype F32 or BF16, row stride ldy >= N
+ *   Y       [M, N] of y_dtype F32 or BF16 (with or without AWQ_W4A8_SUMS_F32), row stride ldy >= N
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each

@@ -632,13 +632,14 @@ def w4a8_workspace_bytes(M: int, K: int, N: int) -> int:
 
 
 def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
-         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+         workspace: Optional[torch.Tensor] = None, fp32_sums: bool = False) -> torch.Tensor:
     """Y = X W_hat^T for 8-bit activations (``Act8``: from ``rmsnorm``, ``act_mul``, or the caller's own)
     and a weight laid out by ``w4a8_weight``.  Y [M, N] is float32 (the default) or bfloat16; e4m3 codes are
-    summed in fp32 for a float32 Y, to 14 bits sixteen at a time for a bfloat16 one (at half the time).
+    summed in fp32 for a float32 Y, to 14 bits sixteen at a time for a bfloat16 one (in half the time for
+    prompts).  ``fp32_sums=True`` sums them in fp32 for a bfloat16 Y too; int8 sums are always exact.
     Rows of the codes start at multiples of 16 bytes.
     ``workspace``: ``w4a8_workspace_bytes`` for (M, K, N), allocated here when not given; calls that may
     run at the same time (two streams, two graphs) need one each."""
     q, scale = X
     data, N, K = weight
-    return _on(q, (_a8 or _bound()).w4a8, q, scale, data, N, K, dtype, out, workspace)
+    return _on(q, (_a8 or _bound()).w4a8, q, scale, data, N, K, dtype, out, workspace, fp32_sums)

@@ -259,9 +259,9 @@ PyObject* act_mul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// w4a8(q, scale, data, N, K, dtype, out, workspace, stream)
+// w4a8(q, scale, data, N, K, dtype, out, workspace, fp32_sums, stream)
 PyObject* w4a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("w4a8", n, 9, [&]() -> PyObject* {
+  return guarded("w4a8", n, 10, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "X.q");
     const at::Tensor& scale = tensor(a[1], "X.scale");
     const at::Tensor& data = tensor(a[2], "weight");
@@ -294,7 +294,9 @@ PyObject* w4a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ldy = row_stride(Y, "out", dev, M, N);
       if (a[5] != Py_None && want != Y.scalar_type()) value_error("dtype and out disagree");
     }
-    const int yc = float_code(Y, "out");
+    const int sums = PyObject_IsTrue(a[8]);
+    if (sums < 0) throw Raise{nullptr, ""};
+    const int yc = float_code(Y, "out") | (sums ? AWQ_W4A8_SUMS_F32 : 0);
     size_t need = lib.workspace_bytes(M, K, N);
     at::Tensor ws;
     if (need > 0) {
@@ -308,7 +310,7 @@ PyObject* w4a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check(lib.w4a8(q.const_data_ptr(), xc, static_cast<const float*>(sp), M, K, ldx, data.const_data_ptr(), N, 128,
                    Y.mutable_data_ptr(), yc, ldy, ws.defined() ? ws.mutable_data_ptr() : nullptr, need,
-                   stream_of(a[8])),
+                   stream_of(a[9])),
           "awq_w4a8");
     return a[6] != Py_None ? Py_NewRef(a[6]) : wrap(Y);
   });

@@ -40,7 +40,7 @@ struct W4a8Args {
   const float* powers;
   void* y;
   int64_t M, K, N, ldx, ldy;
-  bool e4m3, ybf16;
+  bool e4m3, ybf16, sums32;  // sums32: e4m3 codes summed in fp32 for a bf16 y too
 };
 hipError_t launch_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros, int64_t N,
                               int64_t K, uint32_t* codes, uint32_t* steps, float* powers, hipStream_t st);

@@ -103,9 +103,12 @@ constexpr float kE4m3Unit = 0x1p-9f;  // an e4m3 byte b < 16 is b times this
 
 // How a group's products are formed.  The e4m3 matrix instruction adds 16 products at a time after
 // shifting them to the largest one's exponent and keeps 14 bits there (measured; the sums of 16 then add in
-// fp32): about 2^-13 of the largest product, well below a bf16 result's half step but not an fp32 one's.
-// kE4m3Fast is taken for bf16 results; kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32,
-// at half the matrix rate, for fp32 results.
+// fp32): about 2^-13 of the largest product.  On activations with 1% of channels 10 to 50 times the others that
+// adds 2e-4 (rms, relative) to a bf16 result's rounding of 1.7e-3; where a large code's q is its zero point, so that
+// its product cancels, what is lost beside it can be more than that rounding.  kE4m3Fast is taken for bf16
+// results, where it takes half the time: 4096 x 4096 -> 28672 442 us against 875, 1024 x 11008 -> 4096 61 / 105,
+// 16 x 14336 -> 4096 10.7 / 11.4.  kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32, at half
+// the matrix rate, for fp32 results and where the caller asks for such sums.
 constexpr int kInt8 = 0, kE4m3Fast = 1, kE4m3Wide = 2;
 
 template <int KIND>
@@ -1060,7 +1063,7 @@ size_t w4a8_workspace(int64_t M, int64_t K, int64_t N) {
 
 hipError_t launch_w4a8(const W4a8Args& a, void* ws, hipStream_t st) {
   if (!a.e4m3) return launch_kind<kInt8>(a, ws, st);
-  return a.ybf16 ? launch_kind<kE4m3Fast>(a, ws, st) : launch_kind<kE4m3Wide>(a, ws, st);
+  return a.ybf16 && !a.sums32 ? launch_kind<kE4m3Fast>(a, ws, st) : launch_kind<kE4m3Wide>(a, ws, st);
 }
 
 }  // namespace awq

@@ -645,3 +645,40 @@ def test_w4a8_refuses_workspaces_and_alignment(awq):
     with pytest.raises(awq.AwqError):
         awq.w4a8(awq.Act8(a.q[:1].expand(M, K), a.scale), w)
     check_product(awq.w4a8(a, w, workspace=buf[:need]), q, sc, art)
+
+
+# K = 384: stream with one and two token tiles, split, whole tiles
+@pytest.mark.parametrize("M,N", [(3, 40), (40, 48), (300, 70), (8260, 48)])
+def test_w4a8_fp32_sums_for_bf16(awq, M, N):
+    """fp32_sums: a bf16 result of e4m3 codes is the fp32 result rounded once, also where the largest code of each
+    sixteen meets its zero point and cancels, beside which the matrix unit's own sums keep too few bits."""
+    K = 384
+    rng = np.random.default_rng(100)
+    qw = rng.integers(0, 16, (N, K)).astype(np.uint32)
+    qw[:, ::16] = 8
+    words = sum(qw[:, i::8] << np.uint32(4 * i) for i in range(8)).astype(np.uint32).view(np.int32)
+    art = dict(qweight=words, scales=np.full((N, K // 128), 0.01, np.float16), zeros=np.full((N, K // 128), 8, np.float16))
+    assert np.array_equal(o.unpack_words(art["qweight"]), qw)
+    q, sc = codes(M, K, E4M3, 101)
+    v = q.float() * (1.0 / 4096)
+    v[:, ::16] = 448.0
+    q = v.to(E4M3)
+    w = awq.w4a8_weight(*[torch.from_numpy(art[k]).to(DEV) for k in ("qweight", "scales", "zeros")])
+    a = awq.Act8(q.to(DEV), sc.to(DEV))
+    Y32, Y = awq.w4a8(a, w), awq.w4a8(a, w, dtype=BF16, fp32_sums=True)
+    check_product(Y32, q, sc, art)
+    check_product(Y, q, sc, art)
+    assert torch.equal(Y, Y32.to(BF16))
+    i8 = awq.Act8(q.to(DEV).view(I8), a.scale)  # int8 sums are exact: the flag changes nothing
+    assert torch.equal(awq.w4a8(i8, w, fp32_sums=True), awq.w4a8(i8, w))
+
+
+def test_w4a8_fp32_sums_flag_with_given_outputs(awq):
+    art = artefact(64, 256, 102)
+    w = on_gpu(awq, art)
+    q, sc = codes(20, 256, E4M3, 103)
+    a = awq.Act8(q.to(DEV), sc.to(DEV))
+    y = torch.empty((20, 64), dtype=BF16, device=DEV)
+    assert awq.w4a8(a, w, out=y, fp32_sums=True) is y
+    check_product(y, q, sc, art)
+    assert torch.equal(awq.w4a8(a, w, fp32_sums=True), awq.w4a8(a, w))  # an fp32 result: the same sums
