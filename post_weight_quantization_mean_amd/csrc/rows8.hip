@@ -133,7 +133,10 @@ __device__ __forceinline__ float activate(float x, int act, bool fine) {
     p = fmaf(p, t, 0.12122516334056854f);
     p = fmaf(p, t, 1.818873215597705e-06f);
     const float e = p * __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2e));  // erfc(z) / 2
-    return x < 0.0f ? x * e : fmaf(-x, e, x);
+    // e is 0 long before 64: +Inf, cut to it beside e (as integers: one instruction), stays itself; -Inf times 0 is
+    // NaN, as in the definition
+    const int xi = __float_as_int(x), cut = __float_as_int(64.0f);
+    return x < 0.0f ? x * e : fmaf(-__int_as_float(xi < cut ? xi : cut), e, x);
   }
   return x;
 }

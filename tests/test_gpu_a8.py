@@ -682,3 +682,26 @@ def test_w4a8_fp32_sums_flag_with_given_outputs(awq):
     assert awq.w4a8(a, w, out=y, fp32_sums=True) is y
     check_product(y, q, sc, art)
     assert torch.equal(awq.w4a8(a, w, fp32_sums=True), awq.w4a8(a, w))  # an fp32 result: the same sums
+
+
+# K: aligned units, a tail, less than a unit, past the registers
+@pytest.mark.parametrize("K", [8, 1024, 13, 5, 65544])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("out", [F32, BF16, I8, E4M3])
+def test_act_mul_infinities(awq, K, act, out):
+    """A row's own infinities show: +Inf stays +Inf through every activation; -Inf is NaN behind SiLU and GELU, whose
+    definitions multiply it by 0.  In 8 bits such a row's scale is NaN."""
+    x = rand((4, K), F32, 104)
+    x[1, K - 1], x[2, 0], x[3, K // 2] = float("inf"), -float("inf"), float("inf")
+    u = rand((4, K), F32, 105).abs() + 0.5
+    res = awq.act_mul(x.to(DEV), u.to(DEV), None, act, dtype=out)
+    if isinstance(res, tuple):
+        assert res.scale.isnan().tolist() == [False, True, True, True]
+        return
+    y = res.cpu().float()
+    assert y[1, K - 1] == float("inf") and y[3, K // 2] == float("inf")
+    assert y[2, 0] == -float("inf") if act == "none" else y[2, 0].isnan()
+    keep = x.isfinite()
+    y64, want = f64(res), a8.act_mul(np.where(keep, f64(x), 0.0), f64(u), None, act)
+    lim = (HALF[out] + act_tol(torch.where(keep, x, 0.0), act, out, u, None)) * np.abs(want) + 1e-36
+    assert np.all(np.abs(y64 - want)[keep.numpy()] <= lim[keep.numpy()])
