@@ -60,7 +60,8 @@ AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_
  *   Y, y_dtype, ldy, scale   as awq_rmsnorm
  * With act NONE and neither U nor s this quantizes given activations.  y is formed in fp32,
  * with a relative error of at most, in units of 2^-24: NONE 8; SILU 18, and |x| more where Y is not
- * F32; GELU 28 + 2 x^2 (its tail is that ill-conditioned; a result below 2^-126 may be 0).
+ * F32; GELU 28 + 2 x^2 (its tail is that ill-conditioned).  An activation below 2^-126 is within 2^-149 (SiLU), or
+ * may be 0 (GELU).
  * Any K.  Y may be G or U where it has their type
  * and row stride, and overlaps them in no other way.
  * ------------------------------------------------------------------------------------- */

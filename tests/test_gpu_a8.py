@@ -705,3 +705,21 @@ def test_act_mul_infinities(awq, K, act, out):
     y64, want = f64(res), a8.act_mul(np.where(keep, f64(x), 0.0), f64(u), None, act)
     lim = (HALF[out] + act_tol(torch.where(keep, x, 0.0), act, out, u, None)) * np.abs(want) + 1e-36
     assert np.all(np.abs(y64 - want)[keep.numpy()] <= lim[keep.numpy()])
+
+
+# one element, a tail, units, past the registers
+@pytest.mark.parametrize("K", [1, 13, 512, 65537])
+@pytest.mark.parametrize("xt,out", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
+def test_silu_far_negative(awq, K, xt, out):
+    """SiLU of -79 .. -105, where exp(-x) and 1 / exp(-x) leave fp32 while the result is inside: the documented bound
+    down to the least normal number, and half a step of the subnormals (2^-149) below it."""
+    M = 200 if K < 1000 else 3
+    x = (-79.0 - 26.0 * torch.rand((M, K), generator=torch.Generator().manual_seed(106))).to(xt)
+    x[0, 0] = -88.8
+    if K > 8:
+        x[1, 3], x[1, 9] = 1.5, -2.0  # among ordinary ones
+    want = a8.act_mul(f64(x), None, None, "silu")
+    y = f64(awq.act_mul(x.to(DEV), None, None, "silu", dtype=out))
+    ulp = 18.0 + (0.0 if out == F32 else 1.0) * np.abs(f64(x))
+    least = 2.0 ** -149 if out == F32 else 2.0 ** -134 + 2.0 ** -149  # half a step of bf16's subnormals
+    assert np.all(np.abs(y - want) <= (ulp * U + HALF[out]) * np.abs(want) + least)
