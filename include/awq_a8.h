@@ -55,8 +55,9 @@ AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_
  *          output are two such views); U NULL: no gate's product
  *   act    AWQ_ACT_NONE, AWQ_ACT_GELU (0.5 x (1 + erf(x / sqrt 2))) or AWQ_ACT_SILU
  *          (x / (1 + exp(-x)))
- *   s      fp32 [K] or NULL: the runtime form of 1/s where no producer absorbed it; positive
- *          (not checked here: the search and the pack did)
+ *   s      fp32 [K] or NULL: the runtime form of 1/s where no producer absorbed it; 2^-126 to 2^126,
+ *          so that s and 1/s are normal numbers (not checked here: the search and the pack did that
+ *          s is positive and finite, and what the search writes stays far inside)
  *   Y, y_dtype, ldy, scale   as awq_rmsnorm
  * With act NONE and neither U nor s this quantizes given activations.  y is formed in fp32,
  * with a relative error of at most, in units of 2^-24: NONE 8; SILU 18, and |x| more where Y is not

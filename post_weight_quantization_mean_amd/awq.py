@@ -587,8 +587,8 @@ def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tenso
 
 def act_mul(G: torch.Tensor, U: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None, act: str = "silu",
             *, dtype: Optional[torch.dtype] = None, out=None):
-    """act(G) * U / s (``act`` "silu", "gelu" (exact) or "none"; U [M, K] of G's dtype, s fp32 [K],
-    both optional): the input of a layer behind a gate, or with "none" alone the quantization of
+    """act(G) * U / s (``act`` "silu", "gelu" (exact) or "none"; U [M, K] of G's dtype, s fp32 [K] in 2^-126
+    to 2^126, both optional): the input of a layer behind a gate, or with "none" alone the quantization of
     given activations.  G and U may be the halves of one gate/up output.  ``dtype`` and ``out`` as in
     ``rmsnorm``; ``out`` may be G or U where it has their dtype and strides."""
     code = _ACTS.get(act)

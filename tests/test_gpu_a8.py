@@ -723,3 +723,19 @@ def test_silu_far_negative(awq, K, xt, out):
     ulp = 18.0 + (0.0 if out == F32 else 1.0) * np.abs(f64(x))
     least = 2.0 ** -149 if out == F32 else 2.0 ** -134 + 2.0 ** -149  # half a step of bf16's subnormals
     assert np.all(np.abs(y - want) <= (ulp * U + HALF[out]) * np.abs(want) + least)
+
+
+@pytest.mark.parametrize("K", [3, 64, 77, 65537])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_act_mul_divides_by_s_to_the_ends_of_its_range(awq, K, out):
+    """s from 2^-126 to 2^126, where s and 1 / s are normal numbers: y = x / s within the documented bound."""
+    M = 4
+    e = torch.tensor([-126, -125, -124, -60, -1, 0, 60, 124, 125, 126])
+    s = (2.0 ** e[torch.arange(K) % 10].double()).float()
+    s = torch.where(s < 2.0 ** 126, s * 1.25, s)
+    x = rand((M, K), F32, 107).double()
+    x = (x.abs() + 0.5) * s.double() * torch.tensor([1.0, -2.0, 4.0, 0.25])[:, None].double()  # results near 1
+    x = x.clamp(-3e38, 3e38).float()
+    want = f64(x) / f64(s)[None, :]
+    y = f64(awq.act_mul(x.to(DEV), None, s.to(DEV), "none", dtype=out))
+    assert np.all(np.abs(y - want) <= (8 * U + HALF[out]) * np.abs(want))
