@@ -82,7 +82,7 @@ AWQ_API int awq_act_mul(const void* G, int x_dtype, int64_t M, int64_t K, int64_
  *            powers fp32 [16 tiles]: 2^e, e per channel such that its largest step lies in
  *                   [2^10, 2^11)
  *   qweight, scales, zeros   as written by awq_pack (qweight 16-byte aligned)
- * awq_w4a8_weight_bytes is 0 for sizes that awq_w4a8_weight rejects.
+ * N is at most 2^27 (AWQ_ERR_SHAPE).  awq_w4a8_weight_bytes is 0 for sizes that awq_w4a8_weight rejects.
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_w4a8_weight_bytes(int64_t N, int64_t K);
 AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros,
@@ -106,7 +106,8 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each
- * K is a multiple of 128; 128 rows of Xq and of Y span less than 2^31 bytes each (AWQ_ERR_SHAPE).
+ * K is a multiple of 128; 128 rows of Xq and of Y span less than 2^31 bytes each; M ceil(N / 256) is below
+ * 2^29 (AWQ_ERR_SHAPE; awq_w4a8_workspace_bytes is then 0).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_w4a8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M, int64_t K, int64_t ldx,

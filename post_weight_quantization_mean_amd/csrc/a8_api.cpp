@@ -53,14 +53,23 @@ bool out_vec(const void* y, int y_type, int64_t ldy) {
 
 int map_hip(hipError_t e) { return e == hipSuccess ? AWQ_OK : AWQ_ERR_HIP; }
 
+// A launch takes fewer than 2^32 threads: 512 per 32 channels at most, and 256 per 64 tokens x 256 channels.
+constexpr int64_t kMaxN = 1 << 27, kMaxTokenTiles = 1 << 29;
+
 bool w4a8_layout(int64_t N, int64_t K, awq::W4a8Layout* L) {
-  if (N <= 0 || K <= 0 || K % kGroup != 0 || N > INT64_MAX - 15) return false;
+  if (N <= 0 || N > kMaxN || K <= 0 || K % kGroup != 0) return false;
   const int64_t rows = awq::w4a8_tiles(N) * 16;
-  if (mul3(rows, K, 1) < 0 || rows > INT64_MAX / 8 || mul3(rows, K, 1) > INT64_MAX / 2) return false;
+  if (mul3(rows, K, 2) < 0) return false;
   L->steps = align_up((size_t)(rows * (K / 2)));
   L->powers = L->steps + align_up((size_t)(rows * (K / kGroup) * 4));
   L->total = L->powers + align_up((size_t)(rows * 4));
   return true;
+}
+
+// The sizes of a product of M tokens, as the plan's arithmetic and the launches take them.
+bool w4a8_sizes(int64_t M, int64_t N, int64_t K, awq::W4a8Layout* L) {
+  return M > 0 && w4a8_layout(N, K, L) && M < kMaxTokenTiles && M * ((N + 255) / 256) < kMaxTokenTiles &&
+         mul3(M, K, 1) >= 0;
 }
 
 }  // namespace
@@ -137,7 +146,7 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
 
 AWQ_API size_t awq_w4a8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   awq::W4a8Layout L;
-  if (M <= 0 || !w4a8_layout(N, K, &L) || mul3(M, K, 1) < 0) return 0;
+  if (!w4a8_sizes(M, N, K, &L)) return 0;
   return awq::w4a8_workspace(M, K, N);
 }
 
@@ -150,7 +159,7 @@ AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M
   if (sums32) y_dtype &= ~AWQ_W4A8_SUMS_F32;
   if (!code_type(x_dtype) || !float_type(y_dtype) || group != kGroup) return AWQ_ERR_UNSUPPORTED;
   awq::W4a8Layout L;
-  if (!w4a8_layout(N, K, &L)) return AWQ_ERR_SHAPE;
+  if (!w4a8_sizes(M, N, K, &L)) return AWQ_ERR_SHAPE;
   int st = check_rows(Xq, x_dtype, M, K, ldx);
   if (st == AWQ_OK) st = check_rows(Y, y_dtype, M, N, ldy);
   if (st != AWQ_OK) return st;

@@ -1021,7 +1021,7 @@ template <int KIND, int TM>
 hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
   const int64_t G = a.K / kGroup, Gp = padded_groups(a.K), pieces = a.M * Gp * 8;
   const int64_t mt = (a.M + 16 * TM - 1) / (16 * TM), nt = (a.N + kTileN - 1) / kTileN;
-  if ((pieces + 255) / 256 > 0x7fffffff || mt * nt > 0x7ffffff) return hipErrorInvalidValue;
+  if ((pieces + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
   w4a8_sums_kernel<KIND != kInt8><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
       static_cast<const uint8_t*>(a.x), a.M, a.ldx, G, Gp, sums);
   w4a8_tile_kernel<KIND, TM><<<(unsigned)((mt * nt + 7) / 8 * 8), 256, 0, st>>>(a, sums, Gp, (int)mt, (int)nt);

@@ -130,3 +130,19 @@ def test_python_refusals_need_no_gpu():
 def test_w4a8_sums_flag(L, yt, status):
     """The flag goes with either result type (these calls get as far as the missing workspace) and with nothing else."""
     assert w4a8(L, M=8260, ws=None, wsb=0, yt=yt) == status
+
+
+@pytest.mark.parametrize("m,k,n", [(1 << 38, 128, 1 << 40), (1 << 37, 128, 1 << 40), (1 << 62, 128, 16), (1 << 29, 128, 16),
+                                   (1 << 28, 128, 512), (1 << 28, 128, 257), (4, 128, (1 << 27) + 1), (1 << 61, 128, 1 << 61)])
+def test_product_sizes_beyond_a_launch(L, m, k, n):
+    """Products of sizes whose tile counts leave int64 (a count of 0 ended the process in a division) or a launch's
+    threads are refused."""
+    assert L.awq_w4a8_workspace_bytes(m, k, n) == 0
+    assert w4a8(L, M=m, K=k, ldx=k, N=n, ldy=n) == SHAPE
+
+
+def test_largest_product_sizes(L):
+    assert L.awq_w4a8_workspace_bytes((1 << 29) - 1, 128, 256) == ((1 << 29) - 1) * 8 * 4
+    assert L.awq_w4a8_workspace_bytes((1 << 28) - 1, 128, 512) == ((1 << 28) - 1) * 8 * 4
+    assert L.awq_w4a8_weight_bytes(1 << 27, 128) == (1 << 27) * (64 + 4 + 4) and L.awq_w4a8_weight_bytes((1 << 27) + 1, 128) == 0
+    assert weight(L, N=(1 << 27) + 1, K=128, wb=1 << 60) == SHAPE
