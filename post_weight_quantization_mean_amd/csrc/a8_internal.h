@@ -9,6 +9,12 @@ namespace awq {
 constexpr int kF32 = 0, kBf16 = 1, kI8 = 2, kE4m3 = 3, kNoOperand = -1;
 constexpr int kActNone = 2;
 
+// Blocks of a kernel that strides over its grid: as many as asked for, but fewer than 2^32 threads, a launch's limit.
+inline unsigned blocks_of(int64_t blocks, int threads) {
+  const int64_t most = 0xffffffffLL / threads;
+  return (unsigned)(blocks < most ? blocks : most);
+}
+
 // ---- row operators (rmsnorm, act_mul) ----------------------------------------------------
 struct RowArgs {
   const void* x;      // [M, K], ldx

@@ -476,19 +476,19 @@ __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
   }
 }
 
-unsigned grid_of(int64_t rows) { return (unsigned)(rows < 0x40000000 ? rows : 0x40000000); }
 
 template <int OP, int XT, int BT, bool ALIGNED>
 void launch_rows_as(const RowArgs& a, hipStream_t st) {
   const int64_t units = a.K / 8;
 #define AWQ_ROWS(WV, UV) \
-  rows_kernel<OP, XT, BT, WV, UV, ALIGNED><<<grid_of(WV == 1 ? (a.M + 3) / 4 : a.M), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
+  rows_kernel<OP, XT, BT, WV, UV, ALIGNED> \
+      <<<blocks_of(WV == 1 ? (a.M - 1) / 4 + 1 : a.M, WV == 1 ? 256 : 64 * WV), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
   // The fewest registers that hold the row: few units per lane leave more rows in flight, and lanes without a
   // unit read for nothing (4096 rows, silu gate, K = 14336, bf16 -> e4m3: 4 waves x 8 units 68.6 us, 4 x 7 58.7,
   // 8 x 4 53.9, 16 x 2 53.1; K = 4096, rmsnorm: 1 x 8 22.8 us, 4 x 2 21.2;
   // 1000 rows of 20480, rmsnorm: 16 x 4 55.6 us, 16 x 3 32.6).  Rows of any alignment take the steps that are kept.
   if (units > 16 * 64 * 4) {
-    rows_any_kernel<OP, XT, BT><<<grid_of(a.M), 1024, 0, st>>>(a);
+    rows_any_kernel<OP, XT, BT><<<blocks_of(a.M, 1024), 1024, 0, st>>>(a);
   } else if (units <= 128) {
     AWQ_ROWS(1, 2);
   } else if (a.M <= 256 && units <= 2048) {

@@ -739,3 +739,22 @@ def test_act_mul_divides_by_s_to_the_ends_of_its_range(awq, K, out):
     want = f64(x) / f64(s)[None, :]
     y = f64(awq.act_mul(x.to(DEV), None, s.to(DEV), "none", dtype=out))
     assert np.all(np.abs(y - want) <= (8 * U + HALF[out]) * np.abs(want))
+
+
+def test_rows_beyond_one_launch(awq):
+    """2^26 + 5 short rows: more than a grid of 2^32 threads holds at four rows per 256 of them, for both operators."""
+    M, K = 2 ** 26 + 5, 8
+    banner(f"rows M={M} K={K}")
+    x = torch.zeros((M, K), dtype=BF16, device=DEV)
+    some = [0, 1, 12345, 2 ** 26 - 5, 2 ** 26 - 4, 2 ** 26 - 1, 2 ** 26, M - 1]
+    small = rand((len(some), K), BF16, 108)
+    x[some] = small.to(DEV)
+    g = (rand((K,), F32, 109) * 0.1 + 1)
+    res = awq.rmsnorm(x, g.to(DEV), dtype=I8)
+    _, want = a8.rmsnorm(f64(small), None, f64(g), 1e-6)
+    check(awq.Act8(res.q[some].cpu(), res.scale[some].cpu()), want, 72 * U)
+    assert int((res.scale > 1e-20).sum()) == len(some) and int((res.q != 0).any(1).sum()) == len(some)
+    del res
+    y = awq.act_mul(x, None, None, "silu", dtype=BF16)
+    check_stored(y[some].cpu(), a8.act_mul(f64(small), None, None, "silu"), act_tol(small, "silu", BF16, None, None))
+    assert int((y != 0).any(1).sum()) == len(some)
