@@ -38,24 +38,25 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
 }
 
 // ---- the weight's layout --------------------------------------------------------------------------
-// One thread per word of the laid-out codes.
+// A thread per word of the laid-out codes (several from 2^32 words on).
 __global__ __launch_bounds__(256) void w4a8_codes_kernel(const uint32_t* __restrict__ qweight, int64_t N, int64_t K,
                                                          int64_t words, uint32_t* __restrict__ codes) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= words) return;
-  const int64_t G = K / kGroup, tg = i / 256;
-  const int l = (int)(i % 256) / 4, w = (int)(i % 4);
-  const int64_t n = (tg / G) * 16 + l % 16, k = (tg % G) * kGroup + 16 * (l / 16) + 64 * (w / 2) + 8 * (w % 2);
-  uint32_t out = 0;
-  if (n < N) {
-    const uint32_t q = qweight[n * (K / 8) + k / 8];
+  const int64_t G = K / kGroup;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) {
+    const int64_t tg = i / 256;
+    const int l = (int)(i % 256) / 4, w = (int)(i % 4);
+    const int64_t n = (tg / G) * 16 + l % 16, k = (tg % G) * kGroup + 16 * (l / 16) + 64 * (w / 2) + 8 * (w % 2);
+    uint32_t out = 0;
+    if (n < N) {
+      const uint32_t q = qweight[n * (K / 8) + k / 8];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      out |= ((q >> (4 * b)) & 15u) << (8 * b);
-      out |= ((q >> (4 * b + 16)) & 15u) << (8 * b + 4);
+      for (int b = 0; b < 4; ++b) {
+        out |= ((q >> (4 * b)) & 15u) << (8 * b);
+        out |= ((q >> (4 * b + 16)) & 15u) << (8 * b + 4);
+      }
     }
+    codes[i] = out;
   }
-  codes[i] = out;
 }
 
 // Sixteen threads per channel: the power of two that takes its largest step into [2^10, 2^11) (there a step
@@ -351,32 +352,32 @@ hipError_t launch_stream(const W4a8Args& a, int tt, hipStream_t st) {
 template <bool E4M3>
 __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restrict__ x, int64_t M, int64_t ldx,
                                                         int64_t G, int64_t Gp, uint32_t* __restrict__ sums) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 8;
   const int piece = threadIdx.x & 7;
-  if (i >= M * Gp) return;
-  const int64_t m = i / Gp, g = i - m * Gp;
-  float s = 0.0f;
-  if (g < G) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ldx + g * kGroup + 16 * piece);
-    if constexpr (E4M3) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 8; i < M * Gp; i += (int64_t)gridDim.x * 32) {
+    const int64_t m = i / Gp, g = i - m * Gp;
+    float s = 0.0f;
+    if (g < G) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + m * ldx + g * kGroup + 16 * piece);
+      if constexpr (E4M3) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(v[d], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(v[d], true);
-        s += (a[0] + a[1]) + (b[0] + b[1]);
+        for (int d = 0; d < 4; ++d) {
+          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(v[d], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(v[d], true);
+          s += (a[0] + a[1]) + (b[0] + b[1]);
+        }
+      } else {
+        int t = 0;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) t = __builtin_amdgcn_sdot4((int)v[d], 0x01010101, t, false);
+        s = (float)t;
       }
-    } else {
-      int t = 0;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) t = __builtin_amdgcn_sdot4((int)v[d], 0x01010101, t, false);
-      s = (float)t;
     }
-  }
-  s += dpp<kDppXor1>(s);
-  s += dpp<kDppXor2>(s);
-  s += dpp<kDppHalfMirror>(s);
-  if (piece == 0) {
-    const uint16_t hi = f2h(s);
-    sums[i] = hi | (uint32_t)f2h(s - h2f(hi)) << 16;
+    s += dpp<kDppXor1>(s);
+    s += dpp<kDppXor2>(s);
+    s += dpp<kDppHalfMirror>(s);
+    if (piece == 0) {
+      const uint16_t hi = f2h(s);
+      sums[i] = hi | (uint32_t)f2h(s - h2f(hi)) << 16;
+    }
   }
 }
 
@@ -1021,8 +1022,7 @@ template <int KIND, int TM>
 hipError_t launch_tile(const W4a8Args& a, uint32_t* sums, hipStream_t st) {
   const int64_t G = a.K / kGroup, Gp = padded_groups(a.K), pieces = a.M * Gp * 8;
   const int64_t mt = (a.M + 16 * TM - 1) / (16 * TM), nt = (a.N + kTileN - 1) / kTileN;
-  if ((pieces + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
-  w4a8_sums_kernel<KIND != kInt8><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(
+  w4a8_sums_kernel<KIND != kInt8><<<blocks_of((pieces + 255) / 256, 256), 256, 0, st>>>(
       static_cast<const uint8_t*>(a.x), a.M, a.ldx, G, Gp, sums);
   w4a8_tile_kernel<KIND, TM><<<(unsigned)((mt * nt + 7) / 8 * 8), 256, 0, st>>>(a, sums, Gp, (int)mt, (int)nt);
   return hipGetLastError();
@@ -1048,8 +1048,7 @@ hipError_t launch_kind(const W4a8Args& a, void* ws, hipStream_t st) {
 hipError_t launch_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros, int64_t N,
                               int64_t K, uint32_t* codes, uint32_t* steps, float* powers, hipStream_t st) {
   const int64_t rows = w4a8_tiles(N) * 16, words = rows * (K / 8);
-  if ((words + 255) / 256 > 0x7fffffff) return hipErrorInvalidValue;
-  w4a8_codes_kernel<<<(unsigned)((words + 255) / 256), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(qweight), N, K,
+  w4a8_codes_kernel<<<blocks_of((words + 255) / 256, 256), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(qweight), N, K,
                                                                      words, codes);
   w4a8_steps_kernel<<<(unsigned)w4a8_tiles(N), 256, 0, st>>>(scales, zeros, N, K / kGroup, steps, powers);
   return hipGetLastError();

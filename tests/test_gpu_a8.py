@@ -758,3 +758,39 @@ def test_rows_beyond_one_launch(awq):
     y = awq.act_mul(x, None, None, "silu", dtype=BF16)
     check_stored(y[some].cpu(), a8.act_mul(f64(small), None, None, "silu"), act_tol(small, "silu", BF16, None, None))
     assert int((y != 0).any(1).sum()) == len(some)
+
+
+def test_w4a8_row_sums_beyond_one_launch(awq):
+    """2^26 + 70 tokens of one group: eight threads for each of eight (padded) groups a token are past 2^32."""
+    M, K, N = 2 ** 26 + 70, 128, 5
+    banner(f"w4a8 M={M} K={K} N={N}")
+    art = artefact(N, K, 110)
+    some = [0, 1, 777777, 2 ** 25 + 1, 2 ** 26 - 1, 2 ** 26, 2 ** 26 + 1, M - 1]
+    q, sc = codes(len(some), K, I8, 111)
+    X = torch.zeros((M, K), dtype=I8, device=DEV)
+    X[some] = q.to(DEV)
+    scale = torch.ones(M, device=DEV)
+    scale[some] = sc.to(DEV)
+    Y = awq.w4a8(awq.Act8(X, scale), on_gpu(awq, art))
+    check_product(Y[some].cpu(), q, sc, art)
+    assert int((Y != 0).any(1).sum()) == len(some)
+
+
+def test_w4a8_largest_weight(awq):
+    """2^21 channels of 16384: 2^32 words of codes, more than the threads of a launch, at offsets past 32 bits."""
+    N, K = 2 ** 21, 16384
+    banner(f"w4a8 N={N} K={K}")
+    some = [0, 17, 2 ** 18 + 3, 2 ** 20, 2 ** 20 + 1, N - 16, N - 1]
+    art = artefact(len(some), K, 112)
+    qw = torch.zeros((N, K // 8), dtype=torch.int32, device=DEV)
+    scales, zeros = (torch.zeros((N, K // 128), dtype=torch.float16, device=DEV) for _ in range(2))
+    qw[some] = torch.from_numpy(art["qweight"]).to(DEV)
+    scales[some], zeros[some] = (torch.from_numpy(art[k].view(np.float16)).to(DEV) for k in ("scales", "zeros"))
+    w = awq.w4a8_weight(qw, scales, zeros)
+    del qw, scales, zeros
+    q, sc = codes(3, K, I8, 113)
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), w)
+    check_product(Y[:, some].cpu(), q, sc, art)
+    assert int((Y != 0).any(0).sum()) <= len(some)
+    del w, Y
+    torch.cuda.empty_cache()
