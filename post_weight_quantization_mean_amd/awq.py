@@ -42,7 +42,7 @@ AWQ_DTYPE_I8 = 2
 AWQ_DTYPE_E4M3 = 3
 
 _lib = None
-_a8 = None  # the native binding of the 8-bit activation calls, once the library is loaded
+_a8 = None  # the native binding of the 8-bit activation calls, once one of them ran
 
 
 class AwqError(RuntimeError):
@@ -123,22 +123,24 @@ def lib() -> ctypes.CDLL:
         L.awq_w4a8.argtypes = [vp, ci, vp, i64, i64, i64, vp, i64, i32, vp, ci, i64, vp, sz, vp]
         if L.awq_abi_version() != 8:
             raise ImportError("libawq ABI version mismatch")
-        _bind(L)
         _lib = L
     return _lib
 
 
-def _bind(L: ctypes.CDLL) -> None:
-    """Load the native binding of the calls that run once per layer and token and hand it L's functions."""
-    global _a8
-    from . import _a8 as binding
-    names = ("awq_rmsnorm", "awq_act_mul", "awq_w4a8", "awq_w4a8_weight_bytes", "awq_w4a8_workspace_bytes")
-    binding.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Act8, AwqError)
-    _a8 = binding
-
-
 def _bound():
-    lib()
+    """The native binding of the calls that run once per layer and token (``_a8.so``), handed the library's
+    functions.  Loaded by the first of those calls: it fits one interpreter and torch only, and nothing else needs it."""
+    global _a8
+    if _a8 is None:
+        L = lib()
+        try:
+            from . import _a8 as binding
+        except ImportError as e:
+            raise ImportError("rmsnorm, act_mul and w4a8 need _a8.so, built for this interpreter and torch "
+                              f"(python -m post_weight_quantization_mean_amd.build): {e}") from e
+        names = ("awq_rmsnorm", "awq_act_mul", "awq_w4a8", "awq_w4a8_weight_bytes", "awq_w4a8_workspace_bytes")
+        binding.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Act8, AwqError)
+        _a8 = binding
     return _a8
 
 

@@ -2,6 +2,8 @@
 and every argument error is reported before any HIP call (no compute call is made here)."""
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -146,3 +148,31 @@ def test_largest_product_sizes(L):
     assert L.awq_w4a8_workspace_bytes((1 << 28) - 1, 128, 512) == ((1 << 28) - 1) * 8 * 4
     assert L.awq_w4a8_weight_bytes(1 << 27, 128) == (1 << 27) * (64 + 4 + 4) and L.awq_w4a8_weight_bytes((1 << 27) + 1, 128) == 0
     assert weight(L, N=(1 << 27) + 1, K=128, wb=1 << 60) == SHAPE
+
+
+def test_other_calls_need_no_native_binding():
+    """Without _a8.so (absent, or built for another interpreter) the library still loads and serves what it served
+    before; the calls that need the module say so, and run once it is there."""
+    code = """
+import sys, torch
+name = "post_weight_quantization_mean_amd._a8"
+sys.modules[name] = None  # the import system's mark of a module that cannot be imported
+from post_weight_quantization_mean_amd import awq
+assert awq.lib().awq_abi_version() == 8 and awq.search_workspace_bytes(64, 128, 128) > 0
+assert awq.w4a8_weight_bytes(16, 128) == 1536
+x, g = torch.zeros(2, 128), torch.ones(128)
+for call in (lambda: awq.rmsnorm(x, g), lambda: awq.act_mul(x)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_a8.so" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+del sys.modules[name]
+try:
+    awq.rmsnorm(x, g)
+except ValueError as e:
+    print("bound:", e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "bound: X must be a 2-D device tensor" in r.stdout, r.stdout + r.stderr
