@@ -80,13 +80,13 @@ def build(verbose: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=4) as pool:
         binding = pool.submit(build_binding)
         objs = list(pool.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    binding.result()  # its failure is raised behind the library, which needs no binding
     return LIB
 
 

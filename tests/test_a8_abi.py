@@ -176,3 +176,17 @@ except ValueError as e:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "bound: X must be a 2-D device tensor" in r.stdout, r.stdout + r.stderr
+
+
+def test_library_is_linked_though_the_binding_fails(tmp_path, monkeypatch):
+    from post_weight_quantization_mean_amd import build
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libawq.so"))
+    monkeypatch.setattr(build, "SOURCES", ["fold.hip"])
+
+    def fails():
+        raise RuntimeError("g++ failed")
+    monkeypatch.setattr(build, "build_binding", fails)
+    with pytest.raises(RuntimeError, match=r"g\+\+ failed"):
+        build.build()
+    assert (tmp_path / "libawq.so").exists()
