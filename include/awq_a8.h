@@ -98,7 +98,8 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  * unit's own sum: at most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more
  * than a bf16 rounding where one large code with q = z stands beside small ones) and then in fp32.
  * y_dtype BF16 | AWQ_W4A8_SUMS_F32 sums in fp32 as for an F32 Y, at half the matrix rate; with I8 or an F32 Y
- * the flag changes nothing.  The steps and the sum over groups are fp32; Y is rounded once.
+ * the flag changes nothing.  The sums z multiplies are within 2^-23 of fp32's.  The steps and the sum over groups
+ * are fp32; Y is rounded once.
  *   Xq      [M, K] of x_dtype I8 or E4M3, row stride ldx, 16-byte aligned rows
  *   xscale  fp32 [M]
  *   wt      as written by awq_w4a8_weight for the same N and K

@@ -347,8 +347,11 @@ hipError_t launch_stream(const W4a8Args& a, int tt, hipStream_t st) {
 }
 
 // ---- many tokens: tiles -----------------------------------------------------------------------------
-// sums[m][g]: sum of row m's codes of group g as two fp16 (high, then the rest: 22 bits; an int8 sum is
-// exact), zero for g in G .. Gp - 1.  Eight lanes per group, 16 bytes each.
+// sums[m][g]: sum of row m's codes of group g, formed in fp32 and kept as two fp16, high = rne(s) and low =
+// rne(s - high), zero for g in G .. Gp - 1.  high leaves at most 2^-11 of s's binade, low 2^-12 of what high left:
+// s to 2^-23, twice fp32's own half step (an int8 sum, and an e4m3 sum of up to 23 bits, is exact).  A third part would
+// hold all 24 bits, for one more round of products every eight groups and twice the workspace; each e4m3 sum of
+// 128 products beside it rounds many times that.  Eight lanes per group, 16 bytes each.
 template <bool E4M3>
 __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restrict__ x, int64_t M, int64_t ldx,
                                                         int64_t G, int64_t Gp, uint32_t* __restrict__ sums) {
@@ -394,7 +397,7 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 // on the steps' multiply-adds (int8: 16); unpacking adds 12 instructions per channel tile and wave,
 // spread over TM products.  The zero points would cost as many multiply-adds
 // again; their sum over groups is a product of its own, sum_g sums[m, g] (D z)[n, g], and runs on the matrix
-// cores in fp16 with both operands as high and low parts (sums 22 bits, D z 15: exact), one
+// cores in fp16 with both operands as high and low parts (sums to 2^-23, D z 15 bits: exact), one
 // instruction of 16 cycles for eight groups.
 //
 // 4096 x 4096 -> 28672: e4m3 440 us (2.2 PFLOP/s), int8 484 (2.0).  A loop of nothing but such products and

@@ -794,3 +794,26 @@ def test_w4a8_largest_weight(awq):
     assert int((Y != 0).any(0).sum()) <= len(some)
     del w, Y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [5, 40, 300, 8260])
+@pytest.mark.parametrize("xt", [I8, E4M3])
+def test_w4a8_row_sums_of_24_bits(awq, M, xt):
+    """Codes q of 0 leave -z sum x alone.  Sums of 24 significant bits (e4m3: 64 times 448 and odd multiples of 2^-9):
+    the tiles' two fp16 parts keep them to 2 units of 2^-24; products, power, scale and result round four times more."""
+    K, N = 128, 33
+    z = np.resize([1.0, 2.0, 4.0, 8.0, 15.0], (N, 1)).astype(np.float16)
+    art = dict(qweight=np.zeros((N, K // 8), np.int32), scales=np.ones((N, 1), np.float16), zeros=z)
+    rng = np.random.default_rng(114)
+    if xt == E4M3:
+        v = torch.from_numpy(rng.integers(1, 8, (M, K)) * 2.0 ** -9)
+        v[:, ::2] = 448.0
+    else:
+        v = torch.from_numpy(rng.integers(-127, 128, (M, K)).astype(np.float64))
+    q = v.to(xt)
+    assert torch.equal(q.double(), v)
+    sc = torch.ones(M)
+    w = awq.w4a8_weight(*[torch.from_numpy(art[k]).to(DEV) for k in ("qweight", "scales", "zeros")])
+    Y = f64(awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), w))
+    want = -v.sum(1).numpy()[:, None] * z.astype(np.float64).T
+    assert np.all(np.abs(Y - want) <= 6 * U * np.abs(want))
