@@ -2,6 +2,7 @@
 #pragma once
 
 #include "awq_internal.h"
+#include "w4a8_plan.h"
 
 namespace awq {
 
@@ -37,7 +38,6 @@ hipError_t launch_act_mul(const RowArgs& a, int x_type, bool vec, hipStream_t st
 struct W4a8Layout {
   size_t steps, powers, total;  // byte offsets of the parts behind the codes
 };
-__host__ __device__ inline int64_t w4a8_tiles(int64_t N) { return (N + 15) / 16; }
 struct W4a8Args {
   const void* x;
   const float* xscale;

@@ -1,0 +1,98 @@
+"""Which kernel the W4A8 product takes by size (CPU): the GPU tests' shapes together reach every one, each kind of sum and
+each shape of block, so that a change of the plan's costs cannot leave one untested unseen."""
+import itertools
+import os
+import subprocess
+
+import pytest
+import torch
+
+from tests import test_gpu_a8 as gpu
+from tests.conftest import ROOT
+
+CSRC = os.path.join(ROOT, "post_weight_quantization_mean_amd", "csrc")
+STREAM, SPLIT, TILE = 0, 1, 2
+PROGRAM = """
+#include <cstdio>
+
+#include "w4a8_plan.h"
+
+int main() {
+  long long m, k, n;
+  while (std::scanf("%lld %lld %lld", &m, &k, &n) == 3) {
+    const awq::Plan p = awq::w4a8_plan(m, k, n);
+    std::printf("%d %d %d %d %d %d\\n", p.path, p.tm, p.splits, p.per_split, p.ct, p.waves);
+  }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(PROGRAM)
+    subprocess.run([os.environ.get("CXX") or "g++", "-std=c++17", "-I", CSRC, str(d / "plan.cpp"), "-o", str(d / "plan")],
+                   check=True, timeout=120)
+
+    def ask(shapes):
+        text = "\n".join("%d %d %d" % s for s in shapes)
+        out = subprocess.run([str(d / "plan")], input=text, capture_output=True, text=True, check=True, timeout=60).stdout
+        return [tuple(map(int, line.split())) for line in out.splitlines()]
+    return ask
+
+
+def parameters(test):
+    """(values of one parametrize mark by name) of a test function."""
+    marks = [m for m in test.pytestmark if m.name == "parametrize"]
+    return {m.args[0]: list(m.args[1]) for m in marks}
+
+
+def cases():
+    """((M, K, N), kind of sum) of every product that a GPU test compares with the definition."""
+    for test in (gpu.test_w4a8, gpu.test_w4a8_tiles, gpu.test_w4a8_some_tokens, gpu.test_w4a8_wide_and_split):
+        p = parameters(test)
+        for shape, (xt, yt) in itertools.product(p["M,K,N"], p["xt,yt"]):
+            yield shape, "int8" if xt == torch.int8 else "fast" if yt == torch.bfloat16 else "wide"
+
+
+def test_every_kernel_is_reached(plan):
+    got = list(cases())
+    seen = set()
+    for (shape, kind), (path, tm, splits, per, ct, waves) in zip(got, plan([s for s, _ in got])):
+        G = shape[1] // 128
+        if path == STREAM:
+            seen.add((kind, STREAM, tm, ct, waves))
+        elif path == SPLIT:
+            seen.add((kind, SPLIT, tm, "parts" if splits > 1 else "whole"))
+            seen.add((kind, SPLIT, tm, "odd" if per % 2 else "even"))
+            if G % per:
+                seen.add((kind, SPLIT, tm, "fewer in the last"))
+        else:
+            tm = 4 if kind == "wide" else tm  # the fp32 sums of e4m3 codes have 64-token tiles only
+            seen.add((kind, TILE, tm, G % 4))
+    want = set()
+    for kind in ("int8", "fast", "wide"):
+        want |= {(kind, STREAM, 1, 1, 16), (kind, STREAM, 1, 2, 8)}
+        want |= {(kind, STREAM, 2, *b) for b in ((2, 8), (3, 8), (4, 8), (3, 4), (4, 4))}
+        want |= {(kind, SPLIT, tm, x) for tm in (2, 4) for x in ("parts", "odd", "even", "fewer in the last")}
+        want.add((kind, SPLIT, 2, "whole"))
+        want |= {(kind, TILE, 4, r) for r in range(4)}
+        if kind != "wide":
+            want |= {(kind, TILE, 8, r) for r in (0, 1, 2, 3)}
+    assert want <= seen, sorted(map(str, want - seen))
+
+
+def test_plan_is_sound(plan):
+    """Over a grid of sizes: every block of a split has a group, splits cover the groups once, blocks have their limits."""
+    shapes = [(m, 128 * g, n) for m in (1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 100, 128, 129, 256, 257, 511, 1000, 4096, 100000)
+              for g in (1, 2, 3, 7, 8, 9, 31, 32, 86, 112, 500) for n in (1, 16, 17, 255, 256, 257, 4096, 5104, 5105, 28672, 200001)]
+    for (m, k, n), (path, tm, splits, per, ct, waves) in zip(shapes, plan(shapes)):
+        G = k // 128
+        assert path in (STREAM, SPLIT, TILE)
+        if path == STREAM:
+            assert m <= 256 and (tm, ct, waves) in {(1, 1, 16), (1, 2, 8), (2, 2, 8), (2, 3, 8), (2, 4, 8), (2, 3, 4), (2, 4, 4)}
+            assert (m <= 16) == (tm == 1)
+        elif path == SPLIT:
+            assert m > 16 and tm in (2, 4) and splits * per >= G > (splits - 1) * per
+        else:
+            assert m > 16 and tm in (4, 8)

@@ -817,3 +817,41 @@ def test_w4a8_row_sums_of_24_bits(awq, M, xt):
     Y = f64(awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), w))
     want = -v.sum(1).numpy()[:, None] * z.astype(np.float64).T
     assert np.all(np.abs(Y - want) <= 6 * U * np.abs(want))
+
+
+_artefacts = {}
+
+
+def kept_artefact(N, K, seed):
+    """``artefact``, packed once for the cases that share it."""
+    if (N, K, seed) not in _artefacts:
+        _artefacts.clear()
+        _artefacts[N, K, seed] = artefact(N, K, seed)
+    return _artefacts[N, K, seed]
+
+
+ALL_KINDS = [(I8, F32), (I8, BF16), (E4M3, F32), (E4M3, BF16)]
+
+# Up to 16 tokens through 320 and more channel tiles: blocks of two.  An odd number of tiles and of channels in the last
+# one, whole tiles; groups fewer than the eight waves, one more, more than two a wave.
+WIDE_SHAPES = [(1, 128, 5121), (5, 384, 5105), (16, 1152, 9001), (3, 2176, 5121), (1, 256, 28672), (16, 640, 5136)]
+# 64-token tiles that share their groups: groups per block even, odd, and fewer in the last one
+SPLIT64_SHAPES = [(130, 14336, 40), (517, 4096, 40), (600, 11008, 300), (519, 4224, 2049), (301, 8192, 2049),
+                  (259, 4224, 4100)]
+
+# whole tiles: groups that are multiples of four (64- and 128-token tiles), and 128-token tiles with two more
+MORE_TILE_SHAPES = [(8200, 512, 40), (4100, 1024, 300), (18521, 512, 520), (18521, 768, 516)]
+
+
+@pytest.mark.parametrize("xt,yt", ALL_KINDS)
+@pytest.mark.parametrize("M,K,N", WIDE_SHAPES + SPLIT64_SHAPES + MORE_TILE_SHAPES)
+def test_w4a8_wide_and_split(awq, M, K, N, xt, yt):
+    banner(f"w4a8 wide or split M={M} K={K} N={N} {xt} {yt}")
+    art = kept_artefact(N, K, 120)
+    q, sc = codes(M, K, xt, 121)
+    Y = torch.full((M + 2, N + 8), -7.0, dtype=yt, device=DEV)
+    w, a = on_gpu(awq, art), awq.Act8(q.to(DEV), sc.to(DEV))
+    awq.w4a8(a, w, out=Y[:M, :N])
+    check_tile(Y[:M, :N], q, sc, art)
+    assert torch.all(Y[M:] == -7.0) and torch.all(Y[:, N:] == -7.0)
+    assert torch.equal(awq.w4a8(a, w, dtype=yt), Y[:M, :N])
