@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "a8_internal.h"
+#include "rows8_plan.h"
 
 namespace awq {
 namespace {
@@ -479,38 +480,30 @@ __global__ __launch_bounds__(1024) void rows_any_kernel(const RowArgs a) {
 
 template <int OP, int XT, int BT, bool ALIGNED>
 void launch_rows_as(const RowArgs& a, hipStream_t st) {
-  const int64_t units = a.K / 8;
 #define AWQ_ROWS(WV, UV) \
   rows_kernel<OP, XT, BT, WV, UV, ALIGNED> \
       <<<blocks_of(WV == 1 ? (a.M - 1) / 4 + 1 : a.M, WV == 1 ? 256 : 64 * WV), WV == 1 ? 256 : 64 * WV, 0, st>>>(a)
-  // The fewest registers that hold the row: few units per lane leave more rows in flight, and lanes without a
-  // unit read for nothing (4096 rows, silu gate, K = 14336, bf16 -> e4m3: 4 waves x 8 units 68.6 us, 4 x 7 58.7,
-  // 8 x 4 53.9, 16 x 2 53.1; K = 4096, rmsnorm: 1 x 8 22.8 us, 4 x 2 21.2;
-  // 1000 rows of 20480, rmsnorm: 16 x 4 55.6 us, 16 x 3 32.6).  Rows of any alignment take the steps that are kept.
-  if (units > 16 * 64 * 4) {
+  const RowLayout l = row_layout(a.M, a.K, ALIGNED);
+  if (l.waves == 0) {
     rows_any_kernel<OP, XT, BT><<<blocks_of(a.M, 1024), 1024, 0, st>>>(a);
-  } else if (units <= 128) {
+  } else if (l.waves == 1) {
     AWQ_ROWS(1, 2);
-  } else if (a.M <= 256 && units <= 2048) {
-    // fewer rows than CUs: each spread over sixteen waves
-    if (units <= 1024) AWQ_ROWS(16, 1);
-    else AWQ_ROWS(16, 2);
-  } else if (ALIGNED && units <= 256) {
-    if constexpr (ALIGNED) AWQ_ROWS(4, 1);
-  } else if (units <= 512) {
+  } else if (l.waves == 4 && l.units == 2) {
     AWQ_ROWS(4, 2);
-  } else if (ALIGNED && units <= 768) {
-    if constexpr (ALIGNED) AWQ_ROWS(4, 3);
-  } else if (units <= 1024) {
+  } else if (l.waves == 4 && l.units == 4) {
     AWQ_ROWS(4, 4);
-  } else if (ALIGNED && units <= 1536) {
-    if constexpr (ALIGNED) AWQ_ROWS(8, 3);
-  } else if (units <= 2048) {
+  } else if (l.waves == 16 && l.units == 1) {
+    AWQ_ROWS(16, 1);
+  } else if (l.waves == 16 && l.units == 2) {
     AWQ_ROWS(16, 2);
-  } else if (units <= 3072) {
+  } else if (l.waves == 16 && l.units == 3) {
     AWQ_ROWS(16, 3);
-  } else {
+  } else if (l.waves == 16) {
     AWQ_ROWS(16, 4);
+  } else if constexpr (ALIGNED) {
+    if (l.waves == 4 && l.units == 1) AWQ_ROWS(4, 1);
+    else if (l.waves == 4) AWQ_ROWS(4, 3);
+    else AWQ_ROWS(8, 3);
   }
 #undef AWQ_ROWS
 }

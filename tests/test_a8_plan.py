@@ -15,11 +15,17 @@ STREAM, SPLIT, TILE = 0, 1, 2
 PROGRAM = """
 #include <cstdio>
 
+#include "rows8_plan.h"
 #include "w4a8_plan.h"
 
-int main() {
+int main(int argc, char**) {
   long long m, k, n;
   while (std::scanf("%lld %lld %lld", &m, &k, &n) == 3) {
+    if (argc > 1) {  // rows: the third number says whether they are aligned
+      const awq::RowLayout l = awq::row_layout(m, k, n != 0);
+      std::printf("%d %d\\n", l.waves, l.units);
+      continue;
+    }
     const awq::Plan p = awq::w4a8_plan(m, k, n);
     std::printf("%d %d %d %d %d %d\\n", p.path, p.tm, p.splits, p.per_split, p.ct, p.waves);
   }
@@ -34,9 +40,9 @@ def plan(tmp_path_factory):
     subprocess.run([os.environ.get("CXX") or "g++", "-std=c++17", "-I", CSRC, str(d / "plan.cpp"), "-o", str(d / "plan")],
                    check=True, timeout=120)
 
-    def ask(shapes):
+    def ask(shapes, *mode):
         text = "\n".join("%d %d %d" % s for s in shapes)
-        out = subprocess.run([str(d / "plan")], input=text, capture_output=True, text=True, check=True, timeout=60).stdout
+        out = subprocess.run([str(d / "plan"), *mode], input=text, capture_output=True, text=True, check=True, timeout=60).stdout
         return [tuple(map(int, line.split())) for line in out.splitlines()]
     return ask
 
@@ -96,3 +102,17 @@ def test_plan_is_sound(plan):
             assert m > 16 and tm in (2, 4) and splits * per >= G > (splits - 1) * per
         else:
             assert m > 16 and tm in (4, 8)
+
+
+def test_every_row_layout_is_reached(plan):
+    """Both operators, rows that start at multiples of 16 bytes and others, over the GPU tests' shapes (whose rows are
+    contiguous: they are aligned where K is a multiple of 8)."""
+    sizes = [(m, k, int(k % 8 == 0)) for m in (1, 256, 257, 5000) for k in range(1, 33100, 67)]
+    sizes += [(m, 8 * u, 1) for m in (1, 257) for u in range(1, 4200)]
+    every = {(a, *l) for (_, _, a), l in zip(sizes, plan(sizes, "rows"))}
+    assert len(every) == 11 + 8
+    for tests in ((gpu.test_rmsnorm, gpu.test_long_rows, gpu.test_rmsnorm_row_layouts),
+                  (gpu.test_act_mul, gpu.test_long_rows, gpu.test_act_mul_row_layouts)):
+        shapes = [(m, k, int(k % 8 == 0)) for t in tests for m, k in parameters(t)["M,K"]]
+        seen = {(a, *l) for (_, _, a), l in zip(shapes, plan(shapes, "rows"))}
+        assert every <= seen, sorted(every - seen)

@@ -855,3 +855,60 @@ def test_w4a8_wide_and_split(awq, M, K, N, xt, yt):
     check_tile(Y[:M, :N], q, sc, art)
     assert torch.all(Y[M:] == -7.0) and torch.all(Y[:, N:] == -7.0)
     assert torch.equal(awq.w4a8(a, w, dtype=yt), Y[:M, :N])
+
+
+# Every row layout, aligned and not, that the lists above leave out: four waves of one, two and four units, eight of three,
+# sixteen of two
+ROW_SHAPES = [(300, 2048), (257, 4096), (300, 8192), (300, 12000), (5, 8192), (300, 2001), (300, 5001), (300, 14333),
+              (2, 14333), (258, 20481), (2, 65543)]
+
+
+@pytest.mark.parametrize("M,K", ROW_SHAPES)
+@pytest.mark.parametrize("xt,rt,out", [(BF16, BF16, E4M3), (F32, BF16, I8), (BF16, None, BF16), (F32, F32, F32)])
+def test_rmsnorm_row_layouts(awq, M, K, xt, rt, out):
+    banner(f"rmsnorm layout M={M} K={K} {xt} {rt} {out}")
+    x, r = rand((M, K), xt, 130, 2.0), None if rt is None else rand((M, K), rt, 131, 3.0)
+    g = rand((K,), F32, 132) * 0.1 + 1
+    h, y = a8.rmsnorm(f64(x), None if r is None else f64(r), f64(g), 1e-6)
+    res = awq.rmsnorm(x.to(DEV), g.to(DEV), None if r is None else r.to(DEV), dtype=out)
+    if rt is not None:
+        res, hh = res
+        check_stored(hh, h, 2 * U)
+    check(res, y, 72 * U)
+
+
+@pytest.mark.parametrize("M,K", ROW_SHAPES)
+@pytest.mark.parametrize("xt,act,gate,scaled,out", [(BF16, "silu", True, False, E4M3), (F32, "gelu", True, True, I8),
+                                                    (BF16, "none", False, True, BF16), (F32, "silu", False, False, F32)])
+def test_act_mul_row_layouts(awq, M, K, xt, act, gate, scaled, out):
+    banner(f"act_mul layout M={M} K={K} {xt} {act} {gate} {scaled} {out}")
+    g, u = rand((M, K), xt, 133, 3.0), rand((M, K), xt, 134) if gate else None
+    s = torch.exp(0.3 * rand((K,), F32, 135)) if scaled else None
+    res = awq.act_mul(g.to(DEV), None if u is None else u.to(DEV), None if s is None else s.to(DEV), act, dtype=out)
+    want = a8.act_mul(f64(g), None if u is None else f64(u), None if s is None else f64(s), act)
+    check(res, want, act_tol(g, act, out, u, s))
+
+
+# across four and sixteen waves, with a tail, past the registers
+@pytest.mark.parametrize("M,K", [(300, 4096), (5, 4096), (300, 5001), (3, 5001), (3, 65543), (2, 65544)])
+@pytest.mark.parametrize("rt,out", [(BF16, I8), (F32, E4M3), (F32, BF16)])
+def test_rmsnorm_residual_in_place(awq, M, K, rt, out):
+    banner(f"rmsnorm in place M={M} K={K} {rt} {out}")
+    x, r = rand((M, K), BF16, 136), rand((M, K), rt, 137)
+    g = rand((K,), F32, 138) * 0.1 + 1
+    h, y = a8.rmsnorm(f64(x), f64(r), f64(g), 1e-6)
+    R = r.to(DEV)
+    res, hh = awq.rmsnorm(x.to(DEV), g.to(DEV), R, dtype=out, residual_out=R)
+    assert hh is R
+    check_stored(R, h, 2 * U)
+    check(res, y, 72 * U)
+
+
+@pytest.mark.parametrize("M,K", [(300, 8192), (5, 14336), (300, 5001), (2, 65544)])
+@pytest.mark.parametrize("which", ["gate", "factor"])
+def test_act_mul_in_place_of_either(awq, M, K, which):
+    g, u = rand((M, K), BF16, 139).to(DEV), rand((M, K), BF16, 140).to(DEV)
+    want = a8.act_mul(f64(g), f64(u), None, "silu")
+    tol = act_tol(g, "silu", BF16, None, None)
+    y = awq.act_mul(g, u, out=g if which == "gate" else u)
+    check_stored(y, want, tol)
