@@ -42,8 +42,9 @@ extern "C" {
  *          round(y / scale) to nearest even in the type, with
  *          scale = max(max_k |y|, 2^-100) / Q,  Q = 127 (I8) or 448 (E4M3)
  *   scale  fp32 [M] for an 8-bit Y, else ignored
- * Any K.  H = R aside, outputs overlap no input and not each other.  A row whose sum of squares
- * is not finite in fp32 (|h| around 1e19 and more, NaN, Inf) has y NaN.
+ * Any K.  H = R aside, outputs overlap no input and not each other (of this only exact starts are checked: Y on
+ * H, an output on gamma, or on an operand in another type or row stride, are AWQ_ERR_INVALID_ARG).  A row whose
+ * sum of squares is not finite in fp32 (|h| around 1e19 and more, NaN, Inf) has y NaN.
  * ------------------------------------------------------------------------------------- */
 AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const void* R,
                         int r_dtype, int64_t ldr, void* H, int64_t ldh, const void* gamma, int g_dtype,
@@ -107,6 +108,7 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each
+ * Y and ws overlap no input and not each other (an exact start is checked: AWQ_ERR_INVALID_ARG).
  * K is a multiple of 128; 128 rows of Xq and of Y span less than 2^31 bytes each; M ceil(N / 256) is below
  * 2^29 (AWQ_ERR_SHAPE; awq_w4a8_workspace_bytes is then 0).
  * ------------------------------------------------------------------------------------- */

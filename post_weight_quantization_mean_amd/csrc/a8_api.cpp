@@ -88,7 +88,14 @@ AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_
   if (st == AWQ_OK && H != nullptr) st = check_rows(H, r_dtype, M, K, ldh);
   if (st == AWQ_OK) st = check_out(Y, y_dtype, M, K, ldy, scale);
   if (st != AWQ_OK) return st;
-  if (H != nullptr && H == R && ldh != ldr) return AWQ_ERR_INVALID_ARG;
+  // an output exactly over an operand in another type or row stride: rows would overwrite other rows' operands
+  auto crossed = [](const void* p, int pt, int64_t pl, const void* q, int qt, int64_t ql) {
+    return p != nullptr && p == q && (pt != qt || pl != ql);
+  };
+  if (crossed(H, r_dtype, ldh, R, r_dtype, ldr) || crossed(H, r_dtype, ldh, X, x_dtype, ldx) ||
+      crossed(Y, y_dtype, ldy, X, x_dtype, ldx) || crossed(Y, y_dtype, ldy, R, r_dtype, ldr) ||
+      Y == H || Y == gamma || (H != nullptr && H == gamma))
+    return AWQ_ERR_INVALID_ARG;
   const bool vec = K % 8 == 0 && rows_aligned(X, x_dtype, ldx, 16) && aligned(gamma, 16) &&
                    (R == nullptr || rows_aligned(R, r_dtype, ldr, 16)) &&
                    (H == nullptr || rows_aligned(H, r_dtype, ldh, 16)) && out_vec(Y, y_dtype, ldy);
@@ -170,6 +177,7 @@ AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M
   const size_t need = awq_w4a8_workspace_bytes(M, K, N);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return AWQ_ERR_WORKSPACE;
   if (need > 0 && !aligned(ws, 16)) return AWQ_ERR_INVALID_ARG;
+  if (Y == Xq || Y == wt || Y == xscale || (need > 0 && (ws == Y || ws == Xq || ws == wt))) return AWQ_ERR_INVALID_ARG;
   const char* p = static_cast<const char*>(wt);
   awq::W4a8Args a{};
   a.x = Xq, a.xscale = xscale, a.y = Y;

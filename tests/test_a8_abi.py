@@ -190,3 +190,24 @@ def test_library_is_linked_though_the_binding_fails(tmp_path, monkeypatch):
     with pytest.raises(RuntimeError, match=r"g\+\+ failed"):
         build.build()
     assert (tmp_path / "libawq.so").exists()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(Y=2 * P, yt=BF16),                      # over H
+    dict(Y=2 * P),                               # the same in codes
+    dict(X=4 * P, Y=4 * P),                      # codes over X
+    dict(X=4 * P, Y=4 * P, yt=F32),
+    dict(X=4 * P, Y=4 * P, yt=BF16, ldy=512),    # X's type in another row stride
+    dict(R=4 * P, Y=4 * P),                      # codes over R
+    dict(X=4 * P, xt=F32, H=4 * P),              # H over X in another type
+    dict(X=4 * P, H=4 * P, ldh=512),
+    dict(gamma=4 * P, Y=4 * P), dict(gamma=4 * P, H=4 * P),
+])
+def test_rmsnorm_refuses_crossed_outputs(L, kw):
+    assert rmsnorm(L, **kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(Y=P, X=P), dict(Y=6 * P, wt=6 * P), dict(Y=6 * P, xs=6 * P),
+                                dict(M=8260, ws=2 * P, Y=2 * P), dict(M=8260, ws=2 * P, X=2 * P), dict(M=8260, ws=2 * P, wt=2 * P)])
+def test_w4a8_refuses_outputs_over_operands(L, kw):
+    assert w4a8(L, **{**dict(X=3 * P, xs=4 * P, wt=5 * P, Y=7 * P, ws=8 * P), **kw}) == INVALID
