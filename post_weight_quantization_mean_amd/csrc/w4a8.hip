@@ -61,8 +61,8 @@ __global__ __launch_bounds__(256) void w4a8_codes_kernel(const uint32_t* __restr
 }
 
 // Sixteen threads per channel: the power of two that takes its largest step into [2^10, 2^11) (there a step
-// times a zero point, at most 15 2^11, is a finite fp16, and only steps below 2^-25 of the largest lose
-// bits), then its steps and zero points.  (4096 channels of 112 groups: 6 us; one thread each: 39.)
+// times a zero point, at most 15 2^11, is a finite fp16, and only steps below 2^-24 of the largest, subnormal then,
+// lose bits), then its steps and zero points.  (4096 channels of 112 groups: 6 us; one thread each: 39.)
 __global__ __launch_bounds__(256) void w4a8_steps_kernel(const uint16_t* __restrict__ scales,
                                                          const uint16_t* __restrict__ zeros, int64_t N, int64_t G,
                                                          uint32_t* __restrict__ steps, float* __restrict__ powers) {
@@ -187,9 +187,11 @@ __device__ __forceinline__ i32x8 join(const u32x4 lo, const u32x4 hi) {
 // ---- few tokens: the weight as a stream ----------------------------------------------------------------
 // A block computes CT tiles of 16 channels for up to 16 TT tokens over all of K.  Its WV waves take the
 // groups in turn, D of them in flight in each wave, with fp32 sums of their own, which meet in LDS at the
-// end in wave order.  Bound: up to 16 tokens by the weight's bytes and the time until they flow (1 x 4096 -> 28672:
-// 12.5 us, 5.0 TB/s, what a copy reaches; 16 x 14336 -> 4096: 11.1 us, 2.8 TB/s, 256 blocks of seven groups a wave);
-// beyond, by the reads of X and the codes from L2, 4 KiB each per wave and group.  Sum x per token and group is one more product, with ones, in the layout of the
+// end in wave order.  Bound: up to 8 tokens by the weight's bytes and the time until they flow (1 x 4096 -> 28672:
+// 12.3 us, 5.1 TB/s, what a copy reaches; 1 and 5 x 14336 -> 4096: 8.0, 256 blocks of seven groups a wave); beyond, by
+// the reads of X from L2 too, 2 KiB per wave, group and 16 tokens: with every token's lanes reading the first token
+// instead, us, 16 x 14336 -> 4096 takes 7.9 for 10.8, 16 x 4096 -> 28672 12.4 / 15.2, 64 x 4096 -> 4096 5.3 / 7.1,
+// 101 x 4096 -> 6144 9.0 / 13.0, 256 x 4096 -> 4096 10.1 / 14.6.  Sum x per token and group is one more product, with ones, in the layout of the
 // sums it corrects.  Rows past the last token repeat it and are not stored.
 template <int KIND, int TT, int CT, int WV, int D>
 __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) {
@@ -401,8 +403,8 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(const W4a8Args p, con
   const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = (int)(p.K / kGroup);
   // Blocks go to the eight XCDs in turn; each XCD takes a contiguous run of tiles, which walk bands
-  // of four token tiles, so that the 32 tiles in work there are about four by eight and share their
-  // operands in the XCD's L2.
+  // of eight token tiles, so that the 64 tiles in work there (two blocks on each of 32 CUs) are about eight by eight
+  // and share their operands in the XCD's L2.
   const int total = mtiles * ntiles, per = (total + 7) / 8;
   const int id = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || id >= total) return;

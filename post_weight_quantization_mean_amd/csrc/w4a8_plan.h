@@ -40,8 +40,12 @@ inline StreamShape stream_shape(int64_t M, int64_t G, int64_t tiles) {
   return {4, 4, 3.2f + 0.356f * g * (b <= 384.0f ? 1.0f : b <= 512.0f ? b / 384.0f : b / 307.0f)};
 }
 
-// The costs are microseconds fitted to measurements (int8 and e4m3, K = 4096 and 14336, N = 4096 to 28672, 17 to
-// 640 tokens, weights from memory); what each path measured at the crossovers stands behind its line.
+// The costs are microseconds fitted to measurements (K = 4096 and 14336, N = 4096 to 28672, 17 to 640 tokens, weights
+// from memory), for the ratio of two paths rather than for themselves: a tile's 0.95 a group is int8's at K = 4096; at
+// K = 11008 int8 takes 0.84, and e4m3 with a bf16 result 0.70 at either, where the streams' estimates are high as much.
+// Stream against tile at their crossovers, us (int8; e4m3 -> bf16): 65 x 4096 -> 16641 26 / 32; 26 / 31 (stream taken),
+// 96 x 4096 -> 17000 30 / 32; 29 / 28 (stream), 65 x 11008 -> 17000 69 / 75; 68 / 65 (stream), 129 x 4096 -> 12288
+// 27 / 31; 27 / 26 (tile), 128 x 4096 -> 17000 39 / 33; 38 / 29 (tile), 192 x 4096 -> 12288 37 / 31; 38 / 26 (tile).
 inline Plan w4a8_plan(int64_t M, int64_t K, int64_t N) {
   const int64_t G = K / kW4a8Group, nt = (N + kTileN - 1) / kTileN;
   const int64_t tiles16 = w4a8_tiles(N);
