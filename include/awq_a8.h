@@ -22,8 +22,9 @@ extern "C" {
 #define AWQ_DTYPE_I8 2   /* int8, codes -127 .. 127 */
 #define AWQ_DTYPE_E4M3 3 /* e4m3 without infinities (OCP), |code| <= 448 */
 
-/* Or'ed into awq_w4a8's y_dtype: e4m3 codes are summed in fp32 for a BF16 Y too. */
-#define AWQ_W4A8_SUMS_F32 0x100
+/* Or'ed into awq_w4a8's y_dtype, at most one: how e4m3 codes are summed. */
+#define AWQ_W4A8_SUMS_F32 0x100    /* in fp32 */
+#define AWQ_W4A8_SUMS_MATRIX 0x200 /* by the matrix unit's own 8-bit products */
 
 /* Activations of awq_act_mul, beside awq.h's AWQ_ACT_GELU and AWQ_ACT_SILU. */
 #define AWQ_ACT_NONE 2
@@ -94,17 +95,20 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  * The W4A8 product:
  *   Y[m, n] = xscale[m] * sum_g scales[n, g] * sum_{k in g} Xq[m, k] (q[n, k] - zeros[n, g])
  * on the 8-bit matrix cores: a code q is an int8 byte as it stands, and as an e4m3 byte it is
- * exactly q 2^-9.  I8: the inner sums are exact integers.  E4M3: the products are exact; for an F32 Y
- * they are summed in fp32, for a BF16 Y sixteen at a time to 14 bits of the largest of them (the matrix
- * unit's own sum: at most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more
- * than a bf16 rounding where one large code with q = z stands beside small ones) and then in fp32.
- * y_dtype BF16 | AWQ_W4A8_SUMS_F32 sums in fp32 as for an F32 Y, at half the matrix rate; with I8 or an F32 Y
- * the flag changes nothing.  The sums z multiplies are within 2^-23 of fp32's.  The steps and the sum over groups
+ * exactly q 2^-9.  I8: the inner sums are exact integers.  E4M3: the products are exact, and a group's are
+ * summed
+ *   in fp32 for an F32 Y, and for a BF16 Y but for many tokens (at half the matrix rate);
+ *   by the matrix unit for a BF16 Y of many tokens: M > 16 and ceil(M / 64) ceil(N / 256) > 128, and not the blocks
+ *     of 32 tokens that up to 256 tokens may run in.  It adds sixteen at a time to 14 bits of the largest of
+ *     them: off by at most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more than a
+ *     bf16 rounding where one large code with q = z stands beside small ones.
+ * AWQ_W4A8_SUMS_F32 or AWQ_W4A8_SUMS_MATRIX in y_dtype ask for one of the two at any size; with I8 they
+ * change nothing.  The sums z multiplies are within 2^-23 of fp32's.  The steps and the sum over groups
  * are fp32; Y is rounded once.
  *   Xq      [M, K] of x_dtype I8 or E4M3, row stride ldx, 16-byte aligned rows
  *   xscale  fp32 [M]
  *   wt      as written by awq_w4a8_weight for the same N and K
- *   Y       [M, N] of y_dtype F32 or BF16 (with or without AWQ_W4A8_SUMS_F32), row stride ldy >= N
+ *   Y       [M, N] of y_dtype F32 or BF16 (and a flag, see above), row stride ldy >= N
  *   ws      device memory of at least awq_w4a8_workspace_bytes(M, K, N) bytes, 16-byte aligned
  *           (NULL where that is 0); nothing in it has to start at zero, and calls that may run at
  *           the same time need one each

@@ -162,8 +162,10 @@ AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M
                      size_t ws_bytes, awq_stream_t stream) {
   if (Xq == nullptr || xscale == nullptr || wt == nullptr || Y == nullptr || M <= 0 || N <= 0 || K <= 0)
     return AWQ_ERR_INVALID_ARG;
-  const bool sums32 = y_dtype >= 0 && (y_dtype & AWQ_W4A8_SUMS_F32) != 0;
-  if (sums32) y_dtype &= ~AWQ_W4A8_SUMS_F32;
+  int sums = awq::kSumsDefault;
+  if (y_dtype >= 0 && (y_dtype & ~0xff) == AWQ_W4A8_SUMS_F32) sums = awq::kSumsF32;
+  if (y_dtype >= 0 && (y_dtype & ~0xff) == AWQ_W4A8_SUMS_MATRIX) sums = awq::kSumsMatrix;
+  if (sums != awq::kSumsDefault) y_dtype &= 0xff;
   if (!code_type(x_dtype) || !float_type(y_dtype) || group != kGroup) return AWQ_ERR_UNSUPPORTED;
   awq::W4a8Layout L;
   if (!w4a8_sizes(M, N, K, &L)) return AWQ_ERR_SHAPE;
@@ -185,7 +187,7 @@ AWQ_API int awq_w4a8(const void* Xq, int x_dtype, const float* xscale, int64_t M
   a.steps = reinterpret_cast<const uint32_t*>(p + L.steps);
   a.powers = reinterpret_cast<const float*>(p + L.powers);
   a.M = M, a.K = K, a.N = N, a.ldx = ldx, a.ldy = ldy;
-  a.e4m3 = x_dtype == AWQ_DTYPE_E4M3, a.ybf16 = y_dtype == AWQ_DTYPE_BF16, a.sums32 = sums32;
+  a.e4m3 = x_dtype == AWQ_DTYPE_E4M3, a.ybf16 = y_dtype == AWQ_DTYPE_BF16, a.sums = sums;
   return map_hip(awq::launch_w4a8(a, ws, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -294,9 +294,11 @@ PyObject* w4a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ldy = row_stride(Y, "out", dev, M, N);
       if (a[5] != Py_None && want != Y.scalar_type()) value_error("dtype and out disagree");
     }
-    const int sums = PyObject_IsTrue(a[8]);
-    if (sums < 0) throw Raise{nullptr, ""};
-    const int yc = float_code(Y, "out") | (sums ? AWQ_W4A8_SUMS_F32 : 0);
+    int yc = float_code(Y, "out");
+    if (a[8] != Py_None) {
+      if (!PyBool_Check(a[8])) type_error("fp32_sums must be True, False or None");
+      yc |= a[8] == Py_True ? AWQ_W4A8_SUMS_F32 : AWQ_W4A8_SUMS_MATRIX;
+    }
     size_t need = lib.workspace_bytes(M, K, N);
     at::Tensor ws;
     if (need > 0) {

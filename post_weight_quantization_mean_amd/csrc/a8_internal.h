@@ -38,6 +38,7 @@ hipError_t launch_act_mul(const RowArgs& a, int x_type, bool vec, hipStream_t st
 struct W4a8Layout {
   size_t steps, powers, total;  // byte offsets of the parts behind the codes
 };
+constexpr int kSumsDefault = 0, kSumsF32 = 1, kSumsMatrix = 2;
 struct W4a8Args {
   const void* x;
   const float* xscale;
@@ -46,7 +47,8 @@ struct W4a8Args {
   const float* powers;
   void* y;
   int64_t M, K, N, ldx, ldy;
-  bool e4m3, ybf16, sums32;  // sums32: e4m3 codes summed in fp32 for a bf16 y too
+  bool e4m3, ybf16;
+  int sums;  // e4m3 codes: kSumsDefault, kSumsF32, kSumsMatrix
 };
 hipError_t launch_w4a8_weight(const int32_t* qweight, const uint16_t* scales, const uint16_t* zeros, int64_t N,
                               int64_t K, uint32_t* codes, uint32_t* steps, float* powers, hipStream_t st);

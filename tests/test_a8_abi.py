@@ -127,10 +127,10 @@ def test_python_refusals_need_no_gpu():
         awq.w4a8(awq.Act8(x.to(torch.int8), torch.ones(2)), awq.W4A8Weight(torch.zeros(8, dtype=torch.uint8), 2, 128))
 
 
-@pytest.mark.parametrize("yt,status", [(BF16 | 0x100, WS), (F32 | 0x100, WS), (I8 | 0x100, UNSUP), (BF16 | 0x200, UNSUP),
-                                       (-1, UNSUP), (-1 & ~0xff | BF16, UNSUP)])
+@pytest.mark.parametrize("yt,status", [(BF16 | 0x100, WS), (F32 | 0x100, WS), (I8 | 0x100, UNSUP), (BF16 | 0x200, WS),
+                                       (F32 | 0x200, WS), (BF16 | 0x300, UNSUP), (BF16 | 0x400, UNSUP), (-1, UNSUP), (-1 & ~0xff | BF16, UNSUP)])
 def test_w4a8_sums_flag(L, yt, status):
-    """The flag goes with either result type (these calls get as far as the missing workspace) and with nothing else."""
+    """Either flag goes with either result type (these calls get as far as the missing workspace), both or others with none."""
     assert w4a8(L, M=8260, ws=None, wsb=0, yt=yt) == status
 
 

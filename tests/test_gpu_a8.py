@@ -682,6 +682,8 @@ def test_w4a8_fp32_sums_flag_with_given_outputs(awq):
     assert awq.w4a8(a, w, out=y, fp32_sums=True) is y
     check_product(y, q, sc, art)
     assert torch.equal(awq.w4a8(a, w, fp32_sums=True), awq.w4a8(a, w))  # an fp32 result: the same sums
+    with pytest.raises(TypeError):
+        awq.w4a8(a, w, fp32_sums=1)
 
 
 # K: aligned units, a tail, less than a unit, past the registers
@@ -912,3 +914,45 @@ def test_act_mul_in_place_of_either(awq, M, K, which):
     tol = act_tol(g, "silu", BF16, None, None)
     y = awq.act_mul(g, u, out=g if which == "gate" else u)
     check_stored(y, want, tol)
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (16, 5200), (40, 48), (200, 4100), (300, 70), (515, 2049)])
+def test_w4a8_bf16_of_few_tokens_is_the_fp32_result_rounded(awq, M, N):
+    """But for whole tiles a bf16 result of e4m3 codes is summed as an fp32 one unless the caller asks otherwise."""
+    K = 1152
+    w = on_gpu(awq, kept_artefact(N, K, 141))
+    q, sc = codes(M, K, E4M3, 142)
+    a = awq.Act8(q.to(DEV), sc.to(DEV))
+    assert torch.equal(awq.w4a8(a, w, dtype=BF16), awq.w4a8(a, w).to(BF16))
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 384, 40), (16, 384, 5200), (40, 640, 48), (101, 384, 4500), (300, 1408, 70),
+                                   (130, 14336, 40), (8260, 384, 48), (18521, 384, 520)])
+@pytest.mark.parametrize("yt", [BF16, F32])
+def test_w4a8_matrix_sums_on_request(awq, M, K, N, yt):
+    """fp32_sums=False: the matrix unit's own sums, on every path and for either result type, within their bound."""
+    art = kept_artefact(N, K, 143)
+    q, sc = codes(M, K, E4M3, 144)
+    Y = awq.w4a8(awq.Act8(q.to(DEV), sc.to(DEV)), on_gpu(awq, art), dtype=yt, fp32_sums=False)
+    want, mag, absmag = a8.w4a8(f64(q), f64(sc), art)
+    lim = (2 * (K // 128) + 16) * U * mag + (HALF[yt] + 4 * U) * np.abs(want) + (2.0 ** -9 + 136 * U) * absmag + 1e-36
+    assert np.all(np.abs(f64(Y) - want) <= lim)
+
+
+@pytest.mark.parametrize("M", [1, 15, 40, 64, 300])
+def test_w4a8_bf16_results_round_as_the_exact_ones(awq, M):
+    """A bf16 result that rounds another way than the exact one turns 8-bit codes made from it by whole steps, so few may:
+    at most one in 2^8.  With outlier channels; e4m3 codes.  A group's 136 fp32 roundings, of partial sums about three
+    times what is left behind the zero points (q about 8.9 rms, q - z about 3), add at random to sqrt(136 / 3) * 3 = 20 u
+    of the result, 1.2e-6; it rounds another way where the border is nearer than that, in 1.6 * 1.2e-6 / 2^-7.5 = 0.04% of
+    all results, a tenth of the limit.  (Sums kept to 14 bits, about 2e-4 off, do in 6%.)"""
+    K, N = 1024, 4096
+    art = kept_artefact(N, K, 145)
+    rng = np.random.default_rng(146)
+    mag = np.where(rng.uniform(size=K) < 0.01, rng.uniform(10, 50, K), 1.0) * np.exp(0.5 * rng.standard_normal(K))
+    x = torch.from_numpy((rng.standard_normal((M, K)) * mag).astype(np.float32))
+    a = awq.act_mul(x.to(DEV), act="none", dtype=E4M3)
+    z = awq.w4a8(a, on_gpu(awq, art), dtype=BF16)
+    want = torch.from_numpy(a8.w4a8(f64(a.q), f64(a.scale), art)[0])
+    near = want.to(F32).to(BF16)  # (fp32's rounding in between moves 2^-16 of the borders)
+    assert float((z.cpu() != near).double().mean()) <= 2.0 ** -8
