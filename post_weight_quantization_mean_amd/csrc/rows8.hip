@@ -176,7 +176,10 @@ __device__ __forceinline__ bool any_far(const Raw8<T>& x) {
   } else {
     u16x2 top = {0, 0};
 #pragma unroll
-    for (int d = 0; d < 4; ++d) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x.q[0][d]));
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t w = x.q[0][d];  // (a bit cast of the vector's element itself reads element 0)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w));
+    }
     return __builtin_amdgcn_ballot_w64(top[0] > (kFar >> 16) || top[1] > (kFar >> 16)) != 0;
   }
 }

@@ -956,3 +956,17 @@ def test_w4a8_bf16_results_round_as_the_exact_ones(awq, M):
     want = torch.from_numpy(a8.w4a8(f64(a.q), f64(a.scale), art)[0])
     near = want.to(F32).to(BF16)  # (fp32's rounding in between moves 2^-16 of the borders)
     assert float((z.cpu() != near).double().mean()) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("K", [8, 13, 512, 2048, 5001, 14336, 65537])
+@pytest.mark.parametrize("xt,out", [(F32, F32), (BF16, F32), (BF16, BF16)])
+def test_silu_one_far_element_among_others(awq, K, xt, out):
+    """Each row has a single element below -79, at another place in its eight, its lane and its wave."""
+    M = 64 if K < 10000 else 24
+    x = rand((M, K), xt, 150)
+    cols = (torch.arange(M) * 37 + torch.arange(M) // 8) % K
+    x[torch.arange(M), cols] = torch.linspace(-80.0, -91.0, M).to(xt)
+    want = a8.act_mul(f64(x), None, None, "silu")
+    y = f64(awq.act_mul(x.to(DEV), None, None, "silu", dtype=out))
+    ulp = 18.0 + (0.0 if out == F32 else 1.0) * np.abs(f64(x))
+    assert np.all(np.abs(y - want) <= (ulp * U + HALF[out]) * np.abs(want) + 2.0 ** -149)
