@@ -45,7 +45,7 @@ extern "C" {
  *   scale  fp32 [M] for an 8-bit Y, else ignored
  * Any K.  H = R aside, outputs overlap no input and not each other (of this only exact starts are checked: Y on
  * H, an output on gamma, or on an operand in another type or row stride, are AWQ_ERR_INVALID_ARG).  A row whose
- * sum of squares is not finite in fp32 (|h| around 1e19 and more, NaN, Inf) has y NaN.
+ * sum of squares is not finite in fp32 (|h| of 1.8e19 / sqrt(K) and more, NaN, Inf) has y NaN.
  * ------------------------------------------------------------------------------------- */
 AWQ_API int awq_rmsnorm(const void* X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const void* R,
                         int r_dtype, int64_t ldr, void* H, int64_t ldh, const void* gamma, int g_dtype,
