@@ -107,8 +107,8 @@ constexpr float kE4m3Unit = 0x1p-9f;  // an e4m3 byte b < 16 is b times this
 // shifting them to the largest one's exponent and keeps 14 bits there (measured; the sums of 16 then add in
 // fp32): about 2^-13 of the largest product.  On activations with 1% of channels 10 to 50 times the others that
 // adds 2e-4 (rms, relative) to a bf16 result's rounding of 1.7e-3; where a large code's q is its zero point, so that
-// its product cancels, what is lost beside it can be more than that rounding.  And the results that it rounds another way
-// turn codes behind them: an MLP in e4m3 (40 tokens) ends 4.4e-3 from its value in 64 bits, 2.1e-3 with fp32 sums.
+// its product cancels, what is lost beside it can be more than that rounding.  And the results that round another way
+// for it turn codes behind them: an MLP in e4m3 (40 tokens) ends 4.4e-3 from its value in 64 bits, 2.1e-3 with fp32 sums.
 // kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32, at half the matrix rate.  It is the default but
 // for bf16 results of whole tiles, where the rate counts (us, kE4m3Fast / kE4m3Wide): 4096 x 4096 -> 28672 435 / 850,
 // 1024 x 11008 -> 4096 60 / 105, against 16 x 14336 -> 4096 10.7 / 11.3, 64 x 4096 -> 4096 7.0 / 7.3, 101 x 4096 ->
@@ -190,10 +190,12 @@ __device__ __forceinline__ i32x8 join(const u32x4 lo, const u32x4 hi) {
 // A block computes CT tiles of 16 channels for up to 16 TT tokens over all of K.  Its WV waves take the
 // groups in turn, D of them in flight in each wave, with fp32 sums of their own, which meet in LDS at the
 // end in wave order.  Bound: up to 8 tokens by the weight's bytes and the time until they flow (1 x 4096 -> 28672:
-// 12.3 us, 5.1 TB/s, what a copy reaches; 1 and 5 x 14336 -> 4096: 8.0, 256 blocks of seven groups a wave); beyond, by
+// 12.3 us, 5.1 TB/s, what a copy reaches; 1 and 5 x 14336 -> 4096: 8.0, 256 blocks of seven groups a wave), in e4m3
+// with fp32 sums by the conversions to bf16 where each block has two channel tiles (16.5 and 8.7); beyond, by
 // the reads of X from L2 too, 2 KiB per wave, group and 16 tokens: with every token's lanes reading the first token
 // instead, us, 16 x 14336 -> 4096 takes 7.9 for 10.8, 16 x 4096 -> 28672 12.4 / 15.2, 64 x 4096 -> 4096 5.3 / 7.1,
-// 101 x 4096 -> 6144 9.0 / 13.0, 256 x 4096 -> 4096 10.1 / 14.6.  Sum x per token and group is one more product, with ones, in the layout of the
+// 101 x 4096 -> 6144 9.0 / 13.0, 256 x 4096 -> 4096 10.1 / 14.6.  Sum x per token and group is one more product, with
+// ones, in the layout of the
 // sums it corrects.  Rows past the last token repeat it and are not stored.
 template <int KIND, int TT, int CT, int WV, int D>
 __global__ __launch_bounds__(64 * WV) void w4a8_stream_kernel(const W4a8Args p) {
@@ -377,8 +379,9 @@ __global__ __launch_bounds__(256) void w4a8_sums_kernel(const uint8_t* __restric
 // cores in fp16 with both operands as high and low parts (sums to 2^-23, D z 15 bits: exact), one
 // instruction of 16 cycles for eight groups.
 //
-// 4096 x 4096 -> 28672: e4m3 440 us (2.2 PFLOP/s), int8 484 (2.0).  A loop of nothing but such products and
-// multiply-adds runs at 4.0 (e4m3) and 2.9 (int8), a library product without steps at 3.1 and 2.55.  The clock is
+// 4096 x 4096 -> 28672, by box: e4m3 434 to 462 us (2.1 to 2.2 PFLOP/s), int8 484 to 520 (1.9 to 2.0), e4m3 in fp32
+// sums 830 to 875 (1.1: bf16's matrix rate, with 64-token tiles and both operands converted in every wave).  A loop of
+// nothing but such products and multiply-adds runs at 4.0 (e4m3) and 2.9 (int8), a library product without steps at 3.1 and 2.55.  The clock is
 // down to 1.7 .. 2.0 GHz under this load.  4096 x 11008 -> 4096, e4m3, 169 us: 149 without the codes' loads, 132
 // without the copies into LDS, 117 without both, 102 without the zero points' part too: what bounds it is the
 // operands' way from L2 (32 KiB a block and step, and the power it takes), then the products.
