@@ -97,11 +97,10 @@ AWQ_API int awq_w4a8_weight(const int32_t* qweight, const uint16_t* scales, cons
  * on the 8-bit matrix cores: a code q is an int8 byte as it stands, and as an e4m3 byte it is
  * exactly q 2^-9.  I8: the inner sums are exact integers.  E4M3: the products are exact, and a group's are
  * summed
- *   in fp32 for an F32 Y, and for a BF16 Y but for many tokens (at half the matrix rate);
- *   by the matrix unit for a BF16 Y of many tokens: M > 16 and ceil(M / 64) ceil(N / 256) > 128, and not the blocks
- *     of 32 tokens that up to 256 tokens may run in.  It adds sixteen at a time to 14 bits of the largest of
- *     them: off by at most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more than a
- *     bf16 rounding where one large code with q = z stands beside small ones.
+ *   in fp32 for an F32 Y, and for a BF16 Y of up to 256 tokens (at half the matrix rate);
+ *   by the matrix unit for a BF16 Y of more.  It adds sixteen at a time to 14 bits of the largest of them: off by at
+ *     most 2^-9 of the sum of the magnitudes |x q| and z |x|, 2^-13 and less as a rule; more than a bf16 rounding
+ *     where one large code with q = z stands beside small ones.
  * AWQ_W4A8_SUMS_F32 or AWQ_W4A8_SUMS_MATRIX in y_dtype ask for one of the two at any size; with I8 they
  * change nothing.  The sums z multiplies are within 2^-23 of fp32's.  The steps and the sum over groups
  * are fp32; Y is rounded once.

@@ -637,9 +637,9 @@ def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, ou
          workspace: Optional[torch.Tensor] = None, fp32_sums: Optional[bool] = None) -> torch.Tensor:
     """Y = X W_hat^T for 8-bit activations (``Act8``: from ``rmsnorm``, ``act_mul``, or the caller's own)
     and a weight laid out by ``w4a8_weight``.  Y [M, N] is float32 (the default) or bfloat16.  int8 sums are exact.
-    e4m3 codes are summed in fp32, but for a bfloat16 Y of many tokens (more than 128 tiles of 64 tokens x 256
-    channels) by the matrix unit: sixteen at a time to 14 bits of the largest, in half the time.  ``fp32_sums`` True
-    or False asks for the one or the other at any size and type.
+    e4m3 codes are summed in fp32, but for a bfloat16 Y of more than 256 tokens by the matrix unit: sixteen at a time
+    to 14 bits of the largest, in half the time.  ``fp32_sums`` True or False asks for the one or the other at any
+    size and type.
     Rows of the codes start at multiples of 16 bytes.
     ``workspace``: ``w4a8_workspace_bytes`` for (M, K, N), allocated here when not given; calls that may
     run at the same time (two streams, two graphs) need one each."""

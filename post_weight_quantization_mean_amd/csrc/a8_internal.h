@@ -38,7 +38,6 @@ hipError_t launch_act_mul(const RowArgs& a, int x_type, bool vec, hipStream_t st
 struct W4a8Layout {
   size_t steps, powers, total;  // byte offsets of the parts behind the codes
 };
-constexpr int kSumsDefault = 0, kSumsF32 = 1, kSumsMatrix = 2;
 struct W4a8Args {
   const void* x;
   const float* xscale;

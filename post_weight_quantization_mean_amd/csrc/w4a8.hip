@@ -109,10 +109,8 @@ constexpr float kE4m3Unit = 0x1p-9f;  // an e4m3 byte b < 16 is b times this
 // adds 2e-4 (rms, relative) to a bf16 result's rounding of 1.7e-3; where a large code's q is its zero point, so that
 // its product cancels, what is lost beside it can be more than that rounding.  And the results that round another way
 // for it turn codes behind them: an MLP in e4m3 (40 tokens) ends 4.4e-3 from its value in 64 bits, 2.1e-3 with fp32 sums.
-// kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32, at half the matrix rate.  It is the default but
-// for bf16 results of whole tiles, where the rate counts (us, kE4m3Fast / kE4m3Wide): 4096 x 4096 -> 28672 435 / 850,
-// 1024 x 11008 -> 4096 60 / 105, against 16 x 14336 -> 4096 10.7 / 11.3, 64 x 4096 -> 4096 7.0 / 7.3, 101 x 4096 ->
-// 6144 13.0 / 14.7, 1 x 4096 -> 28672 12.7 / 16.2, 256 x 14336 -> 4096 32 / 44.
+// kE4m3Wide converts both operands to bf16 (exactly) and adds in fp32, at half the matrix rate.  matrix_sums says which is
+// taken.
 constexpr int kInt8 = 0, kE4m3Fast = 1, kE4m3Wide = 2;
 
 template <int KIND>
@@ -990,8 +988,8 @@ size_t w4a8_workspace(int64_t M, int64_t K, int64_t N) {
 hipError_t launch_w4a8(const W4a8Args& a, void* ws, hipStream_t st) {
   const Plan pl = w4a8_plan(a.M, a.K, a.N);
   if (!a.e4m3) return launch_kind<kInt8>(a, pl, ws, st);
-  const bool matrix = a.sums == kSumsMatrix || (a.sums == kSumsDefault && a.ybf16 && pl.path == kTile);
-  return matrix ? launch_kind<kE4m3Fast>(a, pl, ws, st) : launch_kind<kE4m3Wide>(a, pl, ws, st);
+  return matrix_sums(a.sums, a.ybf16, a.M) ? launch_kind<kE4m3Fast>(a, pl, ws, st)
+                                           : launch_kind<kE4m3Wide>(a, pl, ws, st);
 }
 
 }  // namespace awq

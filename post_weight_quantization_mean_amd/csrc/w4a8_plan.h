@@ -19,6 +19,17 @@ struct Plan {
   int ct, waves;          // stream: channel tiles of 16 and waves per block
 };
 
+// How a product of e4m3 codes is summed: true, by the matrix unit (14 bits of the largest of sixteen products), false, in
+// fp32.  Left to the kernel, bf16 results of more than 256 tokens take the matrix unit's sums, because there the matrix
+// rate counts, which fp32 sums halve; not the plan's path, so that a re-fitted cost changes no result.  us, matrix unit
+// / fp32: 4096 x 4096 -> 28672 435 / 845, 1024 x 11008 -> 4096 60 / 104, 512 x 4096 -> 4096 17 / 26; up to 256 tokens, 1 x
+// 4096 -> 28672 12.7 / 16.5, 16 x 14336 -> 4096 10.7 / 11.3, 64 x 4096 -> 4096 7.0 / 7.3, 101 x 4096 -> 6144 13.0 / 14.6, 256 x
+// 14336 -> 4096 32 / 42, 128 x 4096 -> 17000 29 / 44.
+constexpr int kSumsDefault = 0, kSumsF32 = 1, kSumsMatrix = 2;
+constexpr bool matrix_sums(int sums, bool ybf16, int64_t M) {
+  return sums == kSumsMatrix || (sums == kSumsDefault && ybf16 && M > 256);
+}
+
 // Blocks of 32 tokens and ct channel tiles: the fewest channels that leave at most one block of eight waves per CU
 // (more channels read X less often, fewer blocks leave CUs idle); then blocks of four waves, several per CU.
 // K = 4096, us: 192 blocks of 2 tiles 7.5, 256 of 3 8.4, 256 of 4 8.9; 512 of 3 in four waves 13.3 (384 of 4 14.6,

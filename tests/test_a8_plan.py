@@ -27,7 +27,8 @@ int main(int argc, char**) {
       continue;
     }
     const awq::Plan p = awq::w4a8_plan(m, k, n);
-    std::printf("%d %d %d %d %d %d\\n", p.path, p.tm, p.splits, p.per_split, p.ct, p.waves);
+    std::printf("%d %d %d %d %d %d %d\\n", p.path, p.tm, p.splits, p.per_split, p.ct, p.waves,
+                (int)awq::matrix_sums(awq::kSumsDefault, true, m));
   }
 }
 """
@@ -54,18 +55,22 @@ def parameters(test):
 
 
 def cases():
-    """((M, K, N), kind of sum) of every product that a GPU test compares with the definition."""
+    """((M, K, N), codes, result, kind of sum asked for) of every product that a GPU test compares with the definition."""
     for test in (gpu.test_w4a8, gpu.test_w4a8_tiles, gpu.test_w4a8_some_tokens, gpu.test_w4a8_wide_and_split):
         p = parameters(test)
         for shape, (xt, yt) in itertools.product(p["M,K,N"], p["xt,yt"]):
-            yield shape, "int8" if xt == torch.int8 else "fast" if yt == torch.bfloat16 else "wide"
+            yield shape, xt, yt, None
+    p = parameters(gpu.test_w4a8_matrix_sums_on_request)
+    for shape, yt in itertools.product(p["M,K,N"], p["yt"]):
+        yield shape, torch.float8_e4m3fn, yt, "matrix"
 
 
 def test_every_kernel_is_reached(plan):
     got = list(cases())
     seen = set()
-    for (shape, kind), (path, tm, splits, per, ct, waves) in zip(got, plan([s for s, _ in got])):
+    for (shape, xt, yt, asked), (path, tm, splits, per, ct, waves, matrix) in zip(got, plan([c[0] for c in got])):
         G = shape[1] // 128
+        kind = "int8" if xt == torch.int8 else "fast" if asked or (matrix and yt == torch.bfloat16) else "wide"
         if path == STREAM:
             seen.add((kind, STREAM, tm, ct, waves))
         elif path == SPLIT:
@@ -92,9 +97,9 @@ def test_plan_is_sound(plan):
     """Over a grid of sizes: every block of a split has a group, splits cover the groups once, blocks have their limits."""
     shapes = [(m, 128 * g, n) for m in (1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 100, 128, 129, 256, 257, 511, 1000, 4096, 100000)
               for g in (1, 2, 3, 7, 8, 9, 31, 32, 86, 112, 500) for n in (1, 16, 17, 255, 256, 257, 4096, 5104, 5105, 28672, 200001)]
-    for (m, k, n), (path, tm, splits, per, ct, waves) in zip(shapes, plan(shapes)):
+    for (m, k, n), (path, tm, splits, per, ct, waves, matrix) in zip(shapes, plan(shapes)):
         G = k // 128
-        assert path in (STREAM, SPLIT, TILE)
+        assert path in (STREAM, SPLIT, TILE) and matrix == (m > 256)
         if path == STREAM:
             assert m <= 256 and (tm, ct, waves) in {(1, 1, 16), (1, 2, 8), (2, 2, 8), (2, 3, 8), (2, 4, 8), (2, 3, 4), (2, 4, 4)}
             assert (m <= 16) == (tm == 1)

@@ -916,18 +916,25 @@ def test_act_mul_in_place_of_either(awq, M, K, which):
     check_stored(y, want, tol)
 
 
-@pytest.mark.parametrize("M,N", [(3, 40), (16, 5200), (40, 48), (200, 4100), (300, 70), (515, 2049)])
-def test_w4a8_bf16_of_few_tokens_is_the_fp32_result_rounded(awq, M, N):
-    """But for whole tiles a bf16 result of e4m3 codes is summed as an fp32 one unless the caller asks otherwise."""
-    K = 1152
+@pytest.mark.parametrize("M,K,N", [(3, 1152, 40), (16, 1152, 5200), (40, 1152, 48), (200, 1152, 4100), (130, 14336, 40),
+                                   (256, 384, 8400)])
+def test_w4a8_bf16_of_few_tokens_is_the_fp32_result_rounded(awq, M, K, N):
+    """Up to 256 tokens, on every path, a bf16 result of e4m3 codes is summed as an fp32 one unless the caller asks
+    otherwise."""
     w = on_gpu(awq, kept_artefact(N, K, 141))
     q, sc = codes(M, K, E4M3, 142)
     a = awq.Act8(q.to(DEV), sc.to(DEV))
     assert torch.equal(awq.w4a8(a, w, dtype=BF16), awq.w4a8(a, w).to(BF16))
 
 
-@pytest.mark.parametrize("M,K,N", [(3, 384, 40), (16, 384, 5200), (40, 640, 48), (101, 384, 4500), (300, 1408, 70),
-                                   (130, 14336, 40), (8260, 384, 48), (18521, 384, 520)])
+# every path, block shape and remainder of groups, as the lists above reach them
+MATRIX_SHAPES = [(3, 384, 40), (16, 384, 5200), (16, 1152, 5121), (33, 1152, 1000), (63, 256, 4100), (96, 256, 3600),
+                 (40, 128, 9000), (101, 384, 4500), (250, 640, 1025), (32, 256, 20000), (125, 256, 4090), (31, 384, 28001),
+                 (300, 1408, 70), (257, 256, 40), (400, 1664, 777), (130, 14336, 40), (600, 11008, 300), (519, 4224, 2049),
+                 (301, 8192, 2049)] + TILE_SHAPES + MORE_TILE_SHAPES
+
+
+@pytest.mark.parametrize("M,K,N", MATRIX_SHAPES)
 @pytest.mark.parametrize("yt", [BF16, F32])
 def test_w4a8_matrix_sums_on_request(awq, M, K, N, yt):
     """fp32_sums=False: the matrix unit's own sums, on every path and for either result type, within their bound."""
@@ -939,7 +946,7 @@ def test_w4a8_matrix_sums_on_request(awq, M, K, N, yt):
     assert np.all(np.abs(f64(Y) - want) <= lim)
 
 
-@pytest.mark.parametrize("M", [1, 15, 40, 64, 300])
+@pytest.mark.parametrize("M", [1, 15, 40, 64, 256])
 def test_w4a8_bf16_results_round_as_the_exact_ones(awq, M):
     """A bf16 result that rounds another way than the exact one turns 8-bit codes made from it by whole steps, so few may:
     at most one in 2^8.  With outlier channels; e4m3 codes.  A group's 136 fp32 roundings, of partial sums about three
