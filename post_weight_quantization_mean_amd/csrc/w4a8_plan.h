@@ -19,12 +19,12 @@ struct Plan {
   int ct, waves;          // stream: channel tiles of 16 and waves per block
 };
 
-// How a product of e4m3 codes is summed: true, by the matrix unit (14 bits of the largest of sixteen products), false, in
-// fp32.  Left to the kernel, bf16 results of more than 256 tokens take the matrix unit's sums, because there the matrix
-// rate counts, which fp32 sums halve; not the plan's path, so that a re-fitted cost changes no result.  us, matrix unit
-// / fp32: 4096 x 4096 -> 28672 435 / 845, 1024 x 11008 -> 4096 60 / 104, 512 x 4096 -> 4096 17 / 26; up to 256 tokens, 1 x
-// 4096 -> 28672 12.7 / 16.5, 16 x 14336 -> 4096 10.7 / 11.3, 64 x 4096 -> 4096 7.0 / 7.3, 101 x 4096 -> 6144 13.0 / 14.6, 256 x
-// 14336 -> 4096 32 / 42, 128 x 4096 -> 17000 29 / 44.
+// How a product of e4m3 codes is summed: true, by the matrix unit (14 bits of the largest of sixteen products),
+// false, in fp32.  Left to the kernel, bf16 results of more than 256 tokens take the matrix unit's sums, because there
+// the matrix rate counts, which fp32 sums halve; a rule on the tokens, not on the plan's path, so that a re-fitted cost
+// changes no result.  us, matrix unit / fp32: 4096 x 4096 -> 28672 435 / 845, 1024 x 11008 -> 4096 60 / 104, 512 x 4096
+// -> 4096 17 / 26; up to 256 tokens, 1 x 4096 -> 28672 12.7 / 16.5, 16 x 14336 -> 4096 10.7 / 11.3, 64 x 4096 -> 4096
+// 7.0 / 7.3, 101 x 4096 -> 6144 13.0 / 14.6, 256 x 14336 -> 4096 32 / 42, 128 x 4096 -> 17000 29 / 44.
 constexpr int kSumsDefault = 0, kSumsF32 = 1, kSumsMatrix = 2;
 constexpr bool matrix_sums(int sums, bool ybf16, int64_t M) {
   return sums == kSumsMatrix || (sums == kSumsDefault && ybf16 && M > 256);
