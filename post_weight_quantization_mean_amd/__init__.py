@@ -7,7 +7,7 @@ and raise if it has not been built.
 """
 
 __all__ = ["stats", "search", "pack", "search_workspace_bytes", "stats_workspace_bytes", "rmsnorm", "act_mul",
-           "w4a8_weight", "w4a8", "Act8"]
+           "w4a8_weight", "w4a8", "Act8", "moe_route", "moe_weight", "moe", "lora", "Routing", "MoEWeight"]
 
 
 def __getattr__(name):

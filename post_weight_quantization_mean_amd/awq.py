@@ -121,6 +121,20 @@ def lib() -> ctypes.CDLL:
         L.awq_w4a8_workspace_bytes.argtypes = [i64, i64, i64]
         L.awq_w4a8.restype = ci
         L.awq_w4a8.argtypes = [vp, ci, vp, i64, i64, i64, vp, i64, i32, vp, ci, i64, vp, sz, vp]
+        L.awq_moe_route.restype = ci
+        L.awq_moe_route.argtypes = [vp, ci, i64, i64, i64, i32, ci, ci, vp, vp, vp]
+        L.awq_moe_workspace_bytes.restype = sz
+        L.awq_moe_workspace_bytes.argtypes = [i64, i64, i32, i64, i64]
+        L.awq_moe.restype = ci
+        L.awq_moe.argtypes = [vp, ci, vp, i64, i64, i64, vp, vp, i32, vp, vp, i64, i64, i32, ci, vp, ci, i64, vp, sz, vp]
+        L.awq_moe_layer.restype = ci
+        L.awq_moe_layer.argtypes = [vp, ci, vp, i64, i64, i64, vp, ci, i64, i32, ci, ci, vp, vp, i64, i64, i32, ci,
+                                    vp, ci, i64, vp, sz, vp]
+        L.awq_lora_workspace_bytes.restype = sz
+        L.awq_lora_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.awq_lora.restype = ci
+        L.awq_lora.argtypes = [vp, ci, vp, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, ci, i64, i64, vp,
+                               sz, vp]
         if L.awq_abi_version() != 8:
             raise ImportError("libawq ABI version mismatch")
         _lib = L
@@ -136,10 +150,12 @@ def _bound():
         try:
             from . import _a8 as binding
         except ImportError as e:
-            raise ImportError("rmsnorm, act_mul and w4a8 need _a8.so, built for this interpreter and torch "
+            raise ImportError("rmsnorm, act_mul, w4a8, moe and lora need _a8.so, built for this interpreter and torch "
                               f"(python -m post_weight_quantization_mean_amd.build): {e}") from e
-        names = ("awq_rmsnorm", "awq_act_mul", "awq_w4a8", "awq_w4a8_weight_bytes", "awq_w4a8_workspace_bytes")
-        binding.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Act8, AwqError)
+        names = ("awq_rmsnorm", "awq_act_mul", "awq_w4a8", "awq_w4a8_weight_bytes", "awq_w4a8_workspace_bytes",
+                 "awq_moe_route", "awq_moe", "awq_moe_layer", "awq_moe_workspace_bytes", "awq_lora",
+                 "awq_lora_workspace_bytes")
+        binding.bind(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Act8, Routing, AwqError)
         _a8 = binding
     return _a8
 
@@ -646,3 +662,96 @@ def w4a8(X: Act8, weight: W4A8Weight, *, dtype: Optional[torch.dtype] = None, ou
     q, scale = X
     data, N, K = weight
     return _on(q, (_a8 or _bound()).w4a8, q, scale, data, N, K, dtype, out, workspace, fp32_sums)
+
+
+# ---- rows that choose their weights ---------------------------------------------------------
+
+
+class Routing(NamedTuple):
+    """The experts of each token: ``ids`` int32 [M, k] (a value that is no expert's: none), ``weights`` fp32 [M, k]."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+
+
+class MoEWeight(NamedTuple):
+    """E experts' packed weights laid out for ``moe`` (by ``moe_weight``): ``data`` uint8, N x K each."""
+    data: torch.Tensor
+    E: int
+    N: int
+    K: int
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score: str) -> int:
+    code = _SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {', '.join(_SCORES)}")
+    return code
+
+
+def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormalize: bool = True,
+              out: Optional[Routing] = None) -> Routing:
+    """The k experts of each token with the largest logits ([M, E] fp32 or bf16, E at most 1024, k at most 32), largest
+    first, ties to the lowest index, and their weights: ``score`` "softmax" (over all experts) or "sigmoid", divided by
+    their sum with ``renormalize``.  A logit of -Inf masks its expert; where fewer than k are left the rest has id -1 and
+    weight 0.  NaN is chosen first and makes the row's weights NaN."""
+    return _on(logits, (_a8 or _bound()).moe_route, logits, k, _score(score), renormalize, out)
+
+
+def moe_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = GROUP, *,
+               out: Optional[torch.Tensor] = None) -> MoEWeight:
+    """The artefacts of ``pack`` of E experts (qweight int32 [E, N, K/8], scales and zeros fp16 [E, N, K/128], N a multiple
+    of 16) laid out for ``moe``, once per layer.  For the gate/up weight N = 2 I: gate rows, then up rows.  ``out``: uint8
+    of at least ``w4a8_weight_bytes(E * N, K)``, 256-byte aligned."""
+    if qweight.dim() != 3 or not qweight.is_contiguous():
+        raise ValueError("qweight must be a contiguous int32 [E, N, K/8] device tensor")
+    E, N, K = qweight.shape[0], qweight.shape[1], qweight.shape[2] * 8
+    if N % 16 != 0:
+        raise ValueError("N must be a multiple of 16")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t.shape != (E, N, K // max(group_size, 1)) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp16 [E, N, K/group] tensor")
+    data = w4a8_weight(*(t.view(E * N, t.shape[2]) for t in (qweight, scales, zeros)), group_size, out=out).data
+    return MoEWeight(data, E, N, K)
+
+
+def moe_workspace_bytes(M: int, E: int, k: int, H: int, I: int) -> int:
+    return int(lib().awq_moe_workspace_bytes(M, E, k, H, I))
+
+
+def moe(X, routing, gate_up: MoEWeight, down: MoEWeight, act: str = "silu", *, k: Optional[int] = None,
+        score: str = "softmax", renormalize: bool = True, dtype: Optional[torch.dtype] = None,
+        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture of experts over packed 4-bit weights: Y[m] = sum_j w_j D_e (act(G_e x) * (U_e x)) with e and w of
+    ``routing``: a ``Routing`` (ids outside 0 .. E-1 are skipped), or the router's logits [M, E] with ``k``, ``score`` and
+    ``renormalize`` as in ``moe_route``, for the whole layer in one call.
+    X [M, H] is float32, bfloat16 or an ``Act8``, its rows 16-byte aligned; ``gate_up`` E experts of [2 I, H] and ``down``
+    of [H, I], from ``moe_weight``; ``act`` "silu" or "gelu".  Y [M, H] is float32 (the default) or bfloat16, all sums in
+    fp32.  Made for decode batches and short prompts; more than 2048 / k tokens run in passes that each read the weights.
+    ``workspace``: ``moe_workspace_bytes`` for (M, E, k, H, I), allocated here when not given; calls that may run at the
+    same time (two streams, two graphs) need one each."""
+    code = _ACTS.get(act)
+    if code is None or code == ACT_NONE:
+        raise ValueError("act must be silu or gelu")
+    return _on(X[0] if isinstance(X, tuple) else X, (_a8 or _bound()).moe, X, routing, k, _score(score), renormalize,
+               gate_up, down, code, dtype, out, workspace)
+
+
+def lora_workspace_bytes(M: int, K: int, N: int, R: int) -> int:
+    return int(lib().awq_lora_workspace_bytes(M, K, N, R))
+
+
+def lora(X, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, base: torch.Tensor, *,
+         scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection: Y[m] = base[m] + scale[a] B[a] (A[a] x[m]) with
+    a = ids[m] (int32 [M]; a value that is no adapter's leaves the row as it is).  ``base`` [M, N] is the projection's
+    output for X (``w4a8``, ``w4a16``, any), float32 or bfloat16, and Y has its type; ``out`` may be ``base``.
+    X [M, K] is float32, bfloat16 or an ``Act8``; A bfloat16 [adapters, R, K], B bfloat16 [adapters, N, R]; K and R multiples
+    of 8, R at most 256.  ``ranks`` int32 [adapters]: the rows of A and columns of B that count (all without it); ``scale``
+    fp32 [adapters].
+    ``workspace``: ``lora_workspace_bytes`` for (M, K, N, R), allocated here when not given; calls that may run at the same
+    time (two streams, two graphs) need one each."""
+    return _on(X[0] if isinstance(X, tuple) else X, (_a8 or _bound()).lora, X, A, B, ids, base, scale, ranks, out, workspace)

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libawq.so")
 BINDING = os.path.join(PKG, "_a8.so")
 
 SOURCES = ["stats.hip", "scales.hip", "search.hip", "gram.hip", "pack.hip", "clip.hip", "fold.hip", "w4a16.hip",
-           "rows8.hip", "w4a8.hip", "awq_api.cpp", "a8_api.cpp"]
+           "rows8.hip", "w4a8.hip", "moe.hip", "lora.hip", "awq_api.cpp", "a8_api.cpp", "moe_api.cpp", "lora_api.cpp"]
 
 # -ffp-contract=off: every fp32 operation of the quantizer contract is rounded on its own
 #   (fused multiply-adds are written explicitly where the search wants them).

@@ -1,5 +1,5 @@
-// Python binding of the 8-bit activation calls (awq_a8.h): argument marshalling only.  These calls run once
-// per layer and token, where the checks and the output's allocation, made in Python, would take longer than
+// Python binding of the 8-bit activation calls (awq_a8.h), the mixture of experts (awq_moe.h) and the low-rank adapters
+// (awq_lora.h): argument marshalling only.  These calls run once per layer and token, where the checks and the output's allocation, made in Python, would take longer than
 // the kernel; the rest of the library is bound with ctypes.  The library's functions are handed in as
 // addresses (bind), so that this module does not load it.
 #define PY_SSIZE_T_CLEAN
@@ -10,22 +10,33 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <cstdint>
+#include <cstring>
 #include <exception>
 #include <string>
 
 #include "awq_a8.h"
+#include "awq_lora.h"
+#include "awq_moe.h"
 
 namespace {
 
-struct Lib {
+struct Lib {  // in the order of bind's addresses
   decltype(&awq_rmsnorm) rmsnorm;
   decltype(&awq_act_mul) act_mul;
   decltype(&awq_w4a8) w4a8;
   decltype(&awq_w4a8_weight_bytes) weight_bytes;
   decltype(&awq_w4a8_workspace_bytes) workspace_bytes;
+  decltype(&awq_moe_route) moe_route;
+  decltype(&awq_moe) moe;
+  decltype(&awq_moe_layer) moe_layer;
+  decltype(&awq_moe_workspace_bytes) moe_workspace_bytes;
+  decltype(&awq_lora) lora;
+  decltype(&awq_lora_workspace_bytes) lora_workspace_bytes;
 } lib;
-PyObject* act8_type = nullptr;  // awq.Act8, a tuple of two
+PyObject* act8_type = nullptr;     // awq.Act8, a tuple of two
+PyObject* routing_type = nullptr;  // awq.Routing, a tuple of two
 PyObject* error_type = nullptr;  // awq.AwqError(status, what)
 
 struct Raise {  // a Python exception to set
@@ -318,22 +329,242 @@ PyObject* w4a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(rmsnorm, act_mul, w4a8, weight_bytes, workspace_bytes, Act8, AwqError): the library's addresses, and the types
+// Activations in any of the four types: a tensor, or an Act8's codes with their scale.
+struct Rows {
+  at::Tensor x, scale;
+  int code = 0;
+  int64_t M = 0, K = 0, ld = 0;
+  const float* scale_ptr = nullptr;
+
+  explicit Rows(PyObject* o) {
+    const bool codes = PyTuple_Check(o);
+    if (codes) {
+      if (PyTuple_GET_SIZE(o) != 2) type_error("X must be a tensor or an Act8");
+      x = tensor(PyTuple_GET_ITEM(o, 0), "X.q");
+      scale = tensor(PyTuple_GET_ITEM(o, 1), "X.scale");
+    } else {
+      x = tensor(o, "X");
+    }
+    first(x, codes ? "X.q" : "X");
+    M = x.size(0), K = x.size(1);
+    ld = row_stride(x, codes ? "X.q" : "X", x.device(), M, K);
+    code = codes ? codes_code(x, "X.q") : float_code(x, "X");
+    if (codes) {
+      if (scale.scalar_type() != at::kFloat) type_error("X.scale must be float32");
+      scale_ptr = static_cast<const float*>(vector(scale, "X.scale", x.device(), M));
+    }
+  }
+};
+
+// A contiguous tensor of the given type and sizes on dev.
+const void* plain(const at::Tensor& t, const char* name, c10::Device dev, at::ScalarType type, const char* type_name,
+                  at::IntArrayRef sizes) {
+  if (t.scalar_type() != type) type_error(std::string(name) + " must be " + type_name);
+  if (t.sizes() != sizes || t.device() != dev || !t.is_contiguous()) {
+    std::string s;
+    for (const int64_t n : sizes) s += (s.empty() ? "" : ", ") + std::to_string(n);
+    value_error(std::string(name) + " must be a contiguous [" + s + "] tensor on " + dev.str());
+  }
+  return t.const_data_ptr();
+}
+
+int64_t whole(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raise{nullptr, ""};
+  return v;
+}
+int small(PyObject* o, const char* name) {
+  const int64_t v = whole(o);
+  if (v < -(1 << 30) || v > (1 << 30)) value_error(std::string(name) + " is out of range");
+  return (int)v;
+}
+
+// The workspace: given, or made here; its size.
+size_t workspace(PyObject* given, size_t need, c10::Device dev, at::Tensor& ws) {
+  if (given == Py_None) {
+    ws = empty({(int64_t)(need > 0 ? need : 1)}, at::kByte, dev);
+  } else {
+    ws = tensor(given, "workspace");
+    if (!ws.is_contiguous() || ws.device() != dev) value_error("workspace must be contiguous and on " + dev.str());
+  }
+  return ws.nbytes();
+}
+
+// moe_route(logits, k, score, renormalize, out, stream): (ids, weights)
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("moe_route", n, 6, [&]() -> PyObject* {
+    const at::Tensor& L = tensor(a[0], "logits");
+    first(L, "logits");
+    const c10::Device dev = L.device();
+    const int64_t M = L.size(0), E = L.size(1);
+    const int64_t ld = row_stride(L, "logits", dev, M, E);
+    const int lc = float_code(L, "logits"), k = small(a[1], "k"), score = small(a[2], "score");
+    const int renorm = PyObject_IsTrue(a[3]);
+    if (renorm < 0) throw Raise{nullptr, ""};
+    at::Tensor ids, weights;
+    if (a[4] == Py_None) {
+      if (k < 1 || k > E) value_error("k must be 1 to the number of experts");
+      ids = empty({M, k}, at::kInt, dev);
+      weights = empty({M, k}, at::kFloat, dev);
+    } else {
+      if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 2) type_error("out must be a Routing");
+      ids = tensor(PyTuple_GET_ITEM(a[4], 0), "out.ids");
+      weights = tensor(PyTuple_GET_ITEM(a[4], 1), "out.weights");
+      plain(ids, "out.ids", dev, at::kInt, "int32", {M, k});
+      plain(weights, "out.weights", dev, at::kFloat, "float32", {M, k});
+    }
+    check(lib.moe_route(L.const_data_ptr(), lc, M, E, ld, k, score, renorm, static_cast<int32_t*>(ids.mutable_data_ptr()),
+                        static_cast<float*>(weights.mutable_data_ptr()), stream_of(a[5])),
+          "awq_moe_route");
+    if (a[4] != Py_None) return Py_NewRef(a[4]);
+    return pair(reinterpret_cast<PyTypeObject*>(routing_type), Ref(wrap(ids)), Ref(wrap(weights)));
+  });
+}
+
+struct Experts {  // moe_weight's handle: (data, E, N, K)
+  const void* data;
+  int64_t E, N, K;
+  Experts(PyObject* o, const char* name, c10::Device dev) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) type_error(std::string(name) + " must be the result of moe_weight");
+    const at::Tensor& t = tensor(PyTuple_GET_ITEM(o, 0), name);
+    E = whole(PyTuple_GET_ITEM(o, 1)), N = whole(PyTuple_GET_ITEM(o, 2)), K = whole(PyTuple_GET_ITEM(o, 3));
+    const size_t bytes = E > 0 && N > 0 && N < INT32_MAX && E < INT32_MAX ? lib.weight_bytes(E * N, K) : 0;
+    if (bytes == 0 || t.device() != dev || t.scalar_type() != at::kByte || !t.is_contiguous() || (size_t)t.numel() < bytes)
+      value_error(std::string(name) + " must be the result of moe_weight on " + dev.str());
+    data = t.const_data_ptr();
+  }
+};
+
+// moe(X, routing or logits, k, score, renormalize, gate_up, down, act, dtype, out, workspace, stream)
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("moe", n, 12, [&]() -> PyObject* {
+    const Rows X(a[0]);
+    const c10::Device dev = X.x.device();
+    const Experts gu(a[5], "gate_up", dev), down(a[6], "down", dev);
+    if (gu.E != down.E || gu.K != X.K || down.N != X.K || gu.N % 2 != 0 || gu.N / 2 != down.K)
+      value_error("X, gate_up and down disagree: [M, H], E experts of [2 I, H], E experts of [H, I]");
+    const int64_t E = gu.E, I = down.K;
+    const int act = small(a[7], "act"), score = small(a[3], "score");
+    int k = 0, lc = 0;
+    int64_t ldl = 0;
+    const void *ids = nullptr, *weights = nullptr, *logits = nullptr;
+    const bool routed = PyTuple_Check(a[1]);
+    if (routed) {
+      if (PyTuple_GET_SIZE(a[1]) != 2) type_error("routing must be a Routing or the router's logits");
+      if (a[2] != Py_None) value_error("k goes with logits");
+      const at::Tensor& ti = tensor(PyTuple_GET_ITEM(a[1], 0), "routing.ids");
+      const at::Tensor& tw = tensor(PyTuple_GET_ITEM(a[1], 1), "routing.weights");
+      if (ti.dim() != 2) value_error("routing.ids must be a [M, k] tensor");
+      if (ti.size(1) > 1 << 30) value_error("routing.ids has too many columns");
+      k = (int)ti.size(1);
+      ids = plain(ti, "routing.ids", dev, at::kInt, "int32", {X.M, k});
+      weights = plain(tw, "routing.weights", dev, at::kFloat, "float32", {X.M, k});
+    } else {
+      const at::Tensor& L = tensor(a[1], "routing");
+      if (a[2] == Py_None) value_error("logits need k");
+      k = small(a[2], "k");
+      lc = float_code(L, "logits");
+      ldl = row_stride(L, "logits", dev, X.M, E);
+      logits = L.const_data_ptr();
+    }
+    const int renorm = PyObject_IsTrue(a[4]);
+    if (renorm < 0) throw Raise{nullptr, ""};
+    at::ScalarType want = at::kFloat;
+    if (a[8] != Py_None) {
+      if (!THPDtype_Check(a[8])) type_error("dtype must be a torch.dtype");
+      want = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+    }
+    at::Tensor Y;
+    int64_t ldy = X.K;
+    if (a[9] == Py_None) {
+      if (want != at::kFloat && want != at::kBFloat16) type_error("dtype must be float32 or bfloat16");
+      Y = empty({X.M, X.K}, want, dev);
+    } else {
+      Y = tensor(a[9], "out");
+      ldy = row_stride(Y, "out", dev, X.M, X.K);
+      if (a[8] != Py_None && want != Y.scalar_type()) value_error("dtype and out disagree");
+    }
+    const int yc = float_code(Y, "out");
+    at::Tensor ws;
+    const size_t bytes = workspace(a[10], lib.moe_workspace_bytes(X.M, E, k, X.K, I), dev, ws);
+    const awq_stream_t st = stream_of(a[11]);
+    if (routed)
+      check(lib.moe(X.x.const_data_ptr(), X.code, X.scale_ptr, X.M, X.K, X.ld, static_cast<const int32_t*>(ids),
+                    static_cast<const float*>(weights), k, gu.data, down.data, E, I, 128, act, Y.mutable_data_ptr(), yc, ldy,
+                    ws.mutable_data_ptr(), bytes, st),
+            "awq_moe");
+    else
+      check(lib.moe_layer(X.x.const_data_ptr(), X.code, X.scale_ptr, X.M, X.K, X.ld, logits, lc, ldl, k, score, renorm,
+                          gu.data, down.data, E, I, 128, act, Y.mutable_data_ptr(), yc, ldy, ws.mutable_data_ptr(), bytes, st),
+            "awq_moe_layer");
+    return a[9] != Py_None ? Py_NewRef(a[9]) : wrap(Y);
+  });
+}
+
+// lora(X, A, B, ids, base, scale, ranks, out, workspace, stream)
+PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("lora", n, 10, [&]() -> PyObject* {
+    const Rows X(a[0]);
+    const c10::Device dev = X.x.device();
+    const at::Tensor& A = tensor(a[1], "A");
+    const at::Tensor& B = tensor(a[2], "B");
+    const at::Tensor& base = tensor(a[4], "base");
+    if (A.dim() != 3 || B.dim() != 3) value_error("A must be [adapters, R, K] and B [adapters, N, R]");
+    const int64_t count = A.size(0), R = A.size(1), N = B.size(1);
+    const void* ap = plain(A, "A", dev, at::kBFloat16, "bfloat16", {count, R, X.K});
+    const void* bp = plain(B, "B", dev, at::kBFloat16, "bfloat16", {count, N, R});
+    const void* ip = plain(tensor(a[3], "ids"), "ids", dev, at::kInt, "int32", {X.M});
+    const void *sp = nullptr, *rp = nullptr;
+    if (a[5] != Py_None) sp = plain(tensor(a[5], "scale"), "scale", dev, at::kFloat, "float32", {count});
+    if (a[6] != Py_None) rp = plain(tensor(a[6], "ranks"), "ranks", dev, at::kInt, "int32", {count});
+    const int yc = float_code(base, "base");
+    const int64_t ldb = row_stride(base, "base", dev, X.M, N);
+    at::Tensor Y;
+    int64_t ldy = N;
+    if (a[7] == Py_None) {
+      Y = empty({X.M, N}, base.scalar_type(), dev);
+    } else {
+      Y = tensor(a[7], "out");
+      if (Y.scalar_type() != base.scalar_type()) type_error("out must have base's dtype");
+      ldy = row_stride(Y, "out", dev, X.M, N);
+    }
+    at::Tensor ws;
+    const size_t bytes = workspace(a[8], lib.lora_workspace_bytes(X.M, X.K, N, R), dev, ws);
+    check(lib.lora(X.x.const_data_ptr(), X.code, X.scale_ptr, X.M, X.K, X.ld, ap, bp, count, R,
+                   static_cast<const int32_t*>(rp), static_cast<const float*>(sp), static_cast<const int32_t*>(ip),
+                   base.const_data_ptr(), ldb, Y.mutable_data_ptr(), yc, ldy, N, ws.mutable_data_ptr(), bytes, stream_of(a[9])),
+          "awq_lora");
+    return a[7] != Py_None ? Py_NewRef(a[7]) : wrap(Y);
+  });
+}
+
+// bind(addresses, Act8, Routing, AwqError): the library's functions in Lib's order, and the types
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long f[5];
-  PyObject *act8, *error;
-  if (!PyArg_ParseTuple(args, "KKKKKO!O", &f[0], &f[1], &f[2], &f[3], &f[4], &PyType_Type, &act8, &error))
+  PyObject *functions, *act8, *routing, *error;
+  if (!PyArg_ParseTuple(args, "O!O!O!O", &PyTuple_Type, &functions, &PyType_Type, &act8, &PyType_Type, &routing, &error))
     return nullptr;
-  if (!PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(act8), &PyTuple_Type)) {
-    PyErr_SetString(PyExc_TypeError, "Act8 must be a tuple type");
+  for (PyObject* t : {act8, routing}) {
+    if (!PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(t), &PyTuple_Type)) {
+      PyErr_SetString(PyExc_TypeError, "Act8 and Routing must be tuple types");
+      return nullptr;
+    }
+  }
+  constexpr Py_ssize_t kFunctions = sizeof(Lib) / sizeof(void*);
+  if (PyTuple_GET_SIZE(functions) != kFunctions) {
+    PyErr_SetString(PyExc_ValueError, "a wrong number of functions");
     return nullptr;
   }
-  lib.rmsnorm = reinterpret_cast<decltype(lib.rmsnorm)>(f[0]);
-  lib.act_mul = reinterpret_cast<decltype(lib.act_mul)>(f[1]);
-  lib.w4a8 = reinterpret_cast<decltype(lib.w4a8)>(f[2]);
-  lib.weight_bytes = reinterpret_cast<decltype(lib.weight_bytes)>(f[3]);
-  lib.workspace_bytes = reinterpret_cast<decltype(lib.workspace_bytes)>(f[4]);
+  void* f[kFunctions];
+  for (Py_ssize_t i = 0; i < kFunctions; ++i) {
+    f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(functions, i));
+    if (f[i] == nullptr) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a function's address is null");
+      return nullptr;
+    }
+  }
+  std::memcpy(&lib, f, sizeof(lib));
   Py_XSETREF(act8_type, Py_NewRef(act8));
+  Py_XSETREF(routing_type, Py_NewRef(routing));
   Py_XSETREF(error_type, Py_NewRef(error));
   Py_RETURN_NONE;
 }
@@ -342,6 +573,9 @@ PyMethodDef methods[] = {
     {"rmsnorm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rmsnorm)), METH_FASTCALL, nullptr},
     {"act_mul", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(act_mul)), METH_FASTCALL, nullptr},
     {"w4a8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(w4a8)), METH_FASTCALL, nullptr},
+    {"moe_route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(moe_route)), METH_FASTCALL, nullptr},
+    {"moe", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(moe)), METH_FASTCALL, nullptr},
+    {"lora", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(lora)), METH_FASTCALL, nullptr},
     {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_a8", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
