@@ -1,13 +1,13 @@
 // Mixture of experts over packed 4-bit weights, for the tokens of a decode batch or a short prompt:
 //   Y[m] = sum_j w[m, j] D_e (act(G_e x[m]) * (U_e x[m])),  e = ids[m, j]
-// Kernel 1 (up) forms act(gate) * up of every (token, expert) pair, kernel 2 (down) its product with D_e times w, kernel 3
-// adds a token's pairs in order.  A block belongs to one expert and some of its channels and streams that part of the weight
-// once for up to 32 of the expert's tokens; which tokens those are it finds itself, by a scan of the ids.
+// The up kernel forms act(gate) * up of every (token, expert) pair; a block belongs to one expert and a run of its channels,
+// keeps the expert's tokens as operands in registers and streams its part of the weight past them.  Which tokens those are
+// it finds itself, by a scan of the ids.  For few tokens the down kernel then takes all experts of some channels of Y in one
+// block and adds them up on chip; for more tokens it works like the up kernel, and a third kernel adds a token's pairs.
 //
 // A weight code becomes a bf16 operand exactly, as 16 + q (a nibble moved into the mantissa of 16.0: one instruction per
-// code and no conversion); a group's products with q - z are sum x (16 + q) - (16 + z) sum x, the second sum a product
-// with ones.  Both are fp32 sums of exact products, then multiplied with the group's step in fp32.  int8 activations take
-// the integer products instead, whose sums are exact.
+// code and no conversion).  A group's sum x (q - z) is sum x (16 + q) - (16 + z) sum x in fp32 sums of exact products, then
+// multiplied with the group's step in fp32.  int8 activations take the integer products instead, whose sums are exact.
 #include "moe_internal.h"
 #include "x_operand.h"
 
@@ -146,26 +146,90 @@ struct W8 {
   }
 };
 
-template <int T>
-__device__ __forceinline__ f32x4 dot(const bf16x8 (&x)[4][T], const bf16x8 (&w)[4]) {
-  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int t = T - 1; t >= 0; --t)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[s][t], w[s], r, 0, 0, 0);
-  return r;
-}
+// ---- sums over a group ---------------------------------------------------------------------------------
+// The activations of sixteen tokens (one per lane % 16) in a group, as operands: T bf16 terms, or int8 codes.
+__device__ __forceinline__ bf16x8 constant8(uint32_t two) { return __builtin_bit_cast(bf16x8, (u32x4){two, two, two, two}); }
 
-// A group of one token per lane % 16.  kTerms: bf16 terms, as stored (planes) or made from the type.
+template <int T>
+struct Terms {
+  using Weight = W16;
+  bf16x8 t[T][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < T; ++k)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) t[k][s] = constant8(0u);
+  }
+  // sum x of the group, for the zero points
+  __device__ __forceinline__ f32x4 ones() const {
+    const bf16x8 one = constant8(0x3f803f80u);
+    f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = T - 1; k >= 0; --k)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], one, r, 0, 0, 0);
+    return r;
+  }
+  // sum x (q - z).  INNER: every 32 products with 16 + q are followed by 32 with -(16 + z), so that no sum grows past those 32
+  // (a sum of 128 rounds at 24 sqrt(128) sigma for a result of 6 sqrt(128) sigma); z is a whole number.  For an fp32
+  // result: 512 -> 512 -> 512, error 1.1e-6 of its norm without.
+  template <bool INNER>
+  __device__ __forceinline__ f32x4 sum(const W16& w, float z, const f32x4 sx) const {
+    f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (INNER) {
+      const bf16x8 mz = constant8(pack_cut(-16.0f - z, -16.0f - z));
+#pragma unroll
+      for (int k = T - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], w.h[s], r, 0, 0, 0);
+          r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], mz, r, 0, 0, 0);
+        }
+      return r;
+    } else {
+#pragma unroll
+      for (int k = T - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], w.h[s], r, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = fmaf(-16.0f - z, sx[i], r[i]);
+      return r;
+    }
+  }
+};
+struct Codes {
+  using Weight = W8;
+  i32x4 b[2];
+  __device__ __forceinline__ void clear() { b[0] = b[1] = (i32x4){0, 0, 0, 0}; }
+  // |sum| is below 2^18: its fp32 form is exact
+  __device__ __forceinline__ static f32x4 dot(const i32x4 (&x)[2], const i32x4 (&w)[2]) {
+    i32x4 r = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i], w[i], r, 0, 0, 0);
+    return (f32x4){(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
+  }
+  __device__ __forceinline__ f32x4 ones() const {
+    const i32x4 one = {0x01010101, 0x01010101, 0x01010101, 0x01010101}, o[2] = {one, one};
+    return dot(b, o);
+  }
+  template <bool>
+  __device__ __forceinline__ f32x4 sum(const W8& w, float z, const f32x4 sx) const {
+    f32x4 r = dot(b, w.b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = fmaf(-z, sx[i], r[i]);  // exact
+    return r;
+  }
+};
+
+// How a group of one token is read: from X, or from the planes that the up kernel left.
 constexpr int kPlanes2 = 4, kPlanes3 = 5;  // beside kF32 .. kE4m3
 template <int XT>
-struct Tokens {
-  using Weight = W16;
-  static constexpr float kZero = 16.0f;  // what the operand holds beyond q
-  static constexpr int kTerms = XT == kF32 ? 3 : 1, kSize = XT == kF32 ? 4 : XT == kBf16 ? 2 : 1;
-  X8<XT> x[4];
-  __device__ __forceinline__ void load(const char* row, int64_t g, int64_t) {
+struct Source {
+  using Operand = Terms<XT == kF32 ? 3 : 1>;
+  static constexpr int kSize = XT == kF32 ? 4 : XT == kBf16 ? 2 : 1;
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
     const char* p = row + g * kGroup * kSize;
+    X8<XT> x[4];
     if constexpr (kSize == 1) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -176,82 +240,49 @@ struct Tokens {
 #pragma unroll
       for (int s = 0; s < 4; ++s) x[s].load(p + (64 * (s / 2) + 8 * (s % 2)) * kSize);
     }
-  }
-  template <int CT>
-  __device__ __forceinline__ void products(const Weight* w, f32x4 (&s)[CT], f32x4& sx) const {
-    bf16x8 t[4][kTerms];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i].terms(t[i]);
-    const u32x4 o = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-    const bf16x8 one = __builtin_bit_cast(bf16x8, o), ones[4] = {one, one, one, one};
-    sx = dot<kTerms>(t, ones);
+    for (int s = 0; s < 4; ++s) {
+      bf16x8 t[X8<XT>::kTerms];
+      x[s].terms(t);
 #pragma unroll
-    for (int q = 0; q < CT; ++q) s[q] = dot<kTerms>(t, w[q].h);
+      for (int k = 0; k < X8<XT>::kTerms; ++k) o.t[k][s] = t[k];
+    }
   }
 };
 template <>
-struct Tokens<kI8> {
-  using Weight = W8;
-  static constexpr float kZero = 0.0f;
+struct Source<kI8> {
+  using Operand = Codes;
   static constexpr int kSize = 1;
-  i32x4 x[2];
-  __device__ __forceinline__ void load(const char* row, int64_t g, int64_t) {
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const i32x4*>(row + g * kGroup + 64 * i);
-  }
-  // |sum| is below 2^18: its fp32 form is exact
-  __device__ __forceinline__ static f32x4 dot8(const i32x4 (&x)[2], const i32x4 (&w)[2]) {
-    i32x4 r = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i], w[i], r, 0, 0, 0);
-    return (f32x4){(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
-  }
-  template <int CT>
-  __device__ __forceinline__ void products(const Weight* w, f32x4 (&s)[CT], f32x4& sx) const {
-    const i32x4 one = {0x01010101, 0x01010101, 0x01010101, 0x01010101}, ones[2] = {one, one};
-    sx = dot8(x, ones);
-#pragma unroll
-    for (int q = 0; q < CT; ++q) s[q] = dot8(x, w[q].b);
+    for (int i = 0; i < 2; ++i) o.b[i] = *reinterpret_cast<const i32x4*>(row + g * kGroup + 64 * i);
   }
 };
 template <int T>
 struct Planes {
-  using Weight = W16;
-  static constexpr float kZero = 16.0f;
+  using Operand = Terms<T>;
   static constexpr int kSize = 2;
-  u32x4 x[T][4];
-  __device__ __forceinline__ void load(const char* row, int64_t g, int64_t plane) {  // plane: bytes
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t plane) {  // plane: bytes
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+    for (int k = 0; k < T; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        x[t][s] = *reinterpret_cast<const u32x4*>(row + t * plane + g * (2 * kGroup) + 128 * (s / 2) + 16 * (s % 2));
-  }
-  template <int CT>
-  __device__ __forceinline__ void products(const Weight* w, f32x4 (&s)[CT], f32x4& sx) const {
-    bf16x8 t[4][T];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < T; ++k) t[i][k] = __builtin_bit_cast(bf16x8, x[k][i]);
-    const u32x4 o = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-    const bf16x8 one = __builtin_bit_cast(bf16x8, o), ones[4] = {one, one, one, one};
-    sx = dot<T>(t, ones);
-#pragma unroll
-    for (int q = 0; q < CT; ++q) s[q] = dot<T>(t, w[q].h);
+        o.t[k][s] = __builtin_bit_cast(
+            bf16x8, *reinterpret_cast<const u32x4*>(row + k * plane + g * (2 * kGroup) + 128 * (s / 2) + 16 * (s % 2)));
   }
 };
 template <>
-struct Tokens<kPlanes2> : Planes<2> {};
+struct Source<kPlanes2> : Planes<2> {};
 template <>
-struct Tokens<kPlanes3> : Planes<3> {};
+struct Source<kPlanes3> : Planes<3> {};
 
 // ---- the pairs of an expert ---------------------------------------------------------------------------
-// list: the pairs p < P with ids[p] = e, ascending; returns their number.  All of the block's 512 threads.
+// list: the pairs p < P with ids[p] = e, ascending; returns their number.  All of the block's WV waves.
+template <int WV>
 __device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, uint16_t* list, int* counts) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int total = 0;
-  for (int p0 = 0; p0 < P; p0 += 512) {
+  for (int p0 = 0; p0 < P; p0 += 64 * WV) {
     const int p = p0 + (int)threadIdx.x;
     const bool hit = p < P && ids[p] == e;
     const uint64_t mask = __ballot(hit);
@@ -260,7 +291,7 @@ __device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, ui
     __syncthreads();
     int before = total;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < WV; ++w) {
       const int c = counts[w];
       if (w < wave) before += c;
       total += c;
@@ -271,70 +302,140 @@ __device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, ui
   return total;
 }
 
-// The block's expert and the list of its pairs: expert `slot` where slots are experts, else the expert of pair `slot`,
-// which the first of its pairs takes for all.  False: nothing to do, for the whole block.
-__device__ __forceinline__ bool block_expert(const MoeArgs& p, int slot, int P, bool by_pair, int e, uint16_t* list,
-                                             int* counts, int& n) {
-  if (e < 0 || e >= p.E) return false;
-  n = expert_pairs(p.ids, P, e, list, counts);
-  return n > 0 && (!by_pair || list[0] == slot);
+// Waves per SIMD that a kernel is built for: four (two blocks of eight waves on a CU) where its operands leave room.
+constexpr int waves_per_simd(size_t operands) { return operands <= 128 ? 4 : 2; }
+
+// The expert of a slot: experts, where there are at least as many pairs as experts, else the expert of the pair of that
+// number, which the first of its pairs takes for all.
+__device__ __forceinline__ int slot_expert(const MoeArgs& p, int slot) {
+  const int e = p.by_pair ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : slot;
+  return e >= 0 && e < p.E ? e : -1;
 }
 
-// ---- the stream ---------------------------------------------------------------------------------------
-// tot[t][q] of 16 TT tokens (row[t]: this lane's, at its channels) with two channel tiles, over this wave's groups: wave,
-// wave + 8, ...; D groups are requested ahead.
-template <typename X, int TT>
-__device__ __forceinline__ void stream(const ExpertWeights& w, const int64_t (&tile)[2], int G, int wave, int lane,
-                                       const char* const (&row)[TT], int64_t plane, f32x4 (&tot)[TT][2]) {
-  constexpr int WV = 8, D = sizeof(X) * TT > 128 ? 1 : 2;
-  const int c = lane & 15;
-  const uint32_t* codes[2];
-  const uint32_t* steps[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) codes[q] = w.codes + tile[q] * G * 256, steps[q] = w.steps + tile[q] * G * 16;
-#pragma unroll
-  for (int t = 0; t < TT; ++t)
-#pragma unroll
-    for (int q = 0; q < 2; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+// ---- an expert's tokens past a run of channel tiles -------------------------------------------------------
+// The block's WV waves share the groups, NG each at a time; the operands of 16 TT tokens stay in registers while the
+// weight passes (they are read again per tile where the groups are more than WV NG).  A step is a pair of channel tiles in
+// WV NG groups; every group's codes are requested a step ahead, into the registers that it just freed.  The waves' sums meet
+// in LDS, in wave order, and out(list position, pair of tiles, channel, sum of the one tile, of the other) takes them.
+struct Tiles {
+  int64_t first, other;  // the run's first tile, and how much further the second of a pair is
+  int step, count;       // from pair to pair; pairs
+};
+
+template <int SRC, int TT, int NG, int WV, bool INNER>
+struct ExpertPass {
+  using S = Source<SRC>;
+  using Op = typename S::Operand;
   struct Group {
     u32x4 w[2];
     uint32_t dz[2];
-    X x[TT];
-  } buf[D];
-  auto fetch = [&](Group& b, int64_t g) AWQ_INLINE {
+  } buf[NG];
+  ExpertWeights w;
+  Tiles tiles;
+  int G, wave, lane;
+
+  __device__ __forceinline__ void fetch(int i, int pair, int g0) {
+    int g = g0 + wave + i * WV;
+    g = g < G ? g : G - 1;  // past the last: loaded, with operands of zero
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes[q] + g * 256) + (unsigned)lane);
-      b.dz[q] = (steps[q] + g * 16)[(unsigned)c];
+      const int64_t at = (tiles.first + (int64_t)pair * tiles.step + q * tiles.other) * G + g;
+      buf[i].w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w.codes + at * 256) + (unsigned)lane);
+      buf[i].dz[q] = (w.steps + at * 16)[(unsigned)(lane & 15)];
     }
+  }
+  __device__ __forceinline__ void begin() {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) b.x[t].load(row[t], g, plane);
-  };
-  auto use = [&](const Group& b) AWQ_INLINE {
-    const typename X::Weight op[2] = {typename X::Weight(b.w[0]), typename X::Weight(b.w[1])};
+    for (int i = 0; i < NG; ++i) fetch(i, 0, 0);
+  }
+
+  // all of the expert's n tokens; row(list position) is a token's first channel for this lane
+  template <typename Row, typename Out>
+  __device__ __forceinline__ void run(int n, int64_t plane, float (*part)[WV][512], Row row, Out out) {
+    const int c = lane & 15, j = lane >> 4;
+    int turn = 0;
+    for (int t0 = 0; t0 < n; t0 += 16 * TT) {
+      const char* r[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      f32x4 s[2], sx;
-      b.x[t].template products<2>(op, s, sx);
+      for (int t = 0; t < TT; ++t) {
+        const int i = t0 + 16 * t + c;
+        r[t] = row(i < n ? i : n - 1);
+      }
+      Op x[TT][NG];
+      f32x4 sx[TT][NG];
+      for (int pair = 0; pair < tiles.count; ++pair) {
+        f32x4 tot[TT][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float d = half_lo(b.dz[q]), z = half_lo(b.dz[q] >> 16) + X::kZero;
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[t][q][i] = fmaf(d, fmaf(-z, sx[i], s[q][i]), tot[t][q][i]);
+          for (int q = 0; q < 2; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t first = (tiles.first + (int64_t)pair * tiles.step) * 16 + (threadIdx.x & 15);
+        const float power0 = w.powers[first], power1 = w.powers[first + 16 * tiles.other];
+        for (int g0 = 0; g0 < G; g0 += WV * NG) {
+          if (pair == 0 || G > WV * NG) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+              const int g = g0 + wave + i * WV;
+#pragma unroll
+              for (int t = 0; t < TT; ++t) {
+                if (t > 0 && t0 + 16 * t >= n) break;
+                if (g < G) S::load(x[t][i], r[t], g, plane);
+                else x[t][i].clear();
+              }
+            }
+            if constexpr (!INNER) {
+#pragma unroll
+              for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                  if (t > 0 && t0 + 16 * t >= n) break;
+                  sx[t][i] = x[t][i].ones();
+                }
+            }
+          }
+          // the step after this one
+          const bool same = g0 + WV * NG < G, more = pair + 1 < tiles.count || t0 + 16 * TT < n;
+          const int npair = same ? pair : pair + 1 < tiles.count ? pair + 1 : 0, ng0 = same ? g0 + WV * NG : 0;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const typename Op::Weight wq(buf[i].w[q]);
+              const float d = half_lo(buf[i].dz[q]), z = half_lo(buf[i].dz[q] >> 16);
+#pragma unroll
+              for (int t = 0; t < TT; ++t) {
+                if (t > 0 && t0 + 16 * t >= n) break;
+                const f32x4 v = x[t][i].template sum<INNER>(wq, z, sx[t][i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tot[t][q][k] = fmaf(d, v[k], tot[t][q][k]);
+              }
+            }
+            if (same || more) fetch(i, npair, ng0);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t, turn ^= 1) {
+          if (t > 0 && t0 + 16 * t >= n) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (t0 + 16 * t + 4 * j + k < n) {
+              part[turn][wave][(4 * j + k) * 16 + c] = tot[t][0][k];
+              part[turn][wave][256 + (4 * j + k) * 16 + c] = tot[t][1][k];
+            }
+          }
+          __syncthreads();  // and the buffer of two turns ago has been read
+          const int o = (int)threadIdx.x, at = t0 + 16 * t + o / 16;
+          if (o < 256 && at < n) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WV; ++v) a += part[turn][v][o], b += part[turn][v][256 + o];
+            out(at, pair, o % 16, a * power0, b * power1);
+          }
+        }
       }
     }
-  };
-  const int n = (G - wave + WV - 1) / WV;  // this wave's groups (none or fewer where G < wave)
-#pragma unroll
-  for (int i = 0; i < D; ++i)
-    if (i < n) fetch(buf[i], wave + i * WV);
-  for (int i0 = 0; i0 < n; i0 += D)
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if (i0 + i < n) use(buf[i]);
-      if (i0 + i + D < n) fetch(buf[i], wave + (int64_t)(i0 + i + D) * WV);
-    }
-}
+  }
+};
 
 __device__ __forceinline__ float activate(float g, int act) {
   if (act != 1) return 0.5f * g * erfcf(-g * 0.70710678f);
@@ -342,119 +443,244 @@ __device__ __forceinline__ float activate(float g, int act) {
   return (g < 0.0f ? g * e : g) / (1.0f + e);
 }
 
-// ---- kernel 1: act(gate) * up ----------------------------------------------------------------------------
-// A block: one expert, sixteen channels of I (a tile of gate rows and the tile of up rows beside it), its tokens 16 TT at a
-// time.
-template <int XT, int TT>
-__global__ __launch_bounds__(512) void moe_up_kernel(const MoeArgs p, bool by_pair) {
-  using X = Tokens<XT>;
-  __shared__ float part[8][512];
+// act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
+template <int XT, int TT, int NG, int WV, bool INNER>
+__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * TT * NG)) void moe_up_kernel(const MoeArgs p, int per) {
+  __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[8];
-  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = (int)blockIdx.y, P = p.M * p.k;
-  const int e = by_pair ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : slot;
-  int n = 0;
-  if (!block_expert(p, slot, P, by_pair, e, list, counts, n)) return;
-  const int64_t first = (int64_t)e * (p.I / 8) + blockIdx.x;  // its gate tile
-  const int64_t tile[2] = {first, first + p.I / 16};
+  __shared__ int counts[WV];
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, slot);
+  if (e < 0) return;
+  const int tile0 = (int)blockIdx.x * per, left = p.I / 16 - tile0;
+  ExpertPass<XT, TT, NG, WV, INNER> pass;
+  pass.w = p.up;
+  pass.tiles = Tiles{(int64_t)e * (p.I / 8) + tile0, p.I / 16, 1, left < per ? left : per};
+  pass.G = p.H / kGroup, pass.lane = lane, pass.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  pass.begin();
+  const int n = expert_pairs<WV>(p.ids, P, e, list, counts);
+  if (n == 0 || (p.by_pair && list[0] != slot)) return;
   const int64_t plane = (int64_t)P * p.I;
-  for (int t0 = 0; t0 < n; t0 += 16 * TT) {
-    const char* row[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int i = t0 + 16 * t + c;
-      row[t] = static_cast<const char*>(p.x) + ((int64_t)(list[i < n ? i : n - 1] / p.k) * p.ldx + 16 * j) * X::kSize;
-    }
-    f32x4 tot[TT][2];
-    stream<X, TT>(p.up, tile, p.H / kGroup, wave, lane, row, 0, tot);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      __syncthreads();  // the sums before are read
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][q * 256 + (4 * j + i) * 16 + c] = tot[t][q][i];
-      __syncthreads();
-      const int o = (int)threadIdx.x, at = t0 + 16 * t + o / 16;
-      if (o < 256 && at < n) {
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) g += part[w][o], u += part[w][256 + o];
-        const int pair = list[at];
-        g *= p.up.powers[tile[0] * 16 + o % 16];
-        u *= p.up.powers[tile[1] * 16 + o % 16];
+  pass.run(
+      n, 0, part,
+      [&](int i) AWQ_INLINE {
+        return static_cast<const char*>(p.x) + ((int64_t)(list[i] / p.k) * p.ldx + 16 * j) * Source<XT>::kSize;
+      },
+      [&](int at, int pair, int ch, float g, float u) AWQ_INLINE {
+        const int q = list[at];
         if constexpr (XT == kI8 || XT == kE4m3) {
-          const float s = p.xscale[pair / p.k];
+          const float s = p.xscale[q / p.k];
           g *= s, u *= s;
         }
         float v = activate(g, p.act) * u;
-        uint16_t* h = p.h + (int64_t)pair * p.I + (int64_t)blockIdx.x * 16 + o % 16;
+        uint16_t* h = p.h + (int64_t)q * p.I + (tile0 + pair) * 16 + ch;
         for (int s = 0; s < p.terms - 1; ++s) {  // all but the last cut, the last rounded
           h[s * plane] = (uint16_t)(bits(v) >> 16);
           v -= cut(v);
         }
         h[(p.terms - 1) * plane] = (uint16_t)pack_rne(v, v);
-      }
-    }
-  }
+      });
 }
 
-// ---- kernel 2: w D (...) per pair ---------------------------------------------------------------------------
-// A block: one expert, 32 channels of H.
-template <int T, int TT>
-__global__ __launch_bounds__(512) void moe_down_kernel(const MoeArgs p, bool by_pair) {
-  using X = Tokens<T == 2 ? kPlanes2 : kPlanes3>;
-  __shared__ float part[8][512];
+// w D (...) of every pair.  A block: a slot, `per` pairs of tiles of sixteen channels of H.
+template <int T, int TT, int NG, int WV>
+__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)) void moe_down_kernel(const MoeArgs p, int per) {
+  __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[8];
+  __shared__ int counts[WV];
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, slot);
+  if (e < 0) return;
+  const int pair0 = (int)blockIdx.x * per, left = p.H / 32 - pair0;
+  ExpertPass<T == 2 ? kPlanes2 : kPlanes3, TT, NG, WV, T == 3> pass;
+  pass.w = p.down;
+  pass.tiles = Tiles{(int64_t)e * (p.H / 16) + 2 * pair0, 1, 2, left < per ? left : per};
+  pass.G = p.I / kGroup, pass.lane = lane, pass.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  pass.begin();
+  const int n = expert_pairs<WV>(p.ids, P, e, list, counts);
+  if (n == 0 || (p.by_pair && list[0] != slot)) return;
+  pass.run(
+      n, (int64_t)P * p.I * 2, part,
+      [&](int i) AWQ_INLINE { return reinterpret_cast<const char*>(p.h + (int64_t)list[i] * p.I + 16 * j); },
+      [&](int at, int pair, int ch, float a, float b) AWQ_INLINE {
+        const int q = list[at];
+        float* o = p.o + (int64_t)q * p.H + (pair0 + pair) * 32 + ch;
+        o[0] = a * p.weights[q];
+        o[16] = b * p.weights[q];
+      });
+}
+
+// ---- few tokens: all experts of a run of channels of Y --------------------------------------------------------
+// A block: CT tiles of sixteen channels, a share of the work: items of one expert and one part of its groups, taken by the
+// waves in turn.  Every wave adds w D (...) into sums of its own in LDS, [token][channel]; they meet at the end in wave
+// order.  With one share the block writes Y, with more the shares' sums go to memory and another kernel adds them.
+template <int T, int CT, int WV>
+__global__ __launch_bounds__(64 * WV) void moe_down_few_kernel(const MoeArgs p, int parts) {
+  using S = Source<T == 2 ? kPlanes2 : kPlanes3>;
+  using Op = typename S::Operand;
+  constexpr int C = 16 * CT, DW = WV == 16 ? 3 : 4, DX = WV == 16 ? 1 : 2;
+  extern __shared__ float sums[];  // [WV][M][C]
+  __shared__ int16_t active[kMaxExperts], ids[kMoeFewPairs];
+  __shared__ float wts[kMoeFewPairs];
+  __shared__ uint8_t lists[WV][kMoeFewPairs];
+  __shared__ uint32_t has[kMaxExperts / 32];
+  __shared__ int counts[WV];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = (int)blockIdx.y, P = p.M * p.k;
-  const int e = by_pair ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : slot;
-  int n = 0;
-  if (!block_expert(p, slot, P, by_pair, e, list, counts, n)) return;
-  const int64_t first = (int64_t)e * (p.H / 16) + 2 * blockIdx.x;
-  const int64_t tile[2] = {first, first + 1};
-  const int64_t plane = (int64_t)P * p.I * 2;
-  for (int t0 = 0; t0 < n; t0 += 16 * TT) {
-    const char* row[TT];
+  const int share = (int)blockIdx.y, shares = (int)gridDim.y, P = p.M * p.k, G = p.I / kGroup;
+  const int per = (G + parts - 1) / parts;
+  for (int i = threadIdx.x; i < WV * p.M * C; i += 64 * WV) sums[i] = 0.0f;
+  for (int i = threadIdx.x; i < (int)(sizeof(has) / sizeof(has[0])); i += 64 * WV) has[i] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < P; i += 64 * WV) {
+    const int e = p.ids[i];
+    ids[i] = e >= 0 && e < p.E ? (int16_t)e : (int16_t)-1;
+    wts[i] = p.weights[i];
+    if (e >= 0 && e < p.E) atomicOr(&has[e / 32], 1u << e % 32);
+  }
+  __syncthreads();
+  int total = 0;  // experts with tokens
+  for (int s0 = 0; s0 < p.E; s0 += 64 * WV) {
+    const int s = s0 + (int)threadIdx.x;
+    const bool hit = s < p.E && (has[s / 32] >> s % 32 & 1u);
+    const uint64_t mask = __ballot(hit);
+    if (s0 > 0) __syncthreads();
+    if (lane == 0) counts[wave] = __popcll(mask);
+    __syncthreads();
+    int before = total;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int i = t0 + 16 * t + c;
-      row[t] = reinterpret_cast<const char*>(p.h + (int64_t)list[i < n ? i : n - 1] * p.I + 16 * j);
+    for (int w = 0; w < WV; ++w) {
+      const int k = counts[w];
+      if (w < wave) before += k;
+      total += k;
     }
-    f32x4 tot[TT][2];
-    stream<X, TT>(p.down, tile, p.I / kGroup, wave, lane, row, plane, tot);
+    if (hit) active[before + __popcll(mask & ((1ull << lane) - 1))] = (int16_t)s;
+  }
+  __syncthreads();
+  float* mine = sums + wave * p.M * C;
+  uint8_t* list = lists[wave];
+  const int64_t plane = (int64_t)P * p.I * 2;
+  for (int item = share * WV + wave; item < total * parts; item += shares * WV) {
+    const int e = __builtin_amdgcn_readfirstlane((int)active[item / parts]);
+    const int g0 = item % parts * per, ng = G - g0 < per ? G - g0 : per;
+    if (ng <= 0) continue;
+    const int64_t first = (int64_t)e * (p.H / 16) + (int64_t)blockIdx.x * CT;
+    const uint32_t* codes = p.down.codes + (first * G + g0) * 256;
+    const uint32_t* steps = p.down.steps + (first * G + g0) * 16;
+    float power[CT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      __syncthreads();
+    for (int q = 0; q < CT; ++q) power[q] = p.down.powers[(first + q) * 16 + c];
+    struct Group {
+      u32x4 w[CT];
+      uint32_t dz[CT];
+    } buf[DW];
+    auto fetch = [&](Group& b, int g) AWQ_INLINE {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < CT; ++q) {
+        b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + ((int64_t)q * G + g) * 256) + (unsigned)lane);
+        b.dz[q] = (steps + ((int64_t)q * G + g) * 16)[(unsigned)c];
+      }
+    };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][(4 * j + i) * 32 + 16 * q + c] = tot[t][q][i];
-      __syncthreads();
-      const int o = (int)threadIdx.x, at = t0 + 16 * t + o / 32;
-      if (at < n) {
-        float s = 0.0f;
+    for (int i = 0; i < DW; ++i)
+      if (i < ng) fetch(buf[i], i);
+    int n = 0;  // the expert's pairs, in this wave's own list
+    for (int p0 = 0; p0 < P; p0 += 64) {
+      const bool hit = p0 + lane < P && ids[p0 + lane] == e;
+      const uint64_t mask = __ballot(hit);
+      if (hit) list[n + __popcll(mask & ((1ull << lane) - 1))] = (uint8_t)(p0 + lane);
+      n += __popcll(mask);
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int t0 = 0; t0 < n; t0 += 16) {
+      if (t0 > 0) {
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += part[w][o];
-        const int pair = list[at];
-        p.o[(int64_t)pair * p.H + (int64_t)blockIdx.x * 32 + o % 32] = s * p.down.powers[first * 16 + o % 32] * p.weights[pair];
+        for (int i = 0; i < DW; ++i)
+          if (i < ng) fetch(buf[i], i);
+      }
+      const char* row = reinterpret_cast<const char*>(p.h + (int64_t)list[t0 + c < n ? t0 + c : n - 1] * p.I + 16 * j) +
+                        (int64_t)g0 * (2 * kGroup);
+      Op x[DX];
+#pragma unroll
+      for (int i = 0; i < DX; ++i)
+        if (i < ng) S::load(x[i], row, i, plane);
+      f32x4 tot[CT];
+#pragma unroll
+      for (int q = 0; q < CT; ++q) tot[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i0 = 0; i0 < ng; i0 += DW) {
+#pragma unroll
+        for (int u = 0; u < DW; ++u) {
+          if (i0 + u < ng) {
+            const f32x4 sx = T == 2 ? x[u % DX].ones() : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < CT; ++q) {
+              const typename Op::Weight w(buf[u].w[q]);
+              const f32x4 s = x[u % DX].template sum<T == 3>(w, half_lo(buf[u].dz[q] >> 16), sx);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) tot[q][k] = fmaf(half_lo(buf[u].dz[q]), s[k], tot[q][k]);
+            }
+            if (i0 + u + DW < ng) fetch(buf[u], i0 + u + DW);
+            if (i0 + u + DX < ng) S::load(x[u % DX], row, i0 + u + DX, plane);
+          }
+        }
+      }
+      // a token that has this expert twice has neighbouring places in the list: four rows at a time then
+      int tok[4];
+      float wt[4];
+      bool twice = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = t0 + 4 * j + k, q = at < n ? list[at] : 0;
+        tok[k] = at < n ? q / p.k : -1;
+        wt[k] = at < n ? wts[q] : 0.0f;
+        if (k > 0) twice |= tok[k] >= 0 && tok[k] == tok[k - 1];
+        if (k == 0 && j > 0 && at < n) twice |= list[at - 1] / p.k == tok[0];
+      }
+      if (__ballot(twice) == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (tok[k] >= 0)
+#pragma unroll
+            for (int q = 0; q < CT; ++q) mine[tok[k] * C + 16 * q + c] += tot[q][k] * power[q] * wt[k];
+      } else {
+        for (int jj = 0; jj < 4; ++jj) {
+          if (j == jj) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (tok[k] >= 0)
+#pragma unroll
+                for (int q = 0; q < CT; ++q) mine[tok[k] * C + 16 * q + c] += tot[q][k] * power[q] * wt[k];
+          }
+          __builtin_amdgcn_wave_barrier();
+        }
       }
     }
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.M * C; i += 64 * WV) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WV; ++w) s += sums[w * p.M * C + i];
+    const int m = i / C, n = (int)blockIdx.x * C + i % C;
+    if (shares > 1) p.o[((int64_t)share * p.M + m) * p.H + n] = s;
+    else if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_rne(s, s);
+    else static_cast<float*>(p.y)[m * p.ldy + n] = s;
+  }
 }
 
-// ---- kernel 3: a token's pairs in order -----------------------------------------------------------------------
-__global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
+// ---- sums in order -----------------------------------------------------------------------------------------
+// Y from a token's pairs (shares = 0), or from the shares of the down kernel.
+__global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p, int shares) {
   const int m = (int)blockIdx.y, n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
   if (n >= p.H) return;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < p.k; ++j) {
-    const int e = p.ids[m * p.k + j];
-    if (e >= 0 && e < p.E) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)m * p.k + j) * p.H + n);
+  if (shares > 0) {
+    for (int j = 0; j < shares; ++j) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)j * p.M + m) * p.H + n);
+  } else {
+    for (int j = 0; j < p.k; ++j) {
+      const int e = p.ids[m * p.k + j];
+      if (e >= 0 && e < p.E) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)m * p.k + j) * p.H + n);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -463,23 +689,74 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
   }
 }
 
-template <int XT>
-hipError_t launch_experts(const MoeArgs& a, hipStream_t st) {
-  const int P = a.M * a.k;
-  const bool by_pair = P < a.E;
-  const unsigned slots = (unsigned)(by_pair ? P : a.E);
-  const bool wide = P > 8 * a.E;  // more than eight tokens an expert: 32 at a time
-  const dim3 up((unsigned)(a.I / 16), slots), down((unsigned)(a.H / 32), slots);
-  if (wide) moe_up_kernel<XT, 2><<<up, 512, 0, st>>>(a, by_pair);
-  else moe_up_kernel<XT, 1><<<up, 512, 0, st>>>(a, by_pair);
-  if (a.terms == 2) {
-    if (wide) moe_down_kernel<2, 2><<<down, 512, 0, st>>>(a, by_pair);
-    else moe_down_kernel<2, 1><<<down, 512, 0, st>>>(a, by_pair);
+// Blocks of a run of `units` per slot: about 512 in all (two on a CU) of eight waves, 256 of sixteen.
+int units_per_block(int slots, int units, int waves) {
+  const int total = 4096 / waves, blocks = (total + slots - 1) / slots;
+  const int per = (units + blocks - 1) / blocks;
+  return per < 1 ? 1 : per;
+}
+
+template <int XT, int TT, int NG, int WV, bool INNER>
+void up_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
+  const int per = units_per_block((int)slots, a.I / 16, WV);
+  moe_up_kernel<XT, TT, NG, WV, INNER><<<dim3((unsigned)((a.I / 16 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
+}
+template <int XT, bool INNER>
+void launch_up(const MoeArgs& a, unsigned slots, bool wide, hipStream_t st) {
+  const int G = a.H / kGroup;
+  if (wide) {
+    if (G <= 8) up_with<XT, 2, 1, 8, INNER>(a, slots, st);
+    else up_with<XT, 2, 1, XT == kF32 ? 8 : 16, INNER>(a, slots, st);
   } else {
-    if (wide) moe_down_kernel<3, 2><<<down, 512, 0, st>>>(a, by_pair);
-    else moe_down_kernel<3, 1><<<down, 512, 0, st>>>(a, by_pair);
+    if (G <= 8) up_with<XT, 1, 1, 8, INNER>(a, slots, st);
+    else if (G <= 16) up_with<XT, 1, 2, 8, INNER>(a, slots, st);
+    else up_with<XT, 1, XT == kF32 ? 1 : 2, 16, INNER>(a, slots, st);
   }
-  moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a);
+}
+
+template <int T, int TT, int NG, int WV>
+void down_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
+  const int per = units_per_block((int)slots, a.H / 32, WV);
+  moe_down_kernel<T, TT, NG, WV><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
+}
+template <int T>
+void launch_down(const MoeArgs& a, unsigned slots, bool wide, hipStream_t st) {
+  const int G = a.I / kGroup;
+  if (wide) down_with<T, 2, 1, 8>(a, slots, st);
+  else if (G <= 8) down_with<T, 1, 1, 8>(a, slots, st);
+  else down_with<T, 1, 1, 16>(a, slots, st);
+}
+
+template <int T>
+void launch_down_few(const MoeArgs& a, int shares, int parts, hipStream_t st) {
+  constexpr int WV = T == 2 ? 16 : 8;
+  const size_t lds = (size_t)WV * a.M * 16 * 4;
+  moe_down_few_kernel<T, 1, WV><<<dim3((unsigned)(a.H / 16), (unsigned)shares), 64 * WV, lds, st>>>(a, parts);
+}
+
+template <int XT>
+hipError_t launch_experts(MoeArgs a, hipStream_t st) {
+  const int P = a.M * a.k;
+  a.by_pair = P < a.E;
+  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
+  const bool wide = P > 12 * a.E;  // more than twelve tokens an expert: up to 32 at a time
+  const bool few = P <= kMoeFewPairs;
+  if (a.terms == 2) launch_up<XT, false>(a, slots, wide, st);
+  else launch_up<XT, XT != kI8>(a, slots, wide, st);
+  int shares = 0;
+  if (few) {
+    const int G = a.I / kGroup;
+    shares = 1;
+    int parts = 1;
+    while ((int)slots * parts < 64 && G / (2 * parts) >= 4) parts *= 2;
+    if (a.terms == 2) launch_down_few<2>(a, shares, parts, st);
+    else launch_down_few<3>(a, shares, parts, st);
+    if (shares == 1) return hipGetLastError();
+  } else {
+    if (a.terms == 2) launch_down<2>(a, slots, wide, st);
+    else launch_down<3>(a, slots, wide, st);
+  }
+  moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a, shares);
   return hipGetLastError();
 }
 
