@@ -223,22 +223,31 @@ struct Codes {
 
 // How a group of one token is read: from X, or from the planes that the up kernel left.
 constexpr int kPlanes2 = 4, kPlanes3 = 5;  // beside kF32 .. kE4m3
+// gather: piece(i) is where the group's i-th 16 bytes of the lane's token are, j = lane / 16 which of its channels;
+// load: the same for a row in memory, from this lane's first channel on.
 template <int XT>
 struct Source {
   using Operand = Terms<XT == kF32 ? 3 : 1>;
-  static constexpr int kSize = XT == kF32 ? 4 : XT == kBf16 ? 2 : 1;
-  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
-    const char* p = row + g * kGroup * kSize;
+  static constexpr int kSize = XT == kF32 ? 4 : XT == kBf16 ? 2 : 1, kPlanes = 1;
+  template <typename Piece>
+  static __device__ __forceinline__ void gather(Operand& o, Piece piece, int j, int) {
     X8<XT> x[4];
     if constexpr (kSize == 1) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(p + 64 * i);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(piece(j + 4 * i));
         x[2 * i].w[0] = v[0], x[2 * i].w[1] = v[1], x[2 * i + 1].w[0] = v[2], x[2 * i + 1].w[1] = v[3];
       }
     } else {
+      constexpr int kEach = kSize / 2;  // pieces of eight channels
 #pragma unroll
-      for (int s = 0; s < 4; ++s) x[s].load(p + (64 * (s / 2) + 8 * (s % 2)) * kSize);
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(piece(kEach * (2 * j + 8 * (s / 2) + s % 2) + i));
+#pragma unroll
+          for (int d = 0; d < 4; ++d) x[s].w[4 * i + d] = v[d];
+        }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -248,27 +257,41 @@ struct Source {
       for (int k = 0; k < X8<XT>::kTerms; ++k) o.t[k][s] = t[k];
     }
   }
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
+    const char* p = row + g * kGroup * kSize;
+    gather(o, [&](int i) AWQ_INLINE { return p + 16 * i; }, 0, 0);
+  }
 };
 template <>
 struct Source<kI8> {
   using Operand = Codes;
-  static constexpr int kSize = 1;
-  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
+  static constexpr int kSize = 1, kPlanes = 1;
+  template <typename Piece>
+  static __device__ __forceinline__ void gather(Operand& o, Piece piece, int j, int) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) o.b[i] = *reinterpret_cast<const i32x4*>(row + g * kGroup + 64 * i);
+    for (int i = 0; i < 2; ++i) o.b[i] = *reinterpret_cast<const i32x4*>(piece(j + 4 * i));
+  }
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t) {
+    const char* p = row + g * kGroup;
+    gather(o, [&](int i) AWQ_INLINE { return p + 16 * i; }, 0, 0);
   }
 };
 template <int T>
 struct Planes {
   using Operand = Terms<T>;
-  static constexpr int kSize = 2;
-  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t plane) {  // plane: bytes
+  static constexpr int kSize = 2, kPlanes = T;
+  template <typename Piece>
+  static __device__ __forceinline__ void gather(Operand& o, Piece piece, int j, int64_t plane) {  // plane: bytes
 #pragma unroll
     for (int k = 0; k < T; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         o.t[k][s] = __builtin_bit_cast(
-            bf16x8, *reinterpret_cast<const u32x4*>(row + k * plane + g * (2 * kGroup) + 128 * (s / 2) + 16 * (s % 2)));
+            bf16x8, *reinterpret_cast<const u32x4*>(piece(2 * j + 8 * (s / 2) + s % 2) + k * plane));
+  }
+  static __device__ __forceinline__ void load(Operand& o, const char* row, int64_t g, int64_t plane) {
+    const char* p = row + g * (2 * kGroup);
+    gather(o, [&](int i) AWQ_INLINE { return p + 16 * i; }, 0, plane);
   }
 };
 template <>
@@ -443,6 +466,16 @@ __device__ __forceinline__ float activate(float g, int act) {
   return (g < 0.0f ? g * e : g) / (1.0f + e);
 }
 
+// h of a pair and channel as bf16 terms: all but the last cut, the last rounded.
+__device__ __forceinline__ void store_h(const MoeArgs& p, int64_t plane, int pair, int ch, float v) {
+  uint16_t* h = p.h + (int64_t)pair * p.I + ch;
+  for (int s = 0; s < p.terms - 1; ++s) {
+    h[s * plane] = (uint16_t)(bits(v) >> 16);
+    v -= cut(v);
+  }
+  h[(p.terms - 1) * plane] = (uint16_t)pack_rne(v, v);
+}
+
 // act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
 template <int XT, int TT, int NG, int WV, bool INNER>
 __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * TT * NG)) void moe_up_kernel(const MoeArgs p, int per) {
@@ -472,13 +505,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>:
           const float s = p.xscale[q / p.k];
           g *= s, u *= s;
         }
-        float v = activate(g, p.act) * u;
-        uint16_t* h = p.h + (int64_t)q * p.I + (tile0 + pair) * 16 + ch;
-        for (int s = 0; s < p.terms - 1; ++s) {  // all but the last cut, the last rounded
-          h[s * plane] = (uint16_t)(bits(v) >> 16);
-          v -= cut(v);
-        }
-        h[(p.terms - 1) * plane] = (uint16_t)pack_rne(v, v);
+        store_h(p, plane, q, (tile0 + pair) * 16 + ch, activate(g, p.act) * u);
       });
 }
 
@@ -510,177 +537,203 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)
       });
 }
 
-// ---- few tokens: all experts of a run of channels of Y --------------------------------------------------------
-// A block: CT tiles of sixteen channels, a share of the work: items of one expert and one part of its groups, taken by the
-// waves in turn.  Every wave adds w D (...) into sums of its own in LDS, [token][channel]; they meet at the end in wave
-// order.  With one share the block writes Y, with more the shares' sums go to memory and another kernel adds them.
-template <int T, int CT, int WV>
-__global__ __launch_bounds__(64 * WV) void moe_down_few_kernel(const MoeArgs p, int parts) {
-  using S = Source<T == 2 ? kPlanes2 : kPlanes3>;
-  using Op = typename S::Operand;
-  constexpr int C = 16 * CT, DW = WV == 16 ? 3 : 4, DX = WV == 16 ? 1 : 2;
-  extern __shared__ float sums[];  // [WV][M][C]
-  __shared__ int16_t active[kMaxExperts], ids[kMoeFewPairs];
-  __shared__ float wts[kMoeFewPairs];
-  __shared__ uint8_t lists[WV][kMoeFewPairs];
-  __shared__ uint32_t has[kMaxExperts / 32];
-  __shared__ int counts[WV];
-  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int share = (int)blockIdx.y, shares = (int)gridDim.y, P = p.M * p.k, G = p.I / kGroup;
-  const int per = (G + parts - 1) / parts;
-  for (int i = threadIdx.x; i < WV * p.M * C; i += 64 * WV) sums[i] = 0.0f;
-  for (int i = threadIdx.x; i < (int)(sizeof(has) / sizeof(has[0])); i += 64 * WV) has[i] = 0u;
-  __syncthreads();
-  for (int i = threadIdx.x; i < P; i += 64 * WV) {
-    const int e = p.ids[i];
-    ids[i] = e >= 0 && e < p.E ? (int16_t)e : (int16_t)-1;
-    wts[i] = p.weights[i];
-    if (e >= 0 && e < p.E) atomicOr(&has[e / 32], 1u << e % 32);
+// ---- many tokens an expert: tiles ---------------------------------------------------------------------------
+// A block of four waves: a slot's tokens 16 TM at a time with 256 channels of the weight (up: 128 gate rows and the up rows
+// beside them), all groups one after the other.  A wave has all the tokens and four channel tiles, whose codes come straight
+// into registers a group ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing is
+// summed across waves, and a code is unpacked once for 16 TM tokens.
+// Rows in LDS hold their 16-byte pieces at piece ^ swizzle(row): the reads of sixteen rows' same piece use every bank once.
+template <int SRC, int TM>
+struct TileStage {
+  using S = Source<SRC>;
+  static constexpr int kPlanes = S::kPlanes, kRow = kGroup * S::kSize, kPieces = kRow / 16;  // of a row of a plane
+  static constexpr int kPer = 16 * TM * kPieces / 256;  // pieces of a plane per thread
+  static constexpr int kPlane = 16 * TM * kRow, kBytes = kPlanes * kPlane;
+  static_assert(kPer >= 1, "every thread has a piece");
+  static __device__ __forceinline__ int place(int row, int piece) {
+    return row * kRow + 16 * (piece ^ (kPieces == 8 ? row >> 1 & 7 : row & 15));
   }
-  __syncthreads();
-  int total = 0;  // experts with tokens
-  for (int s0 = 0; s0 < p.E; s0 += 64 * WV) {
-    const int s = s0 + (int)threadIdx.x;
-    const bool hit = s < p.E && (has[s / 32] >> s % 32 & 1u);
-    const uint64_t mask = __ballot(hit);
-    if (s0 > 0) __syncthreads();
-    if (lane == 0) counts[wave] = __popcll(mask);
-    __syncthreads();
-    int before = total;
+  const char* from[kPer];
+  u32x4 v[kPlanes][kPer];
+  // row(r) is where row r of the tile starts in memory
+  template <typename Row>
+  __device__ __forceinline__ void point(Row row) {
 #pragma unroll
-    for (int w = 0; w < WV; ++w) {
-      const int k = counts[w];
-      if (w < wave) before += k;
-      total += k;
+    for (int i = 0; i < kPer; ++i) {
+      const int q = (int)threadIdx.x + 256 * i;
+      from[i] = row(q / kPieces) + 16 * (q % kPieces);
     }
-    if (hit) active[before + __popcll(mask & ((1ull << lane) - 1))] = (int16_t)s;
   }
-  __syncthreads();
-  float* mine = sums + wave * p.M * C;
-  uint8_t* list = lists[wave];
-  const int64_t plane = (int64_t)P * p.I * 2;
-  for (int item = share * WV + wave; item < total * parts; item += shares * WV) {
-    const int e = __builtin_amdgcn_readfirstlane((int)active[item / parts]);
-    const int g0 = item % parts * per, ng = G - g0 < per ? G - g0 : per;
-    if (ng <= 0) continue;
-    const int64_t first = (int64_t)e * (p.H / 16) + (int64_t)blockIdx.x * CT;
-    const uint32_t* codes = p.down.codes + (first * G + g0) * 256;
-    const uint32_t* steps = p.down.steps + (first * G + g0) * 16;
-    float power[CT];
+  __device__ __forceinline__ void load(int g, int64_t plane) {
 #pragma unroll
-    for (int q = 0; q < CT; ++q) power[q] = p.down.powers[(first + q) * 16 + c];
-    struct Group {
-      u32x4 w[CT];
-      uint32_t dz[CT];
-    } buf[DW];
-    auto fetch = [&](Group& b, int g) AWQ_INLINE {
+    for (int k = 0; k < kPlanes; ++k)
 #pragma unroll
-      for (int q = 0; q < CT; ++q) {
-        b.w[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + ((int64_t)q * G + g) * 256) + (unsigned)lane);
-        b.dz[q] = (steps + ((int64_t)q * G + g) * 16)[(unsigned)c];
+      for (int i = 0; i < kPer; ++i) v[k][i] = *reinterpret_cast<const u32x4*>(from[i] + (int64_t)g * kRow + k * plane);
+  }
+  __device__ __forceinline__ void store(char* stage) const {
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int q = (int)threadIdx.x + 256 * i;
+        *reinterpret_cast<u32x4*>(stage + k * kPlane + place(q / kPieces, q % kPieces)) = v[k][i];
+      }
+  }
+  // the operand of the sixteen tokens from row 16 t on
+  static __device__ __forceinline__ void read(typename S::Operand& o, const char* stage, int t, int c, int j) {
+    const int row = 16 * t + c;
+    auto piece = [&](int p) AWQ_INLINE { return stage + place(row, p); };
+    S::gather(o, piece, j, kPlane);
+  }
+};
+
+template <int SRC, int TM, bool INNER>
+struct TilePass {
+  using Stage = TileStage<SRC, TM>;
+  using Op = typename Source<SRC>::Operand;
+  // tot[t][q] of tiles tile[q] over all groups; used: the token tiles that hold any token.  All four waves.
+  static __device__ __forceinline__ void run(const ExpertWeights& w, const int64_t (&tile)[4], int G, Stage& st, int64_t plane,
+                                             char* lds, int used, int lane, f32x4 (&tot)[TM][4]) {
+    const int c = lane & 15, j = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 codes[4];
+    uint32_t dz[4];
+    auto fetch = [&](int g) AWQ_INLINE {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        codes[q] = *(reinterpret_cast<const u32x4*>(w.codes + (tile[q] * G + g) * 256) + (unsigned)lane);
+        dz[q] = (w.steps + (tile[q] * G + g) * 16)[(unsigned)c];
       }
     };
+    fetch(0);
+    st.load(0, plane);
+    __syncthreads();  // the stages have been read
+    st.store(lds);
+    if (G > 1) st.load(1, plane);
+    __syncthreads();
+    for (int g = 0; g < G; ++g) {
+      const char* now = lds + (g & 1) * Stage::kBytes;
+      typename Op::Weight op[4] = {typename Op::Weight(codes[0]), typename Op::Weight(codes[1]), typename Op::Weight(codes[2]),
+                                   typename Op::Weight(codes[3])};
+      float d[4], z[4];
 #pragma unroll
-    for (int i = 0; i < DW; ++i)
-      if (i < ng) fetch(buf[i], i);
-    int n = 0;  // the expert's pairs, in this wave's own list
-    for (int p0 = 0; p0 < P; p0 += 64) {
-      const bool hit = p0 + lane < P && ids[p0 + lane] == e;
-      const uint64_t mask = __ballot(hit);
-      if (hit) list[n + __popcll(mask & ((1ull << lane) - 1))] = (uint8_t)(p0 + lane);
-      n += __popcll(mask);
-    }
-    __builtin_amdgcn_wave_barrier();
-    for (int t0 = 0; t0 < n; t0 += 16) {
-      if (t0 > 0) {
-#pragma unroll
-        for (int i = 0; i < DW; ++i)
-          if (i < ng) fetch(buf[i], i);
+      for (int q = 0; q < 4; ++q) d[q] = half_lo(dz[q]), z[q] = half_lo(dz[q] >> 16);
+      if (g + 1 < G) {
+        fetch(g + 1);
+        st.store(lds + (g + 1 & 1) * Stage::kBytes);
       }
-      const char* row = reinterpret_cast<const char*>(p.h + (int64_t)list[t0 + c < n ? t0 + c : n - 1] * p.I + 16 * j) +
-                        (int64_t)g0 * (2 * kGroup);
-      Op x[DX];
+      if (g + 2 < G) st.load(g + 2, plane);
 #pragma unroll
-      for (int i = 0; i < DX; ++i)
-        if (i < ng) S::load(x[i], row, i, plane);
-      f32x4 tot[CT];
+      for (int t = 0; t < TM; ++t) {
+        if (t > 0 && t >= used) break;
+        Op x;
+        Stage::read(x, now, t, c, j);
+        f32x4 sx = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (!INNER) sx = x.ones();
 #pragma unroll
-      for (int q = 0; q < CT; ++q) tot[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-      for (int i0 = 0; i0 < ng; i0 += DW) {
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = x.template sum<INNER>(op[q], z[q], sx);
 #pragma unroll
-        for (int u = 0; u < DW; ++u) {
-          if (i0 + u < ng) {
-            const f32x4 sx = T == 2 ? x[u % DX].ones() : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int q = 0; q < CT; ++q) {
-              const typename Op::Weight w(buf[u].w[q]);
-              const f32x4 s = x[u % DX].template sum<T == 3>(w, half_lo(buf[u].dz[q] >> 16), sx);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tot[q][k] = fmaf(half_lo(buf[u].dz[q]), s[k], tot[q][k]);
-            }
-            if (i0 + u + DW < ng) fetch(buf[u], i0 + u + DW);
-            if (i0 + u + DX < ng) S::load(x[u % DX], row, i0 + u + DX, plane);
-          }
+          for (int k = 0; k < 4; ++k) tot[t][q][k] = fmaf(d[q], v[k], tot[t][q][k]);
         }
       }
-      // a token that has this expert twice has neighbouring places in the list: four rows at a time then
-      int tok[4];
-      float wt[4];
-      bool twice = false;
+      __syncthreads();
+    }
+  }
+};
+
+template <int XT, int TM, bool INNER>
+__global__ __launch_bounds__(256) void moe_up_tile_kernel(const MoeArgs p) {
+  using Stage = TileStage<XT, TM>;
+  __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
+  __shared__ uint16_t list[kMoePairs];
+  __shared__ int counts[4];
+  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = (int)blockIdx.y, P = p.M * p.k;
+  const int n = expert_pairs<4>(p.ids, P, e, list, counts);
+  const int tile0 = (int)blockIdx.x * 8 + 2 * wave;  // of I: this wave's two
+  const int64_t first = (int64_t)e * (p.I / 8) + tile0, up = p.I / 16;
+  const int64_t tile[4] = {first, first + 1, first + up, first + 1 + up}, plane = (int64_t)P * p.I;
+  for (int t0 = (int)blockIdx.z * 16 * TM; t0 < n; t0 += 16 * TM * (int)gridDim.z) {
+    Stage st;
+    st.point([&](int r) AWQ_INLINE {
+      return static_cast<const char*>(p.x) + (int64_t)(list[t0 + r < n ? t0 + r : n - 1] / p.k) * p.ldx * Source<XT>::kSize;
+    });
+    f32x4 tot[TM][4];
+    TilePass<XT, TM, INNER>::run(p.up, tile, p.H / kGroup, st, 0, lds, (n - t0 + 15) / 16, lane, tot);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int at = t0 + 4 * j + k, q = at < n ? list[at] : 0;
-        tok[k] = at < n ? q / p.k : -1;
-        wt[k] = at < n ? wts[q] : 0.0f;
-        if (k > 0) twice |= tok[k] >= 0 && tok[k] == tok[k - 1];
-        if (k == 0 && j > 0 && at < n) twice |= list[at - 1] / p.k == tok[0];
-      }
-      if (__ballot(twice) == 0) {
+    for (int q = 0; q < 2; ++q) {
+      const float pg = p.up.powers[tile[q] * 16 + c], pu = p.up.powers[tile[2 + q] * 16 + c];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (tok[k] >= 0)
+      for (int t = 0; t < TM; ++t) {
 #pragma unroll
-            for (int q = 0; q < CT; ++q) mine[tok[k] * C + 16 * q + c] += tot[q][k] * power[q] * wt[k];
-      } else {
-        for (int jj = 0; jj < 4; ++jj) {
-          if (j == jj) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (tok[k] >= 0)
-#pragma unroll
-                for (int q = 0; q < CT; ++q) mine[tok[k] * C + 16 * q + c] += tot[q][k] * power[q] * wt[k];
+        for (int k = 0; k < 4; ++k) {
+          const int at = t0 + 16 * t + 4 * j + k;
+          if (at < n) {
+            const int pair = list[at];
+            float a = tot[t][q][k] * pg, b = tot[t][2 + q][k] * pu;
+            if constexpr (XT == kI8 || XT == kE4m3) a *= p.xscale[pair / p.k], b *= p.xscale[pair / p.k];
+            store_h(p, plane, pair, (tile0 + q) * 16 + c, activate(a, p.act) * b);
           }
-          __builtin_amdgcn_wave_barrier();
         }
       }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.M * C; i += 64 * WV) {
-    float s = 0.0f;
+}
+
+template <int T, int TM>
+__global__ __launch_bounds__(256) void moe_down_tile_kernel(const MoeArgs p) {
+  constexpr int SRC = T == 2 ? kPlanes2 : kPlanes3;
+  using Stage = TileStage<SRC, TM>;
+  __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
+  __shared__ uint16_t list[kMoePairs];
+  __shared__ int counts[4];
+  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = (int)blockIdx.y, P = p.M * p.k;
+  const int n = expert_pairs<4>(p.ids, P, e, list, counts);
+  const int tiles = p.H / 16, tile0 = (int)blockIdx.x * 16 + 4 * wave;  // H is a multiple of 128: a wave has all four or none
+  const int64_t first = (int64_t)e * tiles + (tile0 < tiles ? tile0 : 0);
+  const int64_t tile[4] = {first, first + 1, first + 2, first + 3};
+  for (int t0 = (int)blockIdx.z * 16 * TM; t0 < n; t0 += 16 * TM * (int)gridDim.z) {
+    Stage st;
+    st.point([&](int r) AWQ_INLINE {
+      return reinterpret_cast<const char*>(p.h + (int64_t)list[t0 + r < n ? t0 + r : n - 1] * p.I);
+    });
+    f32x4 tot[TM][4];
+    TilePass<SRC, TM, T == 3>::run(p.down, tile, p.I / kGroup, st, (int64_t)P * p.I * 2, lds, (n - t0 + 15) / 16, lane, tot);
+    if (tile0 >= tiles) continue;
 #pragma unroll
-    for (int w = 0; w < WV; ++w) s += sums[w * p.M * C + i];
-    const int m = i / C, n = (int)blockIdx.x * C + i % C;
-    if (shares > 1) p.o[((int64_t)share * p.M + m) * p.H + n] = s;
-    else if (p.ybf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_rne(s, s);
-    else static_cast<float*>(p.y)[m * p.ldy + n] = s;
+    for (int q = 0; q < 4; ++q) {
+      const float power = p.down.powers[tile[q] * 16 + c];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = t0 + 16 * t + 4 * j + k;
+          if (at < n) {
+            const int pair = list[at];
+            p.o[(int64_t)pair * p.H + (tile0 + q) * 16 + c] = tot[t][q][k] * power * p.weights[pair];
+          }
+        }
+      }
+    }
   }
 }
 
 // ---- sums in order -----------------------------------------------------------------------------------------
-// Y from a token's pairs (shares = 0), or from the shares of the down kernel.
-__global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p, int shares) {
+// Y from a token's pairs.
+__global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
   const int m = (int)blockIdx.y, n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
   if (n >= p.H) return;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (shares > 0) {
-    for (int j = 0; j < shares; ++j) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)j * p.M + m) * p.H + n);
-  } else {
-    for (int j = 0; j < p.k; ++j) {
-      const int e = p.ids[m * p.k + j];
-      if (e >= 0 && e < p.E) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)m * p.k + j) * p.H + n);
-    }
+  for (int j = 0; j < p.k; ++j) {
+    const int e = p.ids[m * p.k + j];
+    if (e >= 0 && e < p.E) s += *reinterpret_cast<const f32x4*>(p.o + ((int64_t)m * p.k + j) * p.H + n);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -702,16 +755,11 @@ void up_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
   moe_up_kernel<XT, TT, NG, WV, INNER><<<dim3((unsigned)((a.I / 16 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
 }
 template <int XT, bool INNER>
-void launch_up(const MoeArgs& a, unsigned slots, bool wide, hipStream_t st) {
+void launch_up(const MoeArgs& a, unsigned slots, hipStream_t st) {
   const int G = a.H / kGroup;
-  if (wide) {
-    if (G <= 8) up_with<XT, 2, 1, 8, INNER>(a, slots, st);
-    else up_with<XT, 2, 1, XT == kF32 ? 8 : 16, INNER>(a, slots, st);
-  } else {
-    if (G <= 8) up_with<XT, 1, 1, 8, INNER>(a, slots, st);
-    else if (G <= 16) up_with<XT, 1, 2, 8, INNER>(a, slots, st);
-    else up_with<XT, 1, XT == kF32 ? 1 : 2, 16, INNER>(a, slots, st);
-  }
+  if (G <= 8) up_with<XT, 1, 1, 8, INNER>(a, slots, st);
+  else if (G <= 16) up_with<XT, 1, 2, 8, INNER>(a, slots, st);
+  else up_with<XT, 1, XT == kF32 ? 1 : 2, 16, INNER>(a, slots, st);
 }
 
 template <int T, int TT, int NG, int WV>
@@ -720,43 +768,51 @@ void down_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
   moe_down_kernel<T, TT, NG, WV><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
 }
 template <int T>
-void launch_down(const MoeArgs& a, unsigned slots, bool wide, hipStream_t st) {
-  const int G = a.I / kGroup;
-  if (wide) down_with<T, 2, 1, 8>(a, slots, st);
-  else if (G <= 8) down_with<T, 1, 1, 8>(a, slots, st);
+void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
+  if (a.I / kGroup <= 8) down_with<T, 1, 1, 8>(a, slots, st);
   else down_with<T, 1, 1, 16>(a, slots, st);
 }
 
+// Blocks for a slot's token tiles: what an expert has on average, and one more for those that have more.
+unsigned tile_depth(const MoeArgs& a, int tokens) { return (unsigned)(a.M * a.k / (a.E * tokens) + 2); }
+
+template <int XT, int TM, bool INNER>
+void up_tiles(const MoeArgs& a, hipStream_t st) {
+  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a, 16 * TM)), 256, 0, st>>>(a);
+}
+template <int T, int TM>
+void down_tiles(const MoeArgs& a, hipStream_t st) {
+  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a, 16 * TM)), 256, 0, st>>>(a);
+}
+
+template <int XT, bool INNER>
+void launch_products(const MoeArgs& a, hipStream_t st) {
+  const int P = a.M * a.k;
+  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
+  if (P > 40 * a.E) up_tiles<XT, 4, INNER>(a, st);
+  else if (P > 12 * a.E) up_tiles<XT, 2, INNER>(a, st);
+  else launch_up<XT, INNER>(a, slots, st);
+}
 template <int T>
-void launch_down_few(const MoeArgs& a, int shares, int parts, hipStream_t st) {
-  constexpr int WV = T == 2 ? 16 : 8;
-  const size_t lds = (size_t)WV * a.M * 16 * 4;
-  moe_down_few_kernel<T, 1, WV><<<dim3((unsigned)(a.H / 16), (unsigned)shares), 64 * WV, lds, st>>>(a, parts);
+void launch_sums(const MoeArgs& a, hipStream_t st) {
+  const int P = a.M * a.k;
+  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
+  if (P > 40 * a.E) down_tiles<T, T == 2 ? 4 : 2>(a, st);
+  else if (P > 12 * a.E) down_tiles<T, 2>(a, st);
+  else launch_down<T>(a, slots, st);
+  moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a);
 }
 
 template <int XT>
 hipError_t launch_experts(MoeArgs a, hipStream_t st) {
-  const int P = a.M * a.k;
-  a.by_pair = P < a.E;
-  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
-  const bool wide = P > 12 * a.E;  // more than twelve tokens an expert: up to 32 at a time
-  const bool few = P <= kMoeFewPairs;
-  if (a.terms == 2) launch_up<XT, false>(a, slots, wide, st);
-  else launch_up<XT, XT != kI8>(a, slots, wide, st);
-  int shares = 0;
-  if (few) {
-    const int G = a.I / kGroup;
-    shares = 1;
-    int parts = 1;
-    while ((int)slots * parts < 64 && G / (2 * parts) >= 4) parts *= 2;
-    if (a.terms == 2) launch_down_few<2>(a, shares, parts, st);
-    else launch_down_few<3>(a, shares, parts, st);
-    if (shares == 1) return hipGetLastError();
+  a.by_pair = a.M * a.k < a.E;
+  if (a.terms == 2) {
+    launch_products<XT, false>(a, st);
+    launch_sums<2>(a, st);
   } else {
-    if (a.terms == 2) launch_down<2>(a, slots, wide, st);
-    else launch_down<3>(a, slots, wide, st);
+    launch_products<XT, XT != kI8>(a, st);
+    launch_sums<3>(a, st);
   }
-  moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a, shares);
   return hipGetLastError();
 }
 

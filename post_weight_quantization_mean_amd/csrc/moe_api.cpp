@@ -46,8 +46,7 @@ bool moe_layout(int64_t M, int64_t E, int64_t k, int64_t H, int64_t I, MoeLayout
   const int64_t pairs = L->pass * k;
   L->h = 0;
   L->o = align_up((size_t)(pairs * I * 6));
-  const int64_t few = awq::kMoeShares * (pairs < awq::kMoeFewPairs ? pairs : awq::kMoeFewPairs);
-  L->ids = L->o + align_up((size_t)((pairs > few ? pairs : few) * H * 4));
+  L->ids = L->o + align_up((size_t)(pairs * H * 4));
   L->weights = L->ids + align_up((size_t)(M * k * 4));
   L->total = L->weights + align_up((size_t)(M * k * 4));
   return true;

@@ -7,8 +7,6 @@ namespace awq {
 
 constexpr int kMaxExperts = 1024, kMaxChosen = 32;
 constexpr int kMoePairs = 2048;  // (token, expert) pairs of one pass at most: their list is kept on chip
-constexpr int kMoeFewPairs = 64;  // up to which the down kernel adds the experts up on chip
-constexpr int kMoeShares = 4;    // of the work on a run of channels, at most, each with sums of its own
 constexpr int kSoftmax = 0, kSigmoid = 1;
 
 struct RouteArgs {
@@ -34,7 +32,7 @@ struct MoeArgs {
   ExpertWeights up, down;
   void* y;               // [M, H], ldy
   uint16_t* h;           // [terms][pairs][I]: act(gate) * up as bf16 terms
-  float* o;              // [pairs][H]: the weighted experts' results; few tokens: [shares][M][H]
+  float* o;              // [pairs][H]: the weighted experts' results
   int64_t ldx, ldy;
   int M, k, E, H, I, act, terms;
   bool ybf16, by_pair;   // by_pair: slots are pairs, not experts

@@ -166,10 +166,11 @@ def check_moe(awq, x, x64, ids, w, gu, down, hg, hd, act, out, into=None, **kw):
     return y
 
 
-# tokens, experts, choices, H, I: fewer pairs than experts (a slot per pair) and more (per expert), more than 8 and 16 and 32
+# tokens, experts, choices, H, I: fewer pairs than experts (a slot per pair) and more (per expert), up to 12, up to 40 and more
 # tokens an expert, odd group counts, one and several groups a wave, one expert
 MOE_SHAPES = [(1, 8, 2, 128, 128), (1, 4, 4, 256, 384), (3, 32, 8, 128, 256), (2, 3, 1, 1152, 128), (17, 4, 2, 256, 128),
-              (40, 3, 3, 384, 128), (5, 1, 1, 128, 1280), (70, 2, 1, 128, 256), (9, 16, 4, 2176, 128)]
+              (40, 3, 3, 384, 128), (5, 1, 1, 128, 1280), (70, 2, 1, 128, 256), (9, 16, 4, 2176, 128), (90, 5, 2, 384, 384),
+              (101, 2, 2, 640, 256), (83, 1, 1, 128, 128), (12, 2, 2, 1152, 2176)]
 
 
 @pytest.mark.parametrize("M,E,k,H,I", MOE_SHAPES)
