@@ -538,45 +538,45 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)
 }
 
 // ---- many tokens an expert: tiles ---------------------------------------------------------------------------
-// A block of four waves: a slot's tokens 16 TM at a time with 256 channels of the weight (up: 128 gate rows and the up rows
-// beside them), all groups one after the other.  A wave has all the tokens and four channel tiles, whose codes come straight
-// into registers a group ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing is
-// summed across waves, and a code is unpacked once for 16 TM tokens.
+// A block of eight waves: an expert's tokens 16 TM at a time with 256 channels of the weight (up: 128 gate rows and the up
+// rows beside them), all groups one after the other.  A wave has all the tokens and two channel tiles, whose codes come
+// straight into registers a group ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing
+// is summed across waves, and a code is unpacked once for 16 TM tokens.
 // Rows in LDS hold their 16-byte pieces at piece ^ swizzle(row): the reads of sixteen rows' same piece use every bank once.
 template <int SRC, int TM>
 struct TileStage {
   using S = Source<SRC>;
   static constexpr int kPlanes = S::kPlanes, kRow = kGroup * S::kSize, kPieces = kRow / 16;  // of a row of a plane
-  static constexpr int kPer = 16 * TM * kPieces / 256;  // pieces of a plane per thread
+  static constexpr int kPer = (16 * TM * kPieces + 511) / 512;  // pieces of a plane per thread
   static constexpr int kPlane = 16 * TM * kRow, kBytes = kPlanes * kPlane;
-  static_assert(kPer >= 1, "every thread has a piece");
   static __device__ __forceinline__ int place(int row, int piece) {
     return row * kRow + 16 * (piece ^ (kPieces == 8 ? row >> 1 & 7 : row & 15));
   }
-  const char* from[kPer];
+  const char* from[kPer];  // null: nothing for this thread
   u32x4 v[kPlanes][kPer];
-  // row(r) is where row r of the tile starts in memory
+  // row(r) is where row r < rows of the tile starts in memory
   template <typename Row>
-  __device__ __forceinline__ void point(Row row) {
+  __device__ __forceinline__ void point(int rows, Row row) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int q = (int)threadIdx.x + 256 * i;
-      from[i] = row(q / kPieces) + 16 * (q % kPieces);
+      const int q = (int)threadIdx.x + 512 * i;
+      from[i] = q / kPieces < rows ? row(q / kPieces) + 16 * (q % kPieces) : nullptr;
     }
   }
   __device__ __forceinline__ void load(int g, int64_t plane) {
 #pragma unroll
     for (int k = 0; k < kPlanes; ++k)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[k][i] = *reinterpret_cast<const u32x4*>(from[i] + (int64_t)g * kRow + k * plane);
+      for (int i = 0; i < kPer; ++i)
+        if (from[i] != nullptr) v[k][i] = *reinterpret_cast<const u32x4*>(from[i] + (int64_t)g * kRow + k * plane);
   }
   __device__ __forceinline__ void store(char* stage) const {
 #pragma unroll
     for (int k = 0; k < kPlanes; ++k)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int q = (int)threadIdx.x + 256 * i;
-        *reinterpret_cast<u32x4*>(stage + k * kPlane + place(q / kPieces, q % kPieces)) = v[k][i];
+        const int q = (int)threadIdx.x + 512 * i;
+        if (from[i] != nullptr) *reinterpret_cast<u32x4*>(stage + k * kPlane + place(q / kPieces, q % kPieces)) = v[k][i];
       }
   }
   // the operand of the sixteen tokens from row 16 t on
@@ -591,19 +591,19 @@ template <int SRC, int TM, bool INNER>
 struct TilePass {
   using Stage = TileStage<SRC, TM>;
   using Op = typename Source<SRC>::Operand;
-  // tot[t][q] of tiles tile[q] over all groups; used: the token tiles that hold any token.  All four waves.
-  static __device__ __forceinline__ void run(const ExpertWeights& w, const int64_t (&tile)[4], int G, Stage& st, int64_t plane,
-                                             char* lds, int used, int lane, f32x4 (&tot)[TM][4]) {
+  // tot[t][q] of tiles tile[q] over all groups; used: the token tiles that hold any token.  All eight waves.
+  static __device__ __forceinline__ void run(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st, int64_t plane,
+                                             char* lds, int used, int lane, f32x4 (&tot)[TM][2]) {
     const int c = lane & 15, j = lane >> 4;
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 codes[4];
-    uint32_t dz[4];
+      for (int q = 0; q < 2; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 codes[2];
+    uint32_t dz[2];
     auto fetch = [&](int g) AWQ_INLINE {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         codes[q] = *(reinterpret_cast<const u32x4*>(w.codes + (tile[q] * G + g) * 256) + (unsigned)lane);
         dz[q] = (w.steps + (tile[q] * G + g) * 16)[(unsigned)c];
       }
@@ -614,13 +614,13 @@ struct TilePass {
     st.store(lds);
     if (G > 1) st.load(1, plane);
     __syncthreads();
+#pragma unroll 1
     for (int g = 0; g < G; ++g) {
       const char* now = lds + (g & 1) * Stage::kBytes;
-      typename Op::Weight op[4] = {typename Op::Weight(codes[0]), typename Op::Weight(codes[1]), typename Op::Weight(codes[2]),
-                                   typename Op::Weight(codes[3])};
-      float d[4], z[4];
+      const typename Op::Weight op[2] = {typename Op::Weight(codes[0]), typename Op::Weight(codes[1])};
+      float d[2], z[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) d[q] = half_lo(dz[q]), z[q] = half_lo(dz[q] >> 16);
+      for (int q = 0; q < 2; ++q) d[q] = half_lo(dz[q]), z[q] = half_lo(dz[q] >> 16);
       if (g + 1 < G) {
         fetch(g + 1);
         st.store(lds + (g + 1 & 1) * Stage::kBytes);
@@ -629,12 +629,13 @@ struct TilePass {
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
         if (t > 0 && t >= used) break;
+        __builtin_amdgcn_sched_barrier(0);  // one token tile's operands in registers at a time
         Op x;
         Stage::read(x, now, t, c, j);
         f32x4 sx = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (!INNER) sx = x.ones();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           const f32x4 v = x.template sum<INNER>(op[q], z[q], sx);
 #pragma unroll
           for (int k = 0; k < 4; ++k) tot[t][q][k] = fmaf(d[q], v[k], tot[t][q][k]);
@@ -646,39 +647,36 @@ struct TilePass {
 };
 
 template <int XT, int TM, bool INNER>
-__global__ __launch_bounds__(256) void moe_up_tile_kernel(const MoeArgs p) {
+__global__ __launch_bounds__(512) void moe_up_tile_kernel(const MoeArgs p) {
   using Stage = TileStage<XT, TM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[4];
+  __shared__ int counts[8];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = (int)blockIdx.y, P = p.M * p.k;
-  const int n = expert_pairs<4>(p.ids, P, e, list, counts);
-  const int tile0 = (int)blockIdx.x * 8 + 2 * wave;  // of I: this wave's two
-  const int64_t first = (int64_t)e * (p.I / 8) + tile0, up = p.I / 16;
-  const int64_t tile[4] = {first, first + 1, first + up, first + 1 + up}, plane = (int64_t)P * p.I;
+  const int n = expert_pairs<8>(p.ids, P, e, list, counts);
+  const int tile0 = (int)blockIdx.x * 8 + wave;  // of I
+  const int64_t first = (int64_t)e * (p.I / 8) + tile0, plane = (int64_t)P * p.I;
+  const int64_t tile[2] = {first, first + p.I / 16};
   for (int t0 = (int)blockIdx.z * 16 * TM; t0 < n; t0 += 16 * TM * (int)gridDim.z) {
     Stage st;
-    st.point([&](int r) AWQ_INLINE {
+    st.point(n - t0 < 16 * TM ? (n - t0 + 15) / 16 * 16 : 16 * TM, [&](int r) AWQ_INLINE {
       return static_cast<const char*>(p.x) + (int64_t)(list[t0 + r < n ? t0 + r : n - 1] / p.k) * p.ldx * Source<XT>::kSize;
     });
-    f32x4 tot[TM][4];
+    f32x4 tot[TM][2];
     TilePass<XT, TM, INNER>::run(p.up, tile, p.H / kGroup, st, 0, lds, (n - t0 + 15) / 16, lane, tot);
+    const float pg = p.up.powers[tile[0] * 16 + c], pu = p.up.powers[tile[1] * 16 + c];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float pg = p.up.powers[tile[q] * 16 + c], pu = p.up.powers[tile[2 + q] * 16 + c];
+    for (int t = 0; t < TM; ++t) {
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = t0 + 16 * t + 4 * j + k;
-          if (at < n) {
-            const int pair = list[at];
-            float a = tot[t][q][k] * pg, b = tot[t][2 + q][k] * pu;
-            if constexpr (XT == kI8 || XT == kE4m3) a *= p.xscale[pair / p.k], b *= p.xscale[pair / p.k];
-            store_h(p, plane, pair, (tile0 + q) * 16 + c, activate(a, p.act) * b);
-          }
+      for (int k = 0; k < 4; ++k) {
+        const int at = t0 + 16 * t + 4 * j + k;
+        if (at < n) {
+          const int pair = list[at];
+          float a = tot[t][0][k] * pg, b = tot[t][1][k] * pu;
+          if constexpr (XT == kI8 || XT == kE4m3) a *= p.xscale[pair / p.k], b *= p.xscale[pair / p.k];
+          store_h(p, plane, pair, tile0 * 16 + c, activate(a, p.act) * b);
         }
       }
     }
@@ -686,29 +684,29 @@ __global__ __launch_bounds__(256) void moe_up_tile_kernel(const MoeArgs p) {
 }
 
 template <int T, int TM>
-__global__ __launch_bounds__(256) void moe_down_tile_kernel(const MoeArgs p) {
+__global__ __launch_bounds__(512) void moe_down_tile_kernel(const MoeArgs p) {
   constexpr int SRC = T == 2 ? kPlanes2 : kPlanes3;
   using Stage = TileStage<SRC, TM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[4];
+  __shared__ int counts[8];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = (int)blockIdx.y, P = p.M * p.k;
-  const int n = expert_pairs<4>(p.ids, P, e, list, counts);
-  const int tiles = p.H / 16, tile0 = (int)blockIdx.x * 16 + 4 * wave;  // H is a multiple of 128: a wave has all four or none
+  const int n = expert_pairs<8>(p.ids, P, e, list, counts);
+  const int tiles = p.H / 16, tile0 = (int)blockIdx.x * 16 + 2 * wave;  // a wave has both or, past the end, none
   const int64_t first = (int64_t)e * tiles + (tile0 < tiles ? tile0 : 0);
-  const int64_t tile[4] = {first, first + 1, first + 2, first + 3};
+  const int64_t tile[2] = {first, first + 1};
   for (int t0 = (int)blockIdx.z * 16 * TM; t0 < n; t0 += 16 * TM * (int)gridDim.z) {
     Stage st;
-    st.point([&](int r) AWQ_INLINE {
+    st.point(n - t0 < 16 * TM ? (n - t0 + 15) / 16 * 16 : 16 * TM, [&](int r) AWQ_INLINE {
       return reinterpret_cast<const char*>(p.h + (int64_t)list[t0 + r < n ? t0 + r : n - 1] * p.I);
     });
-    f32x4 tot[TM][4];
+    f32x4 tot[TM][2];
     TilePass<SRC, TM, T == 3>::run(p.down, tile, p.I / kGroup, st, (int64_t)P * p.I * 2, lds, (n - t0 + 15) / 16, lane, tot);
     if (tile0 >= tiles) continue;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
       const float power = p.down.powers[tile[q] * 16 + c];
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
@@ -778,27 +776,25 @@ unsigned tile_depth(const MoeArgs& a, int tokens) { return (unsigned)(a.M * a.k 
 
 template <int XT, int TM, bool INNER>
 void up_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a, 16 * TM)), 256, 0, st>>>(a);
+  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a, 16 * TM)), 512, 0, st>>>(a);
 }
 template <int T, int TM>
 void down_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a, 16 * TM)), 256, 0, st>>>(a);
+  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a, 16 * TM)), 512, 0, st>>>(a);
 }
 
 template <int XT, bool INNER>
 void launch_products(const MoeArgs& a, hipStream_t st) {
   const int P = a.M * a.k;
   const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
-  if (P > 40 * a.E) up_tiles<XT, 4, INNER>(a, st);
-  else if (P > 12 * a.E) up_tiles<XT, 2, INNER>(a, st);
+  if (P > 12 * a.E) up_tiles<XT, XT == kF32 ? 2 : 4, INNER>(a, st);
   else launch_up<XT, INNER>(a, slots, st);
 }
 template <int T>
 void launch_sums(const MoeArgs& a, hipStream_t st) {
   const int P = a.M * a.k;
   const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
-  if (P > 40 * a.E) down_tiles<T, T == 2 ? 4 : 2>(a, st);
-  else if (P > 12 * a.E) down_tiles<T, 2>(a, st);
+  if (P > 12 * a.E) down_tiles<T, T == 2 ? 4 : 2>(a, st);
   else launch_down<T>(a, slots, st);
   moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a);
 }
