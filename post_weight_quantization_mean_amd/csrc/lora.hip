@@ -9,6 +9,8 @@
 namespace awq {
 namespace {
 
+#define AWQ_INLINE __attribute__((always_inline))
+
 constexpr int kNone = -1;    // the row keeps its base
 constexpr int kAbsent = -2;  // no row
 
@@ -39,10 +41,12 @@ __device__ __forceinline__ int adapter_rank(const LoraArgs& p, int a) {
 }
 
 // t[split][m][r] = scale (xscale sum_k x[m, k] A[r, k]) over the split's share of K.  A block: sixteen tokens, RT tiles of
-// sixteen ranks, its eight waves taking steps of 32 channels in turn.
+// sixteen ranks, its eight waves taking steps of 64 channels in turn, U at a time.  The tokens of the first U steps are
+// requested before the adapter is known and stay in registers for all of the tile's adapters: with as many splits as
+// lora_splits makes, that is often all of K.
 template <int XT, int RT>
 __global__ __launch_bounds__(512) void lora_down_kernel(const LoraArgs p, int parts, int rank_blocks) {
-  constexpr int WV = 8, U = XT == kF32 ? 2 : 4;
+  constexpr int WV = 8, U = XT == kF32 ? (RT == 1 ? 2 : 1) : 4 / RT;
   __shared__ float sums[WV][RT * 256];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -51,9 +55,22 @@ __global__ __launch_bounds__(512) void lora_down_kernel(const LoraArgs p, int pa
   const int split = (int)blockIdx.z;
   const int id = row_adapter(p, m0, c);
   const int xs = XT == kF32 ? 4 : XT == kBf16 ? 2 : 1;
-  const char* xrow = static_cast<const char*>(p.x) + ((m0 + c < p.M ? m0 + c : p.M - 1) * p.ldx + 8 * j) * xs;
-  const int64_t steps = (p.K + 31) / 32;
-  each_adapter(id, part, parts, [&](int a, uint32_t rows) {
+  const char* xrow = static_cast<const char*>(p.x) + ((m0 + c < p.M ? m0 + c : p.M - 1) * p.ldx + 16 * j) * xs;
+  const int64_t steps = (p.K + 63) / 64, s0 = (int64_t)split * WV + wave, stride = (int64_t)WV * p.splits;
+  // a step's 64 channels: lane / 16 has sixteen of them, in two operands
+  X8<XT> x[U][2];
+  auto load_x = [&](int64_t s) AWQ_INLINE {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = 64 * (s + u * stride) + 8 * h;
+        if (k + 16 * j < p.K) x[u][h].load(xrow + k * xs);
+        else x[u][h].clear();
+      }
+  };
+  load_x(s0);
+  each_adapter(id, part, parts, [&](int a, uint32_t rows) AWQ_INLINE {
     if (a == kNone) return;
     const int rank = adapter_rank(p, a);
     if (r0 >= rank) return;
@@ -61,38 +78,39 @@ __global__ __launch_bounds__(512) void lora_down_kernel(const LoraArgs p, int pa
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
       const int r = r0 + 16 * q + c < rank ? r0 + 16 * q + c : rank - 1;  // past the rank: its last row again, not kept
-      arow[q] = p.a + ((int64_t)a * p.R + r) * p.K + 8 * j;
+      arow[q] = p.a + ((int64_t)a * p.R + r) * p.K + 16 * j;
     }
     f32x4 acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t s = (int64_t)split * WV + wave; s < steps; s += (int64_t)U * WV * p.splits) {
-      X8<XT> x[U];
-      X8<kBf16> w[U][RT];
+    for (int64_t s = s0; s < steps; s += U * stride) {
+      if (s0 + U * stride < steps) load_x(s);
+      X8<kBf16> w[U][2][RT];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t k = 32 * (s + (int64_t)u * WV * p.splits);
-        if (k + 8 * j < p.K) {
-          x[u].load(xrow + k * xs);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int q = 0; q < RT; ++q) w[u][q].load(reinterpret_cast<const char*>(arow[q] + k));
-        } else {
-          x[u].clear();
+        for (int h = 0; h < 2; ++h) {
+          const int64_t k = 64 * (s + u * stride) + 8 * h;
 #pragma unroll
-          for (int q = 0; q < RT; ++q) w[u][q].clear();
+          for (int q = 0; q < RT; ++q) {
+            if (k + 16 * j < p.K) w[u][h][q].load(reinterpret_cast<const char*>(arow[q] + k));
+            else w[u][h][q].clear();
+          }
         }
-      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        bf16x8 xt[X8<XT>::kTerms];
-        x[u].terms(xt);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) {
-          bf16x8 wt[1];
-          w[u][q].terms(wt);
+        for (int h = 0; h < 2; ++h) {
+          bf16x8 xt[X8<XT>::kTerms];
+          x[u][h].terms(xt);
 #pragma unroll
-          for (int t = X8<XT>::kTerms - 1; t >= 0; --t)
-            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt[t], wt[0], acc[q], 0, 0, 0);
+          for (int q = 0; q < RT; ++q) {
+            bf16x8 wt[1];
+            w[u][h][q].terms(wt);
+#pragma unroll
+            for (int t = X8<XT>::kTerms - 1; t >= 0; --t)
+              acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt[t], wt[0], acc[q], 0, 0, 0);
+          }
         }
       }
     }
@@ -115,120 +133,165 @@ __global__ __launch_bounds__(512) void lora_down_kernel(const LoraArgs p, int pa
   });
 }
 
-// Y = base + B t for sixteen tokens and 64 channels a wave.  The channels are the left operand's rows: row r of tile q is
-// channel 16 (r / 4) + 4 q + r % 4 of the 64, so that a lane holds sixteen consecutive channels of its token.
-template <int T, bool YB, bool VEC>
-__global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs p, int parts) {
-  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t chunks = (p.N + 255) / 256;
-  const int64_t m0 = (int64_t)blockIdx.x / chunks * 16, n0 = ((int64_t)blockIdx.x % chunks * 4 + wave) * 64;
-  if (n0 >= p.N) return;
-  const int id = row_adapter(p, m0, c);
-  const int64_t m = m0 + c < p.M ? m0 + c : p.M - 1;
-  const int64_t n = n0 + 16 * j;  // this lane's first channel
-  constexpr int YS = YB ? 2 : 4;
-  const char* brow = static_cast<const char*>(p.base) + (m * p.ldb + n) * YS;
-  char* yrow = static_cast<char*>(p.y) + (m * p.ldy + n) * YS;
-  const bool copies = p.base != p.y;
-  each_adapter(id, (int)blockIdx.y, parts, [&](int a, uint32_t rows) {
-    if (a == kNone && !copies) return;
-    const bool mine = rows >> c & 1u;
-    const int count = n >= p.N ? 0 : p.N - n < 16 ? (int)(p.N - n) : 16;
-    uint32_t raw[4 * YS];  // the sixteen values of base
-    if (VEC && count == 16) {
-      if (mine) {
+// t of this lane's token (if it is `mine`) and eight ranks from r8 on, of which `have` count, as operand terms.  The splits'
+// parts are requested four at a time and added in order.
+template <int T>
+__device__ __forceinline__ void load_t(const LoraArgs& p, int64_t m, int r8, int have, bool mine, bf16x8 (&t)[T]) {
+  float v[8];
 #pragma unroll
-        for (int i = 0; i < YS; ++i) {
-          const u32x4 v = reinterpret_cast<const u32x4*>(brow)[i];
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (mine && have > 0) {
+    const float* from = p.t + m * p.R + r8;
+    for (int s0 = 0; s0 < p.splits; s0 += 4) {
+      f32x4 x[4][2];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) raw[4 * i + d] = v[d];
-        }
+      for (int s = 0; s < 4; ++s) {
+        const f32x4* tp = reinterpret_cast<const f32x4*>(from + (int64_t)(s0 + s < p.splits ? s0 + s : s0) * p.M * p.R);
+        x[s][0] = tp[0], x[s][1] = tp[1];
       }
-    } else if (mine) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (s0 + s < p.splits)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += x[s][i / 4][i % 4];
+    }
+    if (have < 8)  // beyond the rank: zeros, whatever is stored there
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= have) v[i] = 0.0f;
+  }
+  split_terms<T>(v, t);
+}
+
+// Sixteen consecutive values of a row of base or Y, `have` of which are there.  (In units of 16 bytes, 64 apart, so that a
+// token's four lanes read 64 bytes in a row, the prompt's kernel took 68 us against 64.)
+template <bool YB, bool VEC>
+struct Sixteen {
+  static constexpr int kSize = YB ? 2 : 4, kWords = 4 * kSize;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const char* p, int have) {
+    if (VEC && have >= 16) {
+#pragma unroll
+      for (int i = 0; i < kSize; ++i) {
+        const u32x4 v = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[4 * i + d] = v[d];
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if constexpr (YB) {
-          const uint32_t v = i < count ? reinterpret_cast<const uint16_t*>(brow)[i] : 0u;
-          raw[i / 2] = i % 2 ? raw[i / 2] | v << 16 : v;
+          const uint32_t v = i < have ? reinterpret_cast<const uint16_t*>(p)[i] : 0u;
+          w[i / 2] = i % 2 ? w[i / 2] | v << 16 : v;
         } else {
-          raw[i] = i < count ? reinterpret_cast<const uint32_t*>(brow)[i] : 0u;
+          w[i] = i < have ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
         }
       }
     }
-    f32x4 acc[4];
+  }
+  __device__ __forceinline__ void add(const f32x4 (&v)[4]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    const int rank = a == kNone ? 0 : adapter_rank(p, a);
-    for (int r = 0; r < rank; r += 32) {
-      const int r8 = r + 8 * j, have = rank - r8;  // this lane's eight ranks, and how many of them there are
-      float tv[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) tv[i] = 0.0f;
-      X8<kBf16> w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) w[q].clear();
-      if (have > 0) {
-        if (mine) {
-          for (int s = 0; s < p.splits; ++s) {
-            const f32x4* tp = reinterpret_cast<const f32x4*>(p.t + ((int64_t)s * p.M + m) * p.R + r8);
-            const f32x4 lo = tp[0], hi = tp[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tv[i] += lo[i], tv[4 + i] += hi[i];
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t ch = n0 + 16 * (c / 4) + 4 * q + c % 4;
-          w[q].load(reinterpret_cast<const char*>(p.b + ((int64_t)a * p.N + (ch < p.N ? ch : p.N - 1)) * p.R + r8));
-        }
-        if (have < 8) {  // beyond the rank: zeros, whatever is stored there
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i >= have) tv[i] = 0.0f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[q].w[i] &= 2 * i + 1 < have ? 0xffffffffu : 2 * i < have ? 0x0000ffffu : 0u;
-        }
-      }
-      bf16x8 tt[T];
-      split_terms<T>(tv, tt);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf16x8 wt[1];
-        w[q].terms(wt);
-#pragma unroll
-        for (int t = T - 1; t >= 0; --t)
-          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wt[0], tt[t], acc[q], 0, 0, 0);
-      }
+    for (int i = 0; i < 16; i += 2) {
+      const float a = v[i / 4][i % 4], b = v[i / 4][i % 4 + 1];
+      if constexpr (YB) w[i / 2] = pack_rne(flt(w[i / 2] << 16) + a, flt(w[i / 2] & 0xffff0000u) + b);
+      else w[i] = bits(flt(w[i]) + a), w[i + 1] = bits(flt(w[i + 1]) + b);
     }
-    if (!mine) return;
-    float v[16];
+  }
+  __device__ __forceinline__ void store(char* p, int have) const {
+    if (VEC && have >= 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float b = YB ? flt(i % 2 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16) : flt(raw[i]);
-      v[i] = a == kNone ? b : b + acc[i / 4][i % 4];
-    }
-    if constexpr (YB) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = pack_rne(v[2 * i], v[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) raw[i] = bits(v[i]);
-    }
-    if (VEC && count == 16) {
-#pragma unroll
-      for (int i = 0; i < YS; ++i)
-        reinterpret_cast<u32x4*>(yrow)[i] = (u32x4){raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]};
+      for (int i = 0; i < kSize; ++i)
+        reinterpret_cast<u32x4*>(p)[i] = (u32x4){w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (i < count) {
-          if constexpr (YB) reinterpret_cast<uint16_t*>(yrow)[i] = (uint16_t)(i % 2 ? raw[i / 2] >> 16 : raw[i / 2]);
-          else reinterpret_cast<uint32_t*>(yrow)[i] = raw[i];
+        if (i < have) {
+          if constexpr (YB) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2]);
+          else reinterpret_cast<uint32_t*>(p)[i] = w[i];
         }
+      }
+    }
+  }
+};
+
+// Y = base + B t for sixteen tokens and CHUNKS times 64 channels a wave.  The channels are the left operand's rows, the
+// tokens the right operand's columns: row r of tile q is channel 16 (r / 4) + 4 q + r % 4 of the 64, so that a lane holds
+// sixteen consecutive channels of its token.  t of the first 32 HELD ranks stays in registers over the chunks.
+// All of base is requested before anything else.
+template <int T, bool YB, bool VEC, int HELD, int CHUNKS>
+__global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs p, int parts) {
+  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t across = (p.N + 256 * CHUNKS - 1) / (256 * CHUNKS);
+  const int64_t m0 = (int64_t)blockIdx.x / across * 16;
+  const int64_t n0 = ((int64_t)blockIdx.x % across * 4 + wave) * 64 * CHUNKS;
+  if (n0 >= p.N) return;
+  const int64_t m = m0 + c < p.M ? m0 + c : p.M - 1;
+  using Values = Sixteen<YB, VEC>;
+  const char* brow = static_cast<const char*>(p.base) + (m * p.ldb + n0 + 16 * j) * Values::kSize;
+  char* yrow = static_cast<char*>(p.y) + (m * p.ldy + n0 + 16 * j) * Values::kSize;
+  const int64_t there = p.N - n0 - 16 * j;  // channels from this lane's first on
+  const int have_n = there < 64 * CHUNKS ? (int)there : 64 * CHUNKS;
+  Values v[CHUNKS];
+  if (parts == 1) {
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) v[k].load(brow + 64 * k * Values::kSize, have_n - 64 * k);
+  }
+  const int id = row_adapter(p, m0, c);
+  const bool copies = p.base != p.y;
+  each_adapter(id, (int)blockIdx.y, parts, [&](int a, uint32_t rows) AWQ_INLINE {
+    if (a == kNone && !copies) return;
+    const bool mine = rows >> c & 1u;
+    if (parts > 1 && mine) {
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k) v[k].load(brow + 64 * k * Values::kSize, have_n - 64 * k);
+    }
+    const int rank = a == kNone ? 0 : adapter_rank(p, a);
+    bf16x8 held[HELD][T];
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) load_t<T>(p, m, 32 * h + 8 * j, rank - 32 * h - 8 * j, mine, held[h]);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+      auto ranks = [&](int r, const bf16x8 (&t)[T]) AWQ_INLINE {
+        const int r8 = r + 8 * j, have = rank - r8;  // this lane's eight ranks, and how many of them there are
+        X8<kBf16> w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (have > 0) {
+            const int64_t ch = n0 + 64 * k + 16 * (c / 4) + 4 * q + c % 4;
+            w[q].load(reinterpret_cast<const char*>(p.b + ((int64_t)a * p.N + (ch < p.N ? ch : p.N - 1)) * p.R + r8));
+          } else {
+            w[q].clear();
+          }
+        }
+        if (have < 8) {  // beyond the rank: zeros, whatever is stored there
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[q].w[i] &= 2 * i + 1 < have ? 0xffffffffu : 2 * i < have ? 0x0000ffffu : 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bf16x8 wt[1];
+          w[q].terms(wt);
+#pragma unroll
+          for (int i = T - 1; i >= 0; --i) acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wt[0], t[i], acc[q], 0, 0, 0);
+        }
+      };
+#pragma unroll
+      for (int h = 0; h < HELD; ++h)
+        if (32 * h < rank) ranks(32 * h, held[h]);
+      for (int r = 32 * HELD; r < rank; r += 32) {
+        bf16x8 t[T];
+        load_t<T>(p, m, r + 8 * j, rank - r - 8 * j, mine, t);
+        ranks(r, t);
+      }
+      if (mine) {
+        if (a != kNone) v[k].add(acc);
+        v[k].store(yrow + 64 * k * Values::kSize, have_n - 64 * k);
       }
     }
   });
@@ -251,22 +314,36 @@ hipError_t launch_down(const LoraArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int T, bool YB, bool VEC, int HELD, int CHUNKS>
+void up_with(const LoraArgs& a, hipStream_t st) {
+  const int64_t across = (a.N + 256 * CHUNKS - 1) / (256 * CHUNKS);
+  const int parts = parts_of(a.M);
+  const dim3 grid((unsigned)(across * ((a.M + 15) / 16)), (unsigned)parts);
+  lora_up_kernel<T, YB, VEC, HELD, CHUNKS><<<grid, 256, 0, st>>>(a, parts);
+}
 template <int T, bool YB>
 hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
-  const int parts = parts_of(a.M);
-  const dim3 grid((unsigned)((a.N + 255) / 256 * ((a.M + 15) / 16)), (unsigned)parts);
-  if (a.vec) lora_up_kernel<T, YB, true><<<grid, 256, 0, st>>>(a, parts);
-  else lora_up_kernel<T, YB, false><<<grid, 256, 0, st>>>(a, parts);
+  constexpr int kMost = YB ? 4 : 2;  // runs of 64 channels a wave, where that leaves 4096 waves
+  const int64_t waves = (a.M + 15) / 16 * ((a.N + 63) / 64);
+  const bool run = a.M > kParallelTokens && waves >= 4096 * kMost;
+  if (!a.vec) up_with<T, YB, false, 1, 1>(a, st);
+  else if (a.R <= 32 && run) up_with<T, YB, true, 1, kMost>(a, st);
+  else if (a.R <= 32) up_with<T, YB, true, 1, 1>(a, st);
+  else if (run) up_with<T, YB, true, 2, kMost>(a, st);
+  else up_with<T, YB, true, 2, 1>(a, st);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Blocks that share K, so that few tokens still fill the card: each has at least 512 channels for its eight waves.
+// Blocks that share K: about 512 in all, each with at least 512 channels for its eight waves; for many tokens at most
+// four, because every wave of the second kernel reads all of them.
 int lora_splits(int64_t M, int64_t K, int64_t R) {
-  const int64_t blocks = (M + 15) / 16 * (M < 16 ? M : 16) * ((R + 15) / 16);
-  int64_t s = 32 / blocks;
-  if (s > K / 512) s = K / 512;
+  const int64_t tiles = (M + 15) / 16, ranks = (R + 15) / 16;
+  const int64_t blocks = M > kParallelTokens ? tiles * ((ranks + 3) / 4) : tiles * (M < 16 ? M : 16) * ranks;
+  int64_t s = (512 + blocks - 1) / blocks, most = M > kParallelTokens ? 4 : 16;
+  if (most > K / 512) most = K / 512;
+  if (s > most) s = most;
   return s < 1 ? 1 : (int)s;
 }
 
