@@ -134,7 +134,7 @@ __global__ __launch_bounds__(512) void lora_down_kernel(const LoraArgs p, int pa
 }
 
 // t of this lane's token (if it is `mine`) and eight ranks from r8 on, of which `have` count, as operand terms.  The splits'
-// parts are requested four at a time and added in order.
+// parts are requested two at a time and added in order.
 template <int T>
 __device__ __forceinline__ void load_t(const LoraArgs& p, int64_t m, int r8, int have, bool mine, bf16x8 (&t)[T]) {
   float v[8];
@@ -142,15 +142,15 @@ __device__ __forceinline__ void load_t(const LoraArgs& p, int64_t m, int r8, int
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   if (mine && have > 0) {
     const float* from = p.t + m * p.R + r8;
-    for (int s0 = 0; s0 < p.splits; s0 += 4) {
-      f32x4 x[4][2];
+    for (int s0 = 0; s0 < p.splits; s0 += 2) {
+      f32x4 x[2][2];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < 2; ++s) {
         const f32x4* tp = reinterpret_cast<const f32x4*>(from + (int64_t)(s0 + s < p.splits ? s0 + s : s0) * p.M * p.R);
         x[s][0] = tp[0], x[s][1] = tp[1];
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 2; ++s)
         if (s0 + s < p.splits)
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += x[s][i / 4][i % 4];
@@ -214,87 +214,151 @@ struct Sixteen {
   }
 };
 
-// Y = base + B t for sixteen tokens and CHUNKS times 64 channels a wave.  The channels are the left operand's rows, the
-// tokens the right operand's columns: row r of tile q is channel 16 (r / 4) + 4 q + r % 4 of the 64, so that a lane holds
-// sixteen consecutive channels of its token.  t of the first 32 HELD ranks stays in registers over the chunks.
-// All of base is requested before anything else.
-template <int T, bool YB, bool VEC, int HELD, int CHUNKS>
+// acc[q][i] += B t for the 64 channels from n0 on, over an adapter's ranks.  The channels are the left operand's rows, the
+// tokens the right operand's columns: row r of tile q is channel 16 (r / 4) + 4 q + r % 4 of the 64, so that lane 16 j + c
+// has channels 16 j + 4 q + i of token c.  t of the first 32 HELD ranks is held in registers.
+template <int T, int HELD>
+__device__ __forceinline__ void add_products(const LoraArgs& p, int a, int rank, int64_t n0, int64_t m, bool mine, int c, int j,
+                                             const bf16x8 (&held)[HELD][T], f32x4 (&acc)[4]) {
+  const int last = p.N - n0 < 64 ? (int)(p.N - n0) - 1 : 63;  // past the last channel: the last again, not stored
+  const char* from = reinterpret_cast<const char*>(p.b + ((int64_t)a * p.N + n0) * p.R);
+  int at[4];  // bytes from there: below 2^16
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int ch = 16 * (c / 4) + 4 * q + c % 4;
+    at[q] = ((ch < last ? ch : last) * p.R + 8 * j) * 2;
+  }
+  auto ranks = [&](int r, const bf16x8 (&t)[T]) AWQ_INLINE {
+    const int have = rank - r - 8 * j;  // of this lane's eight ranks
+    X8<kBf16> w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (have > 0) w[q].load(from + 2 * r + at[q]);
+      else w[q].clear();
+    }
+    if (rank & 7) {  // beyond the rank: zeros, whatever is stored there
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[q].w[i] &= 2 * i + 1 < have ? 0xffffffffu : 2 * i < have ? 0x0000ffffu : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8 wt[1];
+      w[q].terms(wt);
+#pragma unroll
+      for (int i = T - 1; i >= 0; --i) acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wt[0], t[i], acc[q], 0, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+    if (32 * h < rank) ranks(32 * h, held[h]);
+  for (int r = 32 * HELD; r < rank; r += 32) {
+    bf16x8 t[T];
+    load_t<T>(p, m, r + 8 * j, rank - r - 8 * j, mine, t);
+    ranks(r, t);
+  }
+}
+
+// Y = base + B t for sixteen tokens and 64 channels a wave; a tile's adapters go to `parts` blocks.
+template <int T, bool YB, bool VEC, int HELD>
 __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs p, int parts) {
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t across = (p.N + 256 * CHUNKS - 1) / (256 * CHUNKS);
-  const int64_t m0 = (int64_t)blockIdx.x / across * 16;
-  const int64_t n0 = ((int64_t)blockIdx.x % across * 4 + wave) * 64 * CHUNKS;
+  const int64_t across = (p.N + 255) / 256;
+  const int64_t m0 = (int64_t)blockIdx.x / across * 16, n0 = ((int64_t)blockIdx.x % across * 4 + wave) * 64;
   if (n0 >= p.N) return;
   const int64_t m = m0 + c < p.M ? m0 + c : p.M - 1;
   using Values = Sixteen<YB, VEC>;
   const char* brow = static_cast<const char*>(p.base) + (m * p.ldb + n0 + 16 * j) * Values::kSize;
   char* yrow = static_cast<char*>(p.y) + (m * p.ldy + n0 + 16 * j) * Values::kSize;
   const int64_t there = p.N - n0 - 16 * j;  // channels from this lane's first on
-  const int have_n = there < 64 * CHUNKS ? (int)there : 64 * CHUNKS;
-  Values v[CHUNKS];
-  if (parts == 1) {
-#pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) v[k].load(brow + 64 * k * Values::kSize, have_n - 64 * k);
-  }
+  const int have = there < 64 ? (int)there : 64;
   const int id = row_adapter(p, m0, c);
   const bool copies = p.base != p.y;
   each_adapter(id, (int)blockIdx.y, parts, [&](int a, uint32_t rows) AWQ_INLINE {
     if (a == kNone && !copies) return;
     const bool mine = rows >> c & 1u;
-    if (parts > 1 && mine) {
+    Values v;
+    if (mine) v.load(brow, have);
+    if (a != kNone) {
+      const int rank = adapter_rank(p, a);
+      bf16x8 held[HELD][T];
 #pragma unroll
-      for (int k = 0; k < CHUNKS; ++k) v[k].load(brow + 64 * k * Values::kSize, have_n - 64 * k);
-    }
-    const int rank = a == kNone ? 0 : adapter_rank(p, a);
-    bf16x8 held[HELD][T];
-#pragma unroll
-    for (int h = 0; h < HELD; ++h) load_t<T>(p, m, 32 * h + 8 * j, rank - 32 * h - 8 * j, mine, held[h]);
-#pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) {
+      for (int h = 0; h < HELD; ++h) load_t<T>(p, m, 32 * h + 8 * j, rank - 32 * h - 8 * j, mine, held[h]);
       f32x4 acc[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-      auto ranks = [&](int r, const bf16x8 (&t)[T]) AWQ_INLINE {
-        const int r8 = r + 8 * j, have = rank - r8;  // this lane's eight ranks, and how many of them there are
-        X8<kBf16> w[4];
+      add_products<T, HELD>(p, a, rank, n0, m, mine, c, j, held, acc);
+      if (mine) v.add(acc);
+    }
+    if (mine) v.store(yrow, have);
+  });
+}
+
+// The same for prompts: sixteen tokens and 512 channels a block, whose eight waves lay their products out in LDS, so that
+// base and Y go by in whole runs of a row (4096 x 4096 -> 14336 with both kernels: 81 us; each lane with its sixteen channels
+// 89; 1024 channels a block 89).  All of base is requested before anything else.  N is a multiple of a run's 16 bytes, the rows start at multiples of them.
+template <int T, bool YB, int HELD>
+__global__ __launch_bounds__(512) void lora_up_rows_kernel(const LoraArgs p) {
+  constexpr int C = 512, kSize = YB ? 2 : 4, kUnit = 16 / kSize;  // channels of a block, of 16 bytes
+  constexpr int kTurns = 16 * C / kUnit / 512;                    // units of a thread
+  static_assert(C / kUnit % 64 == 0, "a wave's units are one row's");
+  constexpr int kRow = C + 4;                                     // sixteen rows' same 16 bytes: all banks
+  __shared__ __attribute__((aligned(16))) float sums[16 * kRow];
+  const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t across = (p.N + C - 1) / C;
+  const int64_t m0 = (int64_t)blockIdx.x / across * 16, b0 = (int64_t)blockIdx.x % across * C, n0 = b0 + 64 * wave;
+  u32x4 v[kTurns];
+  auto place = [&](int i, int& row, int& ch) AWQ_INLINE {
+    const int u = (int)threadIdx.x + 512 * i;
+    row = u / (C / kUnit), ch = u % (C / kUnit) * kUnit;
+    return m0 + row < p.M && b0 + ch < p.N;
+  };
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (have > 0) {
-            const int64_t ch = n0 + 64 * k + 16 * (c / 4) + 4 * q + c % 4;
-            w[q].load(reinterpret_cast<const char*>(p.b + ((int64_t)a * p.N + (ch < p.N ? ch : p.N - 1)) * p.R + r8));
-          } else {
-            w[q].clear();
-          }
-        }
-        if (have < 8) {  // beyond the rank: zeros, whatever is stored there
+  for (int i = 0; i < kTurns; ++i) {
+    int row, ch;
+    if (place(i, row, ch))
+      v[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.base) + ((m0 + row) * p.ldb + b0 + ch) * kSize);
+  }
+  const int64_t m = m0 + c < p.M ? m0 + c : p.M - 1;
+  const int id = row_adapter(p, m0, c);
+  if (n0 < p.N) {
+    each_adapter(id, 0, 1, [&](int a, uint32_t rows) AWQ_INLINE {
+      if (a == kNone) return;
+      const bool mine = rows >> c & 1u;
+      const int rank = adapter_rank(p, a);
+      bf16x8 held[HELD][T];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+      for (int h = 0; h < HELD; ++h) load_t<T>(p, m, 32 * h + 8 * j, rank - 32 * h - 8 * j, mine, held[h]);
+      f32x4 acc[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[q].w[i] &= 2 * i + 1 < have ? 0xffffffffu : 2 * i < have ? 0x0000ffffu : 0u;
-        }
+      for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+      add_products<T, HELD>(p, a, rank, n0, m, mine, c, j, held, acc);
+      if (mine)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x8 wt[1];
-          w[q].terms(wt);
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4*>(sums + c * kRow + 64 * wave + 16 * j + 4 * q) = acc[q];
+    });
+  }
+  __syncthreads();
+  const bool copies = p.base != p.y;
 #pragma unroll
-          for (int i = T - 1; i >= 0; --i) acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wt[0], t[i], acc[q], 0, 0, 0);
-        }
-      };
+  for (int i = 0; i < kTurns; ++i) {
+    int row, ch;
+    const bool there = place(i, row, ch);
+    const int a = __builtin_amdgcn_readlane(id, __builtin_amdgcn_readfirstlane(row));  // a wave's 64 units are one row's
+    if (!there || (a == kNone && !copies)) continue;
+    if (a != kNone) {
+      const float* s = sums + row * kRow + ch;
 #pragma unroll
-      for (int h = 0; h < HELD; ++h)
-        if (32 * h < rank) ranks(32 * h, held[h]);
-      for (int r = 32 * HELD; r < rank; r += 32) {
-        bf16x8 t[T];
-        load_t<T>(p, m, r + 8 * j, rank - r - 8 * j, mine, t);
-        ranks(r, t);
-      }
-      if (mine) {
-        if (a != kNone) v[k].add(acc);
-        v[k].store(yrow + 64 * k * Values::kSize, have_n - 64 * k);
+      for (int d = 0; d < 4; ++d) {
+        if constexpr (YB) v[i][d] = pack_rne(flt(v[i][d] << 16) + s[2 * d], flt(v[i][d] & 0xffff0000u) + s[2 * d + 1]);
+        else v[i][d] = bits(flt(v[i][d]) + s[d]);
       }
     }
-  });
+    *reinterpret_cast<u32x4*>(static_cast<char*>(p.y) + ((m0 + row) * p.ldy + b0 + ch) * kSize) = v[i];
+  }
 }
 
 // Up to this many tokens a tile's distinct adapters go to blocks of their own (a decode batch: up to sixteen requests in a
@@ -314,23 +378,20 @@ hipError_t launch_down(const LoraArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int T, bool YB, bool VEC, int HELD, int CHUNKS>
-void up_with(const LoraArgs& a, hipStream_t st) {
-  const int64_t across = (a.N + 256 * CHUNKS - 1) / (256 * CHUNKS);
-  const int parts = parts_of(a.M);
-  const dim3 grid((unsigned)(across * ((a.M + 15) / 16)), (unsigned)parts);
-  lora_up_kernel<T, YB, VEC, HELD, CHUNKS><<<grid, 256, 0, st>>>(a, parts);
-}
 template <int T, bool YB>
 hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
-  constexpr int kMost = YB ? 4 : 2;  // runs of 64 channels a wave, where that leaves 4096 waves
-  const int64_t waves = (a.M + 15) / 16 * ((a.N + 63) / 64);
-  const bool run = a.M > kParallelTokens && waves >= 4096 * kMost;
-  if (!a.vec) up_with<T, YB, false, 1, 1>(a, st);
-  else if (a.R <= 32 && run) up_with<T, YB, true, 1, kMost>(a, st);
-  else if (a.R <= 32) up_with<T, YB, true, 1, 1>(a, st);
-  else if (run) up_with<T, YB, true, 2, kMost>(a, st);
-  else up_with<T, YB, true, 2, 1>(a, st);
+  const int64_t tiles = (a.M + 15) / 16;
+  if (a.M > kParallelTokens && a.vec && a.N % (YB ? 8 : 4) == 0) {
+    const unsigned grid = (unsigned)((a.N + 511) / 512 * tiles);
+    if (a.R <= 32) lora_up_rows_kernel<T, YB, 1><<<grid, 512, 0, st>>>(a);
+    else lora_up_rows_kernel<T, YB, 2><<<grid, 512, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  const int parts = parts_of(a.M);
+  const dim3 grid((unsigned)((a.N + 255) / 256 * tiles), (unsigned)parts);
+  if (!a.vec) lora_up_kernel<T, YB, false, 1><<<grid, 256, 0, st>>>(a, parts);
+  else if (a.R <= 32) lora_up_kernel<T, YB, true, 1><<<grid, 256, 0, st>>>(a, parts);
+  else lora_up_kernel<T, YB, true, 2><<<grid, 256, 0, st>>>(a, parts);
   return hipGetLastError();
 }
 
