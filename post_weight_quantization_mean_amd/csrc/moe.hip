@@ -29,13 +29,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kMasked = 0x007fffffu;  // -Inf; below: no expert
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return o > v ? o : v;
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = dpp_max<kDppMirror>(dpp_max<kDppHalfMirror>(dpp_max<kDppXor2>(dpp_max<kDppXor1>(v))));
+  uint32_t m = 0;  // of the four rows of sixteen lanes
 #pragma unroll
-  for (int i = 1; i < 64; i *= 2) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, i, 64);
-    v = o > v ? o : v;
+  for (int i = 0; i < 64; i += 16) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, i);
+    m = o > m ? o : m;
   }
-  return v;
+  return m;
 }
 
 // The k choices of one token: lane j < k gets the j-th's expert and weight.
@@ -330,8 +337,8 @@ constexpr int waves_per_simd(size_t operands) { return operands <= 128 ? 4 : 2; 
 
 // The expert of a slot: experts, where there are at least as many pairs as experts, else the expert of the pair of that
 // number, which the first of its pairs takes for all.
-__device__ __forceinline__ int slot_expert(const MoeArgs& p, int slot) {
-  const int e = p.by_pair ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : slot;
+__device__ __forceinline__ int slot_expert(const MoeArgs& p, const int32_t* ids, int slot) {
+  const int e = p.by_pair ? __builtin_amdgcn_readfirstlane(ids[slot]) : slot;
   return e >= 0 && e < p.E ? e : -1;
 }
 
@@ -477,21 +484,41 @@ __device__ __forceinline__ void store_h(const MoeArgs& p, int64_t plane, int pai
 }
 
 // act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
-template <int XT, int TT, int NG, int WV, bool INNER>
-__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * TT * NG)) void moe_up_kernel(const MoeArgs p, int per) {
+// ROUTE: from the router's logits, for a token a wave; every block makes the routing for itself, and one writes it for the
+// kernels behind (4 tokens, 8 of 128 experts: the layer takes ... us, 35.5 with the router in a kernel of its own).
+template <int XT, int TT, int NG, int WV, bool INNER, bool ROUTE>
+__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * TT * NG)) void moe_up_kernel(
+    const MoeArgs p, const RouteArgs r, bool lbf16, int per) {
   __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
   __shared__ int counts[WV];
   const int lane = threadIdx.x & 63, j = lane >> 4;
-  const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, slot);
+  __shared__ int32_t routed[ROUTE ? WV * kMaxChosen : 1];
+  const int slot = (int)blockIdx.y, P = p.M * p.k, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t* ids = p.ids;
+  if constexpr (ROUTE) {
+    if (wave < p.M) {
+      int id;
+      float w;
+      route_token<kRouteHere / 64>(static_cast<const char*>(r.logits) + wave * r.ld * (lbf16 ? 2 : 4), lbf16, r.E, r.k, r.score,
+                                   r.renorm, lane, id, w);
+      if (lane < r.k) {
+        routed[wave * r.k + lane] = id;
+        if (blockIdx.x == 0 && slot == 0) r.ids[wave * r.k + lane] = id, r.weights[wave * r.k + lane] = w;
+      }
+    }
+    __syncthreads();
+    ids = routed;
+  }
+  const int e = slot_expert(p, ids, slot);
   if (e < 0) return;
   const int tile0 = (int)blockIdx.x * per, left = p.I / 16 - tile0;
   ExpertPass<XT, TT, NG, WV, INNER> pass;
   pass.w = p.up;
   pass.tiles = Tiles{(int64_t)e * (p.I / 8) + tile0, p.I / 16, 1, left < per ? left : per};
-  pass.G = p.H / kGroup, pass.lane = lane, pass.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  pass.G = p.H / kGroup, pass.lane = lane, pass.wave = wave;
   pass.begin();
-  const int n = expert_pairs<WV>(p.ids, P, e, list, counts);
+  const int n = expert_pairs<WV>(ids, P, e, list, counts);
   if (n == 0 || (p.by_pair && list[0] != slot)) return;
   const int64_t plane = (int64_t)P * p.I;
   pass.run(
@@ -516,7 +543,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)
   __shared__ uint16_t list[kMoePairs];
   __shared__ int counts[WV];
   const int lane = threadIdx.x & 63, j = lane >> 4;
-  const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, slot);
+  const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, p.ids, slot);
   if (e < 0) return;
   const int pair0 = (int)blockIdx.x * per, left = p.H / 32 - pair0;
   ExpertPass<T == 2 ? kPlanes2 : kPlanes3, TT, NG, WV, T == 3> pass;
@@ -747,17 +774,19 @@ int units_per_block(int slots, int units, int waves) {
   return per < 1 ? 1 : per;
 }
 
-template <int XT, int TT, int NG, int WV, bool INNER>
-void up_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
+template <int XT, int NG, int WV, bool INNER>
+void up_with(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
   const int per = units_per_block((int)slots, a.I / 16, WV);
-  moe_up_kernel<XT, TT, NG, WV, INNER><<<dim3((unsigned)((a.I / 16 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
+  const dim3 grid((unsigned)((a.I / 16 + per - 1) / per), slots);
+  if (r != nullptr) moe_up_kernel<XT, 1, NG, WV, INNER, true><<<grid, 64 * WV, 0, st>>>(a, *r, l_type == kBf16, per);
+  else moe_up_kernel<XT, 1, NG, WV, INNER, false><<<grid, 64 * WV, 0, st>>>(a, RouteArgs{}, false, per);
 }
 template <int XT, bool INNER>
-void launch_up(const MoeArgs& a, unsigned slots, hipStream_t st) {
+void launch_up(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
   const int G = a.H / kGroup;
-  if (G <= 8) up_with<XT, 1, 1, 8, INNER>(a, slots, st);
-  else if (G <= 16) up_with<XT, 1, 2, 8, INNER>(a, slots, st);
-  else up_with<XT, 1, XT == kF32 ? 1 : 2, 16, INNER>(a, slots, st);
+  if (G <= 8) up_with<XT, 1, 8, INNER>(a, r, l_type, slots, st);
+  else if (G <= 16) up_with<XT, 2, 8, INNER>(a, r, l_type, slots, st);
+  else up_with<XT, XT == kF32 ? 1 : 2, 16, INNER>(a, r, l_type, slots, st);
 }
 
 template <int T, int TT, int NG, int WV>
@@ -784,11 +813,11 @@ void down_tiles(const MoeArgs& a, hipStream_t st) {
 }
 
 template <int XT, bool INNER>
-void launch_products(const MoeArgs& a, hipStream_t st) {
+void launch_products(const MoeArgs& a, const RouteArgs* r, int l_type, hipStream_t st) {
   const int P = a.M * a.k;
   const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
   if (P > 12 * a.E) up_tiles<XT, XT == kF32 ? 2 : 4, INNER>(a, st);
-  else launch_up<XT, INNER>(a, slots, st);
+  else launch_up<XT, INNER>(a, r, l_type, slots, st);
 }
 template <int T>
 void launch_sums(const MoeArgs& a, hipStream_t st) {
@@ -800,13 +829,13 @@ void launch_sums(const MoeArgs& a, hipStream_t st) {
 }
 
 template <int XT>
-hipError_t launch_experts(MoeArgs a, hipStream_t st) {
+hipError_t launch_experts(MoeArgs a, const RouteArgs* r, int l_type, hipStream_t st) {
   a.by_pair = a.M * a.k < a.E;
   if (a.terms == 2) {
-    launch_products<XT, false>(a, st);
+    launch_products<XT, false>(a, r, l_type, st);
     launch_sums<2>(a, st);
   } else {
-    launch_products<XT, XT != kI8>(a, st);
+    launch_products<XT, XT != kI8>(a, r, l_type, st);
     launch_sums<3>(a, st);
   }
   return hipGetLastError();
@@ -825,12 +854,15 @@ hipError_t launch_moe_route(const RouteArgs& a, int l_type, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_moe(const MoeArgs& a, int x_type, hipStream_t st) {
+// Up to eight tokens (a wave of the smallest block each) that do not run in tiles, and few enough experts.
+bool moe_routes(int64_t M, int k, int E) { return M <= 8 && E <= kRouteHere && M * k <= 12 * E; }
+
+hipError_t launch_moe(const MoeArgs& a, const RouteArgs* r, int l_type, int x_type, hipStream_t st) {
   switch (x_type) {
-    case kF32: return launch_experts<kF32>(a, st);
-    case kBf16: return launch_experts<kBf16>(a, st);
-    case kI8: return launch_experts<kI8>(a, st);
-    default: return launch_experts<kE4m3>(a, st);
+    case kF32: return launch_experts<kF32>(a, r, l_type, st);
+    case kBf16: return launch_experts<kBf16>(a, r, l_type, st);
+    case kI8: return launch_experts<kI8>(a, r, l_type, st);
+    default: return launch_experts<kE4m3>(a, r, l_type, st);
   }
 }
 

@@ -88,12 +88,17 @@ int run_moe(const void* X, int x_dtype, const float* xscale, int64_t M, int64_t 
   char* w = static_cast<char*>(ws);
   const int32_t* ids = r.ids;
   const float* weights = r.weights;
+  awq::RouteArgs route{};
+  bool here = false;  // routed inside the first kernel of the products
   if (r.logits != nullptr) {
     int32_t* wi = reinterpret_cast<int32_t*>(w + L.ids);
     float* ww = reinterpret_cast<float*>(w + L.weights);
-    const hipError_t e =
-        awq::launch_moe_route(route_args(r.logits, M, E, r.ldl, k, r.score, r.renormalize, wi, ww), r.l_dtype, s);
-    if (e != hipSuccess) return map_hip(e);
+    route = route_args(r.logits, M, E, r.ldl, k, r.score, r.renormalize, wi, ww);
+    here = awq::moe_routes(M, k, (int)E);
+    if (!here) {
+      const hipError_t e = awq::launch_moe_route(route, r.l_dtype, s);
+      if (e != hipSuccess) return map_hip(e);
+    }
     ids = wi, weights = ww;
   }
   auto part = [](const void* wt, const awq::W4a8Layout& l) {
@@ -113,7 +118,7 @@ int run_moe(const void* X, int x_dtype, const float* xscale, int64_t M, int64_t 
     a.xscale = code_type(x_dtype) ? xscale + m : nullptr;
     a.ids = ids + m * k, a.weights = weights + m * k;
     a.y = static_cast<char*>(Y) + m * ldy * dsize(y_dtype);
-    const hipError_t e = awq::launch_moe(a, x_dtype, s);
+    const hipError_t e = awq::launch_moe(a, here ? &route : nullptr, r.l_dtype, x_dtype, s);
     if (e != hipSuccess) return map_hip(e);
   }
   return AWQ_OK;

@@ -7,6 +7,7 @@ namespace awq {
 
 constexpr int kMaxExperts = 1024, kMaxChosen = 32;
 constexpr int kMoePairs = 2048;  // (token, expert) pairs of one pass at most: their list is kept on chip
+constexpr int kRouteHere = 256;  // experts up to which the router may run inside the products' first kernel
 constexpr int kSoftmax = 0, kSigmoid = 1;
 
 struct RouteArgs {
@@ -37,6 +38,9 @@ struct MoeArgs {
   int M, k, E, H, I, act, terms;
   bool ybf16, by_pair;   // by_pair: slots are pairs, not experts
 };
-hipError_t launch_moe(const MoeArgs& a, int x_type, hipStream_t st);
+// Whether the products' first kernel makes the routing of M tokens itself.
+bool moe_routes(int64_t M, int k, int E);
+// r: the routing that it makes (where a.ids and a.weights point), or null where they are given
+hipError_t launch_moe(const MoeArgs& a, const RouteArgs* r, int l_type, int x_type, hipStream_t st);
 
 }  // namespace awq
