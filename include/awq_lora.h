@@ -34,8 +34,8 @@ extern "C" {
  * handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  A row's result does not
  * depend on which rows stand beside it, but for the order of the sums over K, which the sizes alone decide: equal calls
  * give equal bits.
- * 64 rows of X, of base and of Y span less than 2^31 bytes each, M is below 2^24, adapters below 2^31 (AWQ_ERR_SHAPE; the
- * workspace's size is then 0).  Apart from Y = base, Y and ws overlap no input and not each other (an exact start is
+ * M is below 2^24, N below 2^22, K and adapters below 2^31, ceil(M / 16) ceil(N / 256) below 2^23 (AWQ_ERR_SHAPE; the workspace's
+ * size is then 0).  Apart from Y = base, Y and ws overlap no input and not each other (an exact start is
  * checked: AWQ_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R);

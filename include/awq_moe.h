@@ -22,8 +22,8 @@ extern "C" {
 
 /* ---------------------------------------------------------------------------------------
  * The router: the k experts of each token with the largest logits, largest first, ties to the lowest index.
- *   logits   [M, E] of l_dtype (F32, BF16), row stride ldl, E at most 1024
- *   k        1 .. min(E, 32)
+ *   logits   [M, E] of l_dtype (F32, BF16), row stride ldl, M at most 2^24, E 1024 (AWQ_ERR_SHAPE)
+ *   k        1 .. E (AWQ_ERR_INVALID_ARG), at most 32 (AWQ_ERR_SHAPE)
  *   ids      int32 [M, k]
  *   weights  fp32 [M, k]: the score of the expert, and with renormalize != 0 divided by the sum of the k scores (scores
  *            that all underflow keep their ratios)
@@ -49,8 +49,8 @@ AWQ_API int awq_moe_route(const void* logits, int l_dtype, int64_t M, int64_t E,
  *   Y        [M, H] of y_dtype (F32, BF16), row stride ldy; a token without an expert here gets 0
  *   ws       device memory of at least awq_moe_workspace_bytes bytes, 256-byte aligned; nothing in it has to start at
  *            zero, and calls that may run at the same time need one each
- * H and I are multiples of 128, E at most 1024, k at most 32, 2 I E and H E at most 2^27 (AWQ_ERR_SHAPE; the workspace's
- * size is then 0).  Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms), sums fp32;
+ * H and I are multiples of 128 up to 2^20, M is at most 2^24, E 1024, k 32, 2 I E and H E 2^27 (AWQ_ERR_SHAPE; the
+ * workspace's size is then 0).  Zero points are whole numbers, as awq_pack writes them.  Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms), sums fp32;
  * act(gate) * up is formed in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is
  * rounded once.  The order of the sums depends on the sizes alone: equal calls give equal bits.
  * Y and ws overlap no input and not each other (an exact start is checked: AWQ_ERR_INVALID_ARG).

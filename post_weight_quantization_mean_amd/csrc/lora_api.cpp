@@ -10,11 +10,11 @@ namespace {
 
 using namespace awq::api;
 
-constexpr int64_t kMaxRank = 256, kMaxRows = 1 << 24;
+constexpr int64_t kMaxRank = 256, kMaxRows = 1 << 24, kMaxCols = 1 << 22;
 
 // The sizes as the launches take them: fewer than 2^32 threads, and 32-bit tile counts.
 bool lora_sizes(int64_t M, int64_t K, int64_t N, int64_t R) {
-  if (M <= 0 || K <= 0 || N <= 0 || R <= 0 || M >= kMaxRows || N >= kMaxRows || K % 8 != 0 || R % 8 != 0 || R > kMaxRank)
+  if (M <= 0 || K <= 0 || N <= 0 || R <= 0 || M >= kMaxRows || N >= kMaxCols || K % 8 != 0 || R % 8 != 0 || R > kMaxRank)
     return false;
   return (M + 15) / 16 * ((N + 255) / 256) < (1 << 23) && K < (int64_t)INT32_MAX;
 }
@@ -44,8 +44,6 @@ AWQ_API int awq_lora(const void* X, int x_dtype, const float* xscale, int64_t M,
   if (!rows_aligned(X, x_dtype, ldx, code_type(x_dtype) ? 8 : 16) || !aligned(A, 16) || !aligned(B, 16) ||
       !aligned(ids, 4) || !aligned(ranks, 4) || !aligned(scale, 4))
     return AWQ_ERR_INVALID_ARG;
-  for (const int64_t span : {mul3(64, ldx, dsize(x_dtype)), mul3(64, ldb, dsize(y_dtype)), mul3(64, ldy, dsize(y_dtype))})
-    if (span < 0 || span >= (int64_t)INT32_MAX) return AWQ_ERR_SHAPE;
   const size_t need = awq_lora_workspace_bytes(M, K, N, R);
   if (ws == nullptr || ws_bytes < need) return AWQ_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return AWQ_ERR_INVALID_ARG;

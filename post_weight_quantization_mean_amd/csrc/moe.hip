@@ -767,7 +767,9 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
   }
 }
 
-// Blocks of a run of `units` per slot: about 512 in all (two on a CU) of eight waves, 256 of sixteen.
+// Units of a block's run: blocks for one round of the card's CUs, `waves` being a sixteenth of a CU each: about 512 of eight
+// waves where two share a CU, 256 otherwise.  (37 fp32 tokens, 16 experts of 1280 x 896: 27.9 us, 33.1 in two rounds; 4 tokens,
+// 8 of 128 experts, 32.4, with twice the blocks 39.2.)
 int units_per_block(int slots, int units, int waves) {
   const int total = 4096 / waves, blocks = (total + slots - 1) / slots;
   const int per = (units + blocks - 1) / blocks;
@@ -776,7 +778,7 @@ int units_per_block(int slots, int units, int waves) {
 
 template <int XT, int NG, int WV, bool INNER>
 void up_with(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
-  const int per = units_per_block((int)slots, a.I / 16, WV);
+  const int per = units_per_block((int)slots, a.I / 16, WV * 4 / waves_per_simd(sizeof(typename Source<XT>::Operand) * NG));
   const dim3 grid((unsigned)((a.I / 16 + per - 1) / per), slots);
   if (r != nullptr) moe_up_kernel<XT, 1, NG, WV, INNER, true><<<grid, 64 * WV, 0, st>>>(a, *r, l_type == kBf16, per);
   else moe_up_kernel<XT, 1, NG, WV, INNER, false><<<grid, 64 * WV, 0, st>>>(a, RouteArgs{}, false, per);
@@ -791,7 +793,7 @@ void launch_up(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots,
 
 template <int T, int TT, int NG, int WV>
 void down_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
-  const int per = units_per_block((int)slots, a.H / 32, WV);
+  const int per = units_per_block((int)slots, a.H / 32, WV * 4 / waves_per_simd(sizeof(Terms<T>) * NG));
   moe_down_kernel<T, TT, NG, WV><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
 }
 template <int T>
@@ -800,8 +802,11 @@ void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
   else down_with<T, 1, 1, 16>(a, slots, st);
 }
 
-// Blocks for a slot's token tiles: what an expert has on average, and one more for those that have more.
-unsigned tile_depth(const MoeArgs& a, int tokens) { return (unsigned)(a.M * a.k / (a.E * tokens) + 2); }
+// Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
+unsigned tile_depth(const MoeArgs& a, int tokens) {
+  const int depth = a.M * a.k * 3 / (2 * a.E * tokens) + 1;
+  return (unsigned)(depth < 8 ? depth : 8);
+}
 
 template <int XT, int TM, bool INNER>
 void up_tiles(const MoeArgs& a, hipStream_t st) {

@@ -11,7 +11,8 @@ namespace {
 
 using namespace awq::api;
 
-constexpr int64_t kMaxTokens = 1 << 24;  // a launch's threads: 64 per token
+// A launch takes fewer than 2^32 threads: 64 per token (router); a quarter per result of 2048 pairs (sum).
+constexpr int64_t kMaxTokens = 1 << 24, kMaxWidth = 1 << 20;
 
 bool route_sizes(int64_t M, int64_t E, int64_t k) {
   return M > 0 && M <= kMaxTokens && E > 0 && E <= awq::kMaxExperts && k > 0 && k <= awq::kMaxChosen;
@@ -40,7 +41,7 @@ struct MoeLayout {
 };
 
 bool moe_layout(int64_t M, int64_t E, int64_t k, int64_t H, int64_t I, MoeLayout* L) {
-  if (!route_sizes(M, E, k) || H <= 0 || I <= 0 || H > kMaxN || I > kMaxN || H % 32 != 0 || I % 16 != 0) return false;
+  if (!route_sizes(M, E, k) || H <= 0 || I <= 0 || H > kMaxWidth || I > kMaxWidth) return false;
   if (!w4a8_layout(2 * I * E, H, &L->up) || !w4a8_layout(H * E, I, &L->down)) return false;
   L->pass = awq::kMoePairs / k < M ? awq::kMoePairs / k : M;
   const int64_t pairs = L->pass * k;

@@ -170,7 +170,8 @@ def check_moe(awq, x, x64, ids, w, gu, down, hg, hd, act, out, into=None, **kw):
 # tokens an expert, odd group counts, one and several groups a wave, one expert
 MOE_SHAPES = [(1, 8, 2, 128, 128), (1, 4, 4, 256, 384), (3, 32, 8, 128, 256), (2, 3, 1, 1152, 128), (17, 4, 2, 256, 128),
               (40, 3, 3, 384, 128), (5, 1, 1, 128, 1280), (70, 2, 1, 128, 256), (9, 16, 4, 2176, 128), (90, 5, 2, 384, 384),
-              (101, 2, 2, 640, 256), (83, 1, 1, 128, 128), (12, 2, 2, 1152, 2176)]
+              (101, 2, 2, 640, 256), (83, 1, 1, 128, 128), (12, 2, 2, 1152, 2176), (2, 3, 2, 4224, 128),
+              (3, 2, 1, 128, 2304)]
 
 
 @pytest.mark.parametrize("M,E,k,H,I", MOE_SHAPES)
@@ -270,15 +271,18 @@ def test_moe_far_activations(awq):
         check_moe(awq, x, f64(x), ids, w, gu, down, handle(awq, gu), handle(awq, down), act, F32)
 
 
-@pytest.mark.parametrize("M,E,k", [(1, 16, 4), (3, 64, 8), (8, 70, 6), (30, 9, 3), (300, 20, 8)])
-@pytest.mark.parametrize("dtype,score,renorm", [(F32, "softmax", True), (BF16, "sigmoid", False)])
-def test_layer_is_route_and_experts(awq, M, E, k, dtype, score, renorm):
+@pytest.mark.parametrize("M,E,k,H", [(1, 16, 4, 256), (3, 64, 8, 256), (8, 70, 6, 1152), (8, 256, 32, 128), (8, 257, 5, 128),
+                                     (9, 16, 2, 256), (5, 3, 2, 2176), (7, 40, 3, 2176), (30, 9, 3, 256), (300, 20, 8, 256)])
+@pytest.mark.parametrize("kind,dtype,score,renorm", [(BF16, F32, "softmax", True), (F32, BF16, "sigmoid", False),
+                                                     (I8, BF16, "softmax", False), (E4M3, F32, "sigmoid", True)])
+def test_layer_is_route_and_experts(awq, M, E, k, H, kind, dtype, score, renorm):
     """The whole layer gives what the router and the experts give, bit for bit, masked experts among them."""
-    banner(f"layer M={M} E={E} k={k} {dtype} {score}")
+    banner(f"layer M={M} E={E} k={k} H={H} {kind} {dtype} {score}")
     rng = rng_of(10)
-    H, I = 256, 128
+    I = 128
     hg, hd = handle(awq, artefact(rng, E, 2 * I, H)), handle(awq, artefact(rng, E, H, I))
-    x, _ = activations(rng, M, H, BF16)
+    x, _ = activations(rng, M, H, kind)
+    x = awq.Act8(*x) if isinstance(x, tuple) else x
     logits = torch.from_numpy(rng.standard_normal((M, E + 2))).to(dtype).to(DEV)[:, :E]
     logits[0, 2:] = -float("inf")
     r = awq.moe_route(logits, k, score=score, renormalize=renorm)
