@@ -343,16 +343,17 @@ __device__ __forceinline__ int slot_expert(const MoeArgs& p, const int32_t* ids,
 }
 
 // ---- an expert's tokens past a run of channel tiles -------------------------------------------------------
-// The block's WV waves share the groups, NG each at a time; the operands of 16 TT tokens stay in registers while the
-// weight passes (they are read again per tile where the groups are more than WV NG).  A step is a pair of channel tiles in
-// WV NG groups; every group's codes are requested a step ahead, into the registers that it just freed.  The waves' sums meet
-// in LDS, in wave order, and out(list position, pair of tiles, channel, sum of the one tile, of the other) takes them.
+// The block's WV waves share the groups, NG each at a time, and take an expert's tokens sixteen at a time.  A step is a pair
+// of channel tiles in WV NG groups; every group's codes are requested a step ahead, into the registers that it just freed.
+// Where one step covers all groups the tokens' operands stay in registers while the weight passes; otherwise they are read
+// again for every WV NG groups of PC pairs.  The waves' sums meet in LDS, in wave order, and out(list position, pair of
+// tiles, channel, sum of the one tile, of the other) takes them.
 struct Tiles {
   int64_t first, other;  // the run's first tile, and how much further the second of a pair is
   int step, count;       // from pair to pair; pairs
 };
 
-template <int SRC, int TT, int NG, int WV, bool INNER>
+template <int SRC, int NG, int WV, int PC, bool INNER>
 struct ExpertPass {
   using S = Source<SRC>;
   using Op = typename S::Operand;
@@ -384,83 +385,78 @@ struct ExpertPass {
   __device__ __forceinline__ void run(int n, int64_t plane, float (*part)[WV][512], Row row, Out out) {
     const int c = lane & 15, j = lane >> 4;
     int turn = 0;
-    for (int t0 = 0; t0 < n; t0 += 16 * TT) {
-      const char* r[TT];
+    for (int t0 = 0; t0 < n; t0 += 16) {
+      const char* r = row(t0 + c < n ? t0 + c : n - 1);
+      Op x[NG];
+      f32x4 sx[NG];
+      for (int p0 = 0; p0 < tiles.count; p0 += PC) {
+        const int pairs = tiles.count - p0 < PC ? tiles.count - p0 : PC;
+        f32x4 tot[PC][2];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int i = t0 + 16 * t + c;
-        r[t] = row(i < n ? i : n - 1);
-      }
-      Op x[TT][NG];
-      f32x4 sx[TT][NG];
-      for (int pair = 0; pair < tiles.count; ++pair) {
-        f32x4 tot[TT][2];
+        for (int u = 0; u < PC; ++u)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t first = (tiles.first + (int64_t)pair * tiles.step) * 16 + (threadIdx.x & 15);
-        const float power0 = w.powers[first], power1 = w.powers[first + 16 * tiles.other];
+          for (int q = 0; q < 2; ++q) tot[u][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         for (int g0 = 0; g0 < G; g0 += WV * NG) {
-          if (pair == 0 || G > WV * NG) {
+          if (p0 == 0 || G > WV * NG) {
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
               const int g = g0 + wave + i * WV;
-#pragma unroll
-              for (int t = 0; t < TT; ++t) {
-                if (t > 0 && t0 + 16 * t >= n) break;
-                if (g < G) S::load(x[t][i], r[t], g, plane);
-                else x[t][i].clear();
-              }
+              if (g < G) S::load(x[i], r, g, plane);
+              else x[i].clear();
             }
             if constexpr (!INNER) {
 #pragma unroll
-              for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                  if (t > 0 && t0 + 16 * t >= n) break;
-                  sx[t][i] = x[t][i].ones();
-                }
+              for (int i = 0; i < NG; ++i) sx[i] = x[i].ones();
             }
           }
-          // the step after this one
-          const bool same = g0 + WV * NG < G, more = pair + 1 < tiles.count || t0 + 16 * TT < n;
-          const int npair = same ? pair : pair + 1 < tiles.count ? pair + 1 : 0, ng0 = same ? g0 + WV * NG : 0;
 #pragma unroll
-          for (int i = 0; i < NG; ++i) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const typename Op::Weight wq(buf[i].w[q]);
-              const float d = half_lo(buf[i].dz[q]), z = half_lo(buf[i].dz[q] >> 16);
-#pragma unroll
-              for (int t = 0; t < TT; ++t) {
-                if (t > 0 && t0 + 16 * t >= n) break;
-                const f32x4 v = x[t][i].template sum<INNER>(wq, z, sx[t][i]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tot[t][q][k] = fmaf(d, v[k], tot[t][q][k]);
+          for (int u = 0; u < PC; ++u) {
+            if (u > 0 && u >= pairs) break;
+            // the step after this one: the next pair, the next groups, the next pairs, the next tokens
+            int npair = p0 + u + 1, ng0 = g0;
+            bool more = true;
+            if (u + 1 >= pairs) {
+              npair = p0, ng0 = g0 + WV * NG;
+              if (ng0 >= G) {
+                npair = p0 + PC, ng0 = 0;
+                if (npair >= tiles.count) npair = 0, more = t0 + 16 < n;
               }
             }
-            if (same || more) fetch(i, npair, ng0);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const typename Op::Weight wq(buf[i].w[q]);
+                const float d = half_lo(buf[i].dz[q]), z = half_lo(buf[i].dz[q] >> 16);
+                const f32x4 v = x[i].template sum<INNER>(wq, z, sx[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tot[u][q][k] = fmaf(d, v[k], tot[u][q][k]);
+              }
+              if (more) fetch(i, npair, ng0);
+            }
           }
         }
 #pragma unroll
-        for (int t = 0; t < TT; ++t, turn ^= 1) {
-          if (t > 0 && t0 + 16 * t >= n) break;
+        for (int u = 0; u < PC; ++u) {
+          if (u > 0 && u >= pairs) break;
+          const int64_t first = (tiles.first + (int64_t)(p0 + u) * tiles.step) * 16 + (threadIdx.x & 15);
+          const float power0 = w.powers[first], power1 = w.powers[first + 16 * tiles.other];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (t0 + 16 * t + 4 * j + k < n) {
-              part[turn][wave][(4 * j + k) * 16 + c] = tot[t][0][k];
-              part[turn][wave][256 + (4 * j + k) * 16 + c] = tot[t][1][k];
+            if (t0 + 4 * j + k < n) {
+              part[turn][wave][(4 * j + k) * 16 + c] = tot[u][0][k];
+              part[turn][wave][256 + (4 * j + k) * 16 + c] = tot[u][1][k];
             }
           }
           __syncthreads();  // and the buffer of two turns ago has been read
-          const int o = (int)threadIdx.x, at = t0 + 16 * t + o / 16;
+          const int o = (int)threadIdx.x, at = t0 + o / 16;
           if (o < 256 && at < n) {
             float a = 0.0f, b = 0.0f;
 #pragma unroll
             for (int v = 0; v < WV; ++v) a += part[turn][v][o], b += part[turn][v][256 + o];
-            out(at, pair, o % 16, a * power0, b * power1);
+            out(at, p0 + u, o % 16, a * power0, b * power1);
           }
+          turn ^= 1;
         }
       }
     }
@@ -486,8 +482,8 @@ __device__ __forceinline__ void store_h(const MoeArgs& p, int64_t plane, int pai
 // act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
 // ROUTE: from the router's logits, for a token a wave; every block makes the routing for itself, and one writes it for the
 // kernels behind (4 tokens, 8 of 128 experts: the layer takes ... us, 35.5 with the router in a kernel of its own).
-template <int XT, int TT, int NG, int WV, bool INNER, bool ROUTE>
-__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * TT * NG)) void moe_up_kernel(
+template <int XT, int NG, int WV, bool INNER, bool ROUTE>
+__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * NG)) void moe_up_kernel(
     const MoeArgs p, const RouteArgs r, bool lbf16, int per) {
   __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
@@ -513,7 +509,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>:
   const int e = slot_expert(p, ids, slot);
   if (e < 0) return;
   const int tile0 = (int)blockIdx.x * per, left = p.I / 16 - tile0;
-  ExpertPass<XT, TT, NG, WV, INNER> pass;
+  ExpertPass<XT, NG, WV, 1, INNER> pass;
   pass.w = p.up;
   pass.tiles = Tiles{(int64_t)e * (p.I / 8) + tile0, p.I / 16, 1, left < per ? left : per};
   pass.G = p.H / kGroup, pass.lane = lane, pass.wave = wave;
@@ -537,8 +533,8 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>:
 }
 
 // w D (...) of every pair.  A block: a slot, `per` pairs of tiles of sixteen channels of H.
-template <int T, int TT, int NG, int WV>
-__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)) void moe_down_kernel(const MoeArgs p, int per) {
+template <int T, int NG, int WV, int PC>
+__global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * NG)) void moe_down_kernel(const MoeArgs p, int per) {
   __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
   __shared__ int counts[WV];
@@ -546,7 +542,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * TT * NG)
   const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, p.ids, slot);
   if (e < 0) return;
   const int pair0 = (int)blockIdx.x * per, left = p.H / 32 - pair0;
-  ExpertPass<T == 2 ? kPlanes2 : kPlanes3, TT, NG, WV, T == 3> pass;
+  ExpertPass<T == 2 ? kPlanes2 : kPlanes3, NG, WV, PC, T == 3> pass;
   pass.w = p.down;
   pass.tiles = Tiles{(int64_t)e * (p.H / 16) + 2 * pair0, 1, 2, left < per ? left : per};
   pass.G = p.I / kGroup, pass.lane = lane, pass.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -780,8 +776,8 @@ template <int XT, int NG, int WV, bool INNER>
 void up_with(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
   const int per = units_per_block((int)slots, a.I / 16, WV * 4 / waves_per_simd(sizeof(typename Source<XT>::Operand) * NG));
   const dim3 grid((unsigned)((a.I / 16 + per - 1) / per), slots);
-  if (r != nullptr) moe_up_kernel<XT, 1, NG, WV, INNER, true><<<grid, 64 * WV, 0, st>>>(a, *r, l_type == kBf16, per);
-  else moe_up_kernel<XT, 1, NG, WV, INNER, false><<<grid, 64 * WV, 0, st>>>(a, RouteArgs{}, false, per);
+  if (r != nullptr) moe_up_kernel<XT, NG, WV, INNER, true><<<grid, 64 * WV, 0, st>>>(a, *r, l_type == kBf16, per);
+  else moe_up_kernel<XT, NG, WV, INNER, false><<<grid, 64 * WV, 0, st>>>(a, RouteArgs{}, false, per);
 }
 template <int XT, bool INNER>
 void launch_up(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
@@ -791,15 +787,16 @@ void launch_up(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots,
   else up_with<XT, XT == kF32 ? 1 : 2, 16, INNER>(a, r, l_type, slots, st);
 }
 
-template <int T, int TT, int NG, int WV>
+template <int T, int NG, int WV, int PC>
 void down_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
   const int per = units_per_block((int)slots, a.H / 32, WV * 4 / waves_per_simd(sizeof(Terms<T>) * NG));
-  moe_down_kernel<T, TT, NG, WV><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
+  moe_down_kernel<T, NG, WV, PC><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
 }
 template <int T>
 void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
-  if (a.I / kGroup <= 8) down_with<T, 1, 1, 8>(a, slots, st);
-  else down_with<T, 1, 1, 16>(a, slots, st);
+  if (a.I / kGroup <= 8) down_with<T, 1, 8, 1>(a, slots, st);
+  else if (a.I / kGroup <= 16) down_with<T, 1, 16, 1>(a, slots, st);
+  else down_with<T, 1, 16, 2>(a, slots, st);
 }
 
 // Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
