@@ -161,12 +161,6 @@ template <int T>
 struct Terms {
   using Weight = W16;
   bf16x8 t[T][4];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < T; ++k)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) t[k][s] = constant8(0u);
-  }
   // sum x of the group, for the zero points
   __device__ __forceinline__ f32x4 ones() const {
     const bf16x8 one = constant8(0x3f803f80u);
@@ -207,7 +201,6 @@ struct Terms {
 struct Codes {
   using Weight = W8;
   i32x4 b[2];
-  __device__ __forceinline__ void clear() { b[0] = b[1] = (i32x4){0, 0, 0, 0}; }
   // |sum| is below 2^18: its fp32 form is exact
   __device__ __forceinline__ static f32x4 dot(const i32x4 (&x)[2], const i32x4 (&w)[2]) {
     i32x4 r = {0, 0, 0, 0};
@@ -366,8 +359,8 @@ struct ExpertPass {
   int G, wave, lane;
 
   __device__ __forceinline__ void fetch(int i, int pair, int g0) {
-    int g = g0 + wave + i * WV;
-    g = g < G ? g : G - 1;  // past the last: loaded, with operands of zero
+    const int g = g0 + wave + i * WV;
+    if (g >= G) return;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int64_t at = (tiles.first + (int64_t)pair * tiles.step + q * tiles.other) * G + g;
@@ -402,11 +395,11 @@ struct ExpertPass {
             for (int i = 0; i < NG; ++i) {
               const int g = g0 + wave + i * WV;
               if (g < G) S::load(x[i], r, g, plane);
-              else x[i].clear();
             }
             if constexpr (!INNER) {
 #pragma unroll
-              for (int i = 0; i < NG; ++i) sx[i] = x[i].ones();
+              for (int i = 0; i < NG; ++i)
+                if (g0 + wave + i * WV < G) sx[i] = x[i].ones();
             }
           }
 #pragma unroll
@@ -424,6 +417,10 @@ struct ExpertPass {
             }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
+              if (g0 + wave + i * WV >= G) {  // none of this wave's here: only what comes next
+                if (more) fetch(i, npair, ng0);
+                continue;
+              }
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const typename Op::Weight wq(buf[i].w[q]);
