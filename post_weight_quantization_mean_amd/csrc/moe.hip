@@ -1,9 +1,9 @@
 // Mixture of experts over packed 4-bit weights, for the tokens of a decode batch or a short prompt:
 //   Y[m] = sum_j w[m, j] D_e (act(G_e x[m]) * (U_e x[m])),  e = ids[m, j]
-// The up kernel forms act(gate) * up of every (token, expert) pair; a block belongs to one expert and a run of its channels,
-// keeps the expert's tokens as operands in registers and streams its part of the weight past them.  Which tokens those are
-// it finds itself, by a scan of the ids.  For few tokens the down kernel then takes all experts of some channels of Y in one
-// block and adds them up on chip; for more tokens it works like the up kernel, and a third kernel adds a token's pairs.
+// The up kernel forms act(gate) * up of every (token, expert) pair, the down kernel its product with D_e times w, and a third
+// kernel adds a token's pairs in order.  In the first two a block belongs to one expert and a run of its channels, keeps the
+// expert's tokens as operands in registers and streams its part of the weight past them; experts with many tokens take
+// them from LDS, 64 at a time.  Which tokens those are a block finds itself, by a scan of the ids.
 //
 // A weight code becomes a bf16 operand exactly, as 16 + q (a nibble moved into the mantissa of 16.0: one instruction per
 // code and no conversion).  A group's sum x (q - z) is sum x (16 + q) - (16 + z) sum x in fp32 sums of exact products, then
@@ -171,9 +171,10 @@ struct Terms {
       for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], one, r, 0, 0, 0);
     return r;
   }
-  // sum x (q - z).  INNER: every 32 products with 16 + q are followed by 32 with -(16 + z), so that no sum grows past those 32
-  // (a sum of 128 rounds at 24 sqrt(128) sigma for a result of 6 sqrt(128) sigma); z is a whole number.  For an fp32
-  // result: 512 -> 512 -> 512, error 1.1e-6 of its norm without.
+  // sum x (q - z).  INNER: every 32 products with 16 + q are followed by 32 with -(16 + z), so that no sum grows past those
+  // 32 (a sum of 128 rounds at 24 sqrt(128) sigma for a result of 6 sqrt(128) sigma); z is a whole number.  For an fp32
+  // result, whose error was up to 1.3e-6 of its norm without (20 tokens, 129 experts of 768 x 512); a bf16 result rounds a
+  // thousand times that, and takes the half of the products.
   template <bool INNER>
   __device__ __forceinline__ f32x4 sum(const W16& w, float z, const f32x4 sx) const {
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -478,7 +479,7 @@ __device__ __forceinline__ void store_h(const MoeArgs& p, int64_t plane, int pai
 
 // act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
 // ROUTE: from the router's logits, for a token a wave; every block makes the routing for itself, and one writes it for the
-// kernels behind (4 tokens, 8 of 128 experts: the layer takes ... us, 35.5 with the router in a kernel of its own).
+// kernels behind (4 tokens, 8 of 128 experts: the layer takes 32.4 us, 35.5 with the router in a kernel of its own).
 template <int XT, int NG, int WV, bool INNER, bool ROUTE>
 __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * NG)) void moe_up_kernel(
     const MoeArgs p, const RouteArgs r, bool lbf16, int per) {
@@ -796,6 +797,10 @@ void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
   else down_with<T, 1, 16, 2>(a, slots, st);
 }
 
+// More than ten tokens an expert run in tiles of 64 (32), fewer stream past sixteen at a time.  us, stream / tiles: 64
+// experts, 6 tokens each 79 / 93, 12 98 / 85, 16 103 / 90, 31 158 / 118; 8 experts of 4096 x 14336, 8 tokens 168 / 233.
+bool in_tiles(int64_t M, int k, int E) { return M * k > 10 * E; }
+
 // Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
 unsigned tile_depth(const MoeArgs& a, int tokens) {
   const int depth = a.M * a.k * 3 / (2 * a.E * tokens) + 1;
@@ -813,16 +818,14 @@ void down_tiles(const MoeArgs& a, hipStream_t st) {
 
 template <int XT, bool INNER>
 void launch_products(const MoeArgs& a, const RouteArgs* r, int l_type, hipStream_t st) {
-  const int P = a.M * a.k;
-  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
-  if (P > 12 * a.E) up_tiles<XT, XT == kF32 ? 2 : 4, INNER>(a, st);
+  const unsigned slots = (unsigned)(a.by_pair ? a.M * a.k : a.E);
+  if (in_tiles(a.M, a.k, a.E)) up_tiles<XT, XT == kF32 ? 2 : 4, INNER>(a, st);
   else launch_up<XT, INNER>(a, r, l_type, slots, st);
 }
 template <int T>
 void launch_sums(const MoeArgs& a, hipStream_t st) {
-  const int P = a.M * a.k;
-  const unsigned slots = (unsigned)(a.by_pair ? P : a.E);
-  if (P > 12 * a.E) down_tiles<T, T == 2 ? 4 : 2>(a, st);
+  const unsigned slots = (unsigned)(a.by_pair ? a.M * a.k : a.E);
+  if (in_tiles(a.M, a.k, a.E)) down_tiles<T, T == 2 ? 4 : 2>(a, st);
   else launch_down<T>(a, slots, st);
   moe_sum_kernel<<<dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.M), 256, 0, st>>>(a);
 }
@@ -854,7 +857,7 @@ hipError_t launch_moe_route(const RouteArgs& a, int l_type, hipStream_t st) {
 }
 
 // Up to eight tokens (a wave of the smallest block each) that do not run in tiles, and few enough experts.
-bool moe_routes(int64_t M, int k, int E) { return M <= 8 && E <= kRouteHere && M * k <= 12 * E; }
+bool moe_routes(int64_t M, int k, int E) { return M <= 8 && E <= kRouteHere && !in_tiles(M, k, E); }
 
 hipError_t launch_moe(const MoeArgs& a, const RouteArgs* r, int l_type, int x_type, hipStream_t st) {
   switch (x_type) {
