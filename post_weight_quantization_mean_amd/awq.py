@@ -703,7 +703,8 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", renormali
 def moe_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor, group_size: int = GROUP, *,
                out: Optional[torch.Tensor] = None) -> MoEWeight:
     """The artefacts of ``pack`` of E experts (qweight int32 [E, N, K/8], scales and zeros fp16 [E, N, K/128], N a multiple
-    of 16) laid out for ``moe``, once per layer.  For the gate/up weight N = 2 I: gate rows, then up rows.  ``out``: uint8
+    of 16, zero points whole numbers as ``pack`` writes them) laid out for ``moe``, once per layer.  For the gate/up weight
+    N = 2 I: gate rows, then up rows.  ``out``: uint8
     of at least ``w4a8_weight_bytes(E * N, K)``, 256-byte aligned."""
     if qweight.dim() != 3 or not qweight.is_contiguous():
         raise ValueError("qweight must be a contiguous int32 [E, N, K/8] device tensor")
