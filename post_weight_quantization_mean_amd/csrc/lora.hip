@@ -296,12 +296,16 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs p, int part
   });
 }
 
-// The same for prompts: sixteen tokens and 512 channels a block, whose eight waves lay their products out in LDS, so that
-// base and Y go by in whole runs of a row (4096 x 4096 -> 14336 with both kernels: 81 us; each lane with its sixteen channels
-// 89; 1024 channels a block 89).  All of base is requested before anything else.  N is a multiple of a run's 16 bytes, the rows start at multiples of them.
+// The same for prompts: sixteen tokens and 512 or 1024 channels a block, whose eight waves lay their products out in LDS, so
+// that base and Y go by in whole runs of a row.  All of base is requested before anything else.  N is a multiple of a unit of
+// 16 bytes, the rows start at multiples of them.  Two runs of 64 channels a wave where the registers leave two blocks on a
+// CU.  us, both kernels, one run / two: 4096 x 4096 -> 14336 bf16, rank 16, 75 / 70; 777 x 5120 -> 11008 fp32, rank 32,
+// 36 / 39; without LDS, each lane with its sixteen channels, 89 and 40.
+constexpr int up_runs(bool bf16, int held) { return bf16 && held == 1 ? 2 : 1; }
+
 template <int T, bool YB, int HELD>
 __global__ __launch_bounds__(512) void lora_up_rows_kernel(const LoraArgs p) {
-  constexpr int C = 512, kSize = YB ? 2 : 4, kUnit = 16 / kSize;  // channels of a block, of 16 bytes
+  constexpr int RUNS = up_runs(YB, HELD), C = 512 * RUNS, kSize = YB ? 2 : 4, kUnit = 16 / kSize;  // channels of a block, of 16 bytes
   constexpr int kTurns = 16 * C / kUnit / 512;                    // units of a thread
   static_assert(C / kUnit % 64 == 0, "a wave's units are one row's");
   constexpr int kRow = C + 4;                                     // sixteen rows' same 16 bytes: all banks
@@ -309,7 +313,7 @@ __global__ __launch_bounds__(512) void lora_up_rows_kernel(const LoraArgs p) {
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t across = (p.N + C - 1) / C;
-  const int64_t m0 = (int64_t)blockIdx.x / across * 16, b0 = (int64_t)blockIdx.x % across * C, n0 = b0 + 64 * wave;
+  const int64_t m0 = (int64_t)blockIdx.x / across * 16, b0 = (int64_t)blockIdx.x % across * C, n0 = b0 + 64 * RUNS * wave;
   u32x4 v[kTurns];
   auto place = [&](int i, int& row, int& ch) AWQ_INLINE {
     const int u = (int)threadIdx.x + 512 * i;
@@ -332,13 +336,18 @@ __global__ __launch_bounds__(512) void lora_up_rows_kernel(const LoraArgs p) {
       bf16x8 held[HELD][T];
 #pragma unroll
       for (int h = 0; h < HELD; ++h) load_t<T>(p, m, 32 * h + 8 * j, rank - 32 * h - 8 * j, mine, held[h]);
-      f32x4 acc[4];
+#pragma unroll 1
+      for (int k = 0; k < RUNS; ++k) {
+        if (n0 + 64 * k >= p.N) break;
+        f32x4 acc[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-      add_products<T, HELD>(p, a, rank, n0, m, mine, c, j, held, acc);
-      if (mine)
+        for (int q = 0; q < 4; ++q) acc[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        add_products<T, HELD>(p, a, rank, n0 + 64 * k, m, mine, c, j, held, acc);
+        if (mine)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4*>(sums + c * kRow + 64 * wave + 16 * j + 4 * q) = acc[q];
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(sums + c * kRow + 64 * (RUNS * wave + k) + 16 * j + 4 * q) = acc[q];
+      }
     });
   }
   __syncthreads();
@@ -382,8 +391,9 @@ template <int T, bool YB>
 hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
   const int64_t tiles = (a.M + 15) / 16;
   if (a.M > kParallelTokens && a.vec && a.N % (YB ? 8 : 4) == 0) {
-    const unsigned grid = (unsigned)((a.N + 511) / 512 * tiles);
-    if (a.R <= 32) lora_up_rows_kernel<T, YB, 1><<<grid, 512, 0, st>>>(a);
+    const int held = a.R <= 32 ? 1 : 2, C = 512 * up_runs(YB, held);
+    const unsigned grid = (unsigned)((a.N + C - 1) / C * tiles);
+    if (held == 1) lora_up_rows_kernel<T, YB, 1><<<grid, 512, 0, st>>>(a);
     else lora_up_rows_kernel<T, YB, 2><<<grid, 512, 0, st>>>(a);
     return hipGetLastError();
   }

@@ -49,7 +49,7 @@ def check_lora(awq, x, x64, A, B, ids, base, scale=None, ranks=None, **kw):
 # adapters in turn); K off 32 and off 128, N odd, off 64 and off 256, R of one and of several tiles of 16 and 32
 SHAPES = [(1, 8, 1, 8, 1), (1, 4096, 512, 16, 3), (2, 136, 65, 8, 2), (15, 512, 300, 24, 20), (16, 1000, 64, 40, 4),
           (17, 264, 257, 64, 40), (50, 2048, 777, 16, 7), (130, 96, 128, 256, 5), (257, 256, 320, 16, 3),
-          (300, 520, 131, 48, 6), (400, 128, 96, 72, 9), (513, 64, 70, 32, 1)]
+          (300, 520, 131, 48, 6), (400, 128, 96, 72, 9), (513, 64, 70, 32, 1), (260, 64, 2104, 16, 3), (257, 72, 1160, 40, 2)]
 
 
 @pytest.mark.parametrize("M,K,N,R,n", SHAPES)
