@@ -301,26 +301,37 @@ template <>
 struct Source<kPlanes3> : Planes<3> {};
 
 // ---- the pairs of an expert ---------------------------------------------------------------------------
-// list: the pairs p < P with ids[p] = e, ascending; returns their number.  All of the block's WV waves.
+// list: the pairs p < P with ids[p] = e, ascending; returns their number.  All of the block's WV waves; the ids are all
+// requested at once (251 tokens, 8 of 64 experts: 113 us for the layer, 116 one turn after the other).
 template <int WV>
-__device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, uint16_t* list, int* counts) {
+__device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, uint16_t* list, int (*counts)[WV]) {
+  constexpr int TURNS = kMoePairs / (64 * WV);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t mask[TURNS];
+  int id[TURNS];
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    const int p = 64 * WV * i + (int)threadIdx.x;
+    id[i] = p < P ? ids[p] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    mask[i] = __ballot(id[i] == e);
+    if (lane == 0) counts[i][wave] = __popcll(mask[i]);
+  }
+  __syncthreads();
   int total = 0;
-  for (int p0 = 0; p0 < P; p0 += 64 * WV) {
-    const int p = p0 + (int)threadIdx.x;
-    const bool hit = p < P && ids[p] == e;
-    const uint64_t mask = __ballot(hit);
-    if (p0 > 0) __syncthreads();  // counts of the pass before are read
-    if (lane == 0) counts[wave] = __popcll(mask);
-    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    if (i > 0 && 64 * WV * i >= P) break;
     int before = total;
 #pragma unroll
     for (int w = 0; w < WV; ++w) {
-      const int c = counts[w];
+      const int c = counts[i][w];
       if (w < wave) before += c;
       total += c;
     }
-    if (hit) list[before + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)p;
+    if (id[i] == e) list[before + __popcll(mask[i] & ((1ull << lane) - 1))] = (uint16_t)(64 * WV * i + (int)threadIdx.x);
   }
   __syncthreads();
   return total;
@@ -485,7 +496,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>:
     const MoeArgs p, const RouteArgs r, bool lbf16, int per) {
   __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[WV];
+  __shared__ int counts[kMoePairs / (64 * WV)][WV];
   const int lane = threadIdx.x & 63, j = lane >> 4;
   __shared__ int32_t routed[ROUTE ? WV * kMaxChosen : 1];
   const int slot = (int)blockIdx.y, P = p.M * p.k, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -535,7 +546,7 @@ template <int T, int NG, int WV, int PC>
 __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * NG)) void moe_down_kernel(const MoeArgs p, int per) {
   __shared__ float part[2][WV][512];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[WV];
+  __shared__ int counts[kMoePairs / (64 * WV)][WV];
   const int lane = threadIdx.x & 63, j = lane >> 4;
   const int slot = (int)blockIdx.y, P = p.M * p.k, e = slot_expert(p, p.ids, slot);
   if (e < 0) return;
@@ -672,7 +683,7 @@ __global__ __launch_bounds__(512) void moe_up_tile_kernel(const MoeArgs p) {
   using Stage = TileStage<XT, TM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[8];
+  __shared__ int counts[kMoePairs / 512][8];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = (int)blockIdx.y, P = p.M * p.k;
@@ -710,7 +721,7 @@ __global__ __launch_bounds__(512) void moe_down_tile_kernel(const MoeArgs p) {
   using Stage = TileStage<SRC, TM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * Stage::kBytes];
   __shared__ uint16_t list[kMoePairs];
-  __shared__ int counts[8];
+  __shared__ int counts[kMoePairs / 512][8];
   const int lane = threadIdx.x & 63, j = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = (int)blockIdx.y, P = p.M * p.k;
