@@ -35,7 +35,7 @@ def route(logits, k, score, renormalize):
 
 def linear(x, art):
     """x [rows, K] times one packed weight: Y, sum |x| D |q - z|, and sum |x| D (32 + q + z), which the kernel's two sums
-    (codes and zero points, each moved up by sixteen) are bounded by."""
+    (codes and zero points, each moved up by sixteen, and halved) are bounded by."""
     q = o.unpack_words(art["qweight"]).astype(np.float64)
     d, z = art["scales"].astype(np.float64), art["zeros"].astype(np.float64)
     dk, zk = np.repeat(d, 128, axis=1), np.repeat(z, 128, axis=1)

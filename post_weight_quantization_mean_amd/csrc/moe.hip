@@ -5,9 +5,9 @@
 // expert's tokens as operands in registers and streams its part of the weight past them; experts with many tokens take
 // them from LDS, 64 at a time.  Which tokens those are a block finds itself, by a scan of the ids.
 //
-// A weight code becomes a bf16 operand exactly, as 16 + q (a nibble moved into the mantissa of 16.0: one instruction per
-// code and no conversion).  A group's sum x (q - z) is sum x (16 + q) - (16 + z) sum x in fp32 sums of exact products, then
-// multiplied with the group's step in fp32.  int8 activations take the integer products instead, whose sums are exact.
+// A weight code becomes a bf16 operand exactly, as 8 + q / 2 (a nibble moved into the mantissa of 8.0: one instruction per
+// code and no conversion).  A group's sum x (q - z) / 2 is sum x (8 + q / 2) - (8 + z / 2) sum x in fp32 sums of exact
+// products, then multiplied with the group's step in fp32.  int8 activations take the integer products instead, whose sums are exact.
 #include "moe_internal.h"
 #include "x_operand.h"
 
@@ -131,12 +131,12 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const RouteArgs p, bool 
 // The weight's layout gives lane l, of channel l % 16, the codes of k = 16 (l / 16) .. + 15 and 64 further on; step s of
 // four takes eight of them, of both operands.
 struct W16 {
-  bf16x8 h[4];  // 16 + q
+  bf16x8 h[4];  // 8 + q / 2
   __device__ __forceinline__ explicit W16(const u32x4 w) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const uint32_t lo = (w[s] << 3 & 0x78787878u) | 0x80808080u, hi = (w[s] >> 1 & 0x78787878u) | 0x80808080u;
-      constexpr uint32_t k41 = 0x41414141u;  // the upper bytes of 16.0 .. 31.0 in bf16
+      const uint32_t lo = w[s] << 3 & 0x78787878u, hi = w[s] >> 1 & 0x78787878u;
+      constexpr uint32_t k41 = 0x41414141u;  // the upper bytes of 8.0 .. 15.5 in bf16
       h[s] = __builtin_bit_cast(bf16x8, (u32x4){__builtin_amdgcn_perm(lo, k41, 0x00050004), __builtin_amdgcn_perm(lo, k41, 0x00070006),
                                                 __builtin_amdgcn_perm(hi, k41, 0x00050004), __builtin_amdgcn_perm(hi, k41, 0x00070006)});
     }
@@ -160,6 +160,7 @@ __device__ __forceinline__ bf16x8 constant8(uint32_t two) { return __builtin_bit
 template <int T>
 struct Terms {
   using Weight = W16;
+  static constexpr float kUnit = 2.0f;  // of sum()
   bf16x8 t[T][4];
   // sum x of the group, for the zero points
   __device__ __forceinline__ f32x4 ones() const {
@@ -171,15 +172,16 @@ struct Terms {
       for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], one, r, 0, 0, 0);
     return r;
   }
-  // sum x (q - z).  INNER: every 32 products with 16 + q are followed by 32 with -(16 + z), so that no sum grows past those
-  // 32 (a sum of 128 rounds at 24 sqrt(128) sigma for a result of 6 sqrt(128) sigma); z is a whole number.  For an fp32
+  // sum x (q - z) / 2.  INNER: every 32 products with 8 + q / 2 are followed by 32 with -(8 + z / 2), so that no sum grows past
+  // those 32 (a sum of 128 rounds at 12 sqrt(128) sigma for a result of 3 sqrt(128) sigma); z is a whole number.  For an fp32
   // result, whose error was up to 1.3e-6 of its norm without (20 tokens, 129 experts of 768 x 512); a bf16 result rounds a
   // thousand times that, and takes the half of the products.
   template <bool INNER>
   __device__ __forceinline__ f32x4 sum(const W16& w, float z, const f32x4 sx) const {
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (INNER) {
-      const bf16x8 mz = constant8(pack_cut(-16.0f - z, -16.0f - z));
+      const float m = fmaf(z, -0.5f, -8.0f);
+      const bf16x8 mz = constant8(pack_cut(m, m));
 #pragma unroll
       for (int k = T - 1; k >= 0; --k)
 #pragma unroll
@@ -194,13 +196,14 @@ struct Terms {
 #pragma unroll
         for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], w.h[s], r, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = fmaf(-16.0f - z, sx[i], r[i]);
+      for (int i = 0; i < 4; ++i) r[i] = fmaf(fmaf(z, -0.5f, -8.0f), sx[i], r[i]);
       return r;
     }
   }
 };
 struct Codes {
   using Weight = W8;
+  static constexpr float kUnit = 1.0f;
   i32x4 b[2];
   // |sum| is below 2^18: its fp32 form is exact
   __device__ __forceinline__ static f32x4 dot(const i32x4 (&x)[2], const i32x4 (&w)[2]) {
@@ -449,7 +452,7 @@ struct ExpertPass {
         for (int u = 0; u < PC; ++u) {
           if (u > 0 && u >= pairs) break;
           const int64_t first = (tiles.first + (int64_t)(p0 + u) * tiles.step) * 16 + (threadIdx.x & 15);
-          const float power0 = w.powers[first], power1 = w.powers[first + 16 * tiles.other];
+          const float power0 = Op::kUnit * w.powers[first], power1 = Op::kUnit * w.powers[first + 16 * tiles.other];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (t0 + 4 * j + k < n) {
@@ -626,11 +629,19 @@ struct TilePass {
   // tot[t][q] of tiles tile[q] over all groups; used: the token tiles that hold any token.  All eight waves.
   static __device__ __forceinline__ void run(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st, int64_t plane,
                                              char* lds, int used, int lane, f32x4 (&tot)[TM][2]) {
-    const int c = lane & 15, j = lane >> 4;
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
       for (int q = 0; q < 2; ++q) tot[t][q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    if (used <= 1) groups<1>(w, tile, G, st, plane, lds, lane, tot);
+    else if (TM == 2 || used == 2) groups<2>(w, tile, G, st, plane, lds, lane, tot);
+    else if (used == 3) groups<(TM < 3 ? TM : 3)>(w, tile, G, st, plane, lds, lane, tot);
+    else groups<TM>(w, tile, G, st, plane, lds, lane, tot);
+  }
+  template <int USED>
+  static __device__ __forceinline__ void groups(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st, int64_t plane,
+                                                char* lds, int lane, f32x4 (&tot)[TM][2]) {
+    const int c = lane & 15, j = lane >> 4;
     u32x4 codes[2];
     uint32_t dz[2];
     auto fetch = [&](int g) AWQ_INLINE {
@@ -659,9 +670,7 @@ struct TilePass {
       }
       if (g + 2 < G) st.load(g + 2, plane);
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        if (t > 0 && t >= used) break;
-        __builtin_amdgcn_sched_barrier(0);  // one token tile's operands in registers at a time
+      for (int t = 0; t < USED; ++t) {
         Op x;
         Stage::read(x, now, t, c, j);
         f32x4 sx = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -698,7 +707,8 @@ __global__ __launch_bounds__(512) void moe_up_tile_kernel(const MoeArgs p) {
     });
     f32x4 tot[TM][2];
     TilePass<XT, TM, INNER>::run(p.up, tile, p.H / kGroup, st, 0, lds, (n - t0 + 15) / 16, lane, tot);
-    const float pg = p.up.powers[tile[0] * 16 + c], pu = p.up.powers[tile[1] * 16 + c];
+    constexpr float kUnit = Source<XT>::Operand::kUnit;
+    const float pg = kUnit * p.up.powers[tile[0] * 16 + c], pu = kUnit * p.up.powers[tile[1] * 16 + c];
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
 #pragma unroll
@@ -739,7 +749,7 @@ __global__ __launch_bounds__(512) void moe_down_tile_kernel(const MoeArgs p) {
     if (tile0 >= tiles) continue;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float power = p.down.powers[tile[q] * 16 + c];
+      const float power = Terms<T>::kUnit * p.down.powers[tile[q] * 16 + c];
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
 #pragma unroll
