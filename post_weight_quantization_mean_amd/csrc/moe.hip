@@ -305,7 +305,7 @@ struct Source<kPlanes3> : Planes<3> {};
 
 // ---- the pairs of an expert ---------------------------------------------------------------------------
 // list: the pairs p < P with ids[p] = e, ascending; returns their number.  All of the block's WV waves; the ids are all
-// requested at once (251 tokens, 8 of 64 experts: 113 us for the layer, 116 one turn after the other).
+// requested at once (251 tokens, 8 of 64 experts: 3 us of the layer less than one turn after the other).
 template <int WV>
 __device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, uint16_t* list, int (*counts)[WV]) {
   constexpr int TURNS = kMoePairs / (64 * WV);
@@ -493,7 +493,7 @@ __device__ __forceinline__ void store_h(const MoeArgs& p, int64_t plane, int pai
 
 // act(gate) * up.  A block: a slot, `per` tiles of sixteen channels of I.
 // ROUTE: from the router's logits, for a token a wave; every block makes the routing for itself, and one writes it for the
-// kernels behind (4 tokens, 8 of 128 experts: the layer takes 32.4 us, 35.5 with the router in a kernel of its own).
+// kernels behind (4 tokens, 8 of 128 experts: the layer takes 30.9 us, 32.0 with the router in a kernel of its own).
 template <int XT, int NG, int WV, bool INNER, bool ROUTE>
 __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * NG)) void moe_up_kernel(
     const MoeArgs p, const RouteArgs r, bool lbf16, int per) {
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * NG)) voi
 // ---- many tokens an expert: tiles ---------------------------------------------------------------------------
 // A block of eight waves: an expert's tokens 16 TM at a time with 256 channels of the weight (up: 128 gate rows and the up
 // rows beside them), all groups one after the other.  A wave has all the tokens and two channel tiles, whose codes come
-// straight into registers a group ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing
+// straight into registers a group or two ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing
 // is summed across waves, and a code is unpacked once for 16 TM tokens.
 // Rows in LDS hold their 16-byte pieces at piece ^ swizzle(row): the reads of sixteen rows' same piece use every bank once.
 template <int SRC, int TM>
@@ -638,37 +638,50 @@ struct TilePass {
     else if (used == 3) groups<(TM < 3 ? TM : 3)>(w, tile, G, st, plane, lds, lane, tot);
     else groups<TM>(w, tile, G, st, plane, lds, lane, tot);
   }
+  // Codes are requested two groups ahead where a group is few products, one ahead where these hide the way to memory.  us, one
+  // ahead / two / as here: 16 experts of 4096 x 4096, 16 tokens each, 163 / 134 / 135; 8 of 4096 x 14336, 32 tokens each,
+  // 384 / 365 / 343; 64 of 2048 x 1024, 31 tokens each, 107 / 108 / 106.
   template <int USED>
   static __device__ __forceinline__ void groups(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st, int64_t plane,
                                                 char* lds, int lane, f32x4 (&tot)[TM][2]) {
     const int c = lane & 15, j = lane >> 4;
-    u32x4 codes[2];
-    uint32_t dz[2];
-    auto fetch = [&](int g) AWQ_INLINE {
+    constexpr int kAhead = TM == 4 && USED <= 2 ? 2 : 1;
+    u32x4 codes[kAhead][2];
+    uint32_t dz[kAhead][2];
+    auto fetch = [&](auto parity, int g) AWQ_INLINE {
+      constexpr int C = decltype(parity)::value % kAhead;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        codes[q] = *(reinterpret_cast<const u32x4*>(w.codes + (tile[q] * G + g) * 256) + (unsigned)lane);
-        dz[q] = (w.steps + (tile[q] * G + g) * 16)[(unsigned)c];
+        codes[C][q] = *(reinterpret_cast<const u32x4*>(w.codes + (tile[q] * G + g) * 256) + (unsigned)lane);
+        dz[C][q] = (w.steps + (tile[q] * G + g) * 16)[(unsigned)c];
       }
     };
-    fetch(0);
+    constexpr std::integral_constant<int, 0> even;
+    constexpr std::integral_constant<int, 1> odd;
+    fetch(even, 0);
     st.load(0, plane);
     __syncthreads();  // the stages have been read
     st.store(lds);
-    if (G > 1) st.load(1, plane);
+    if (G > 1) {
+      if constexpr (kAhead == 2) fetch(odd, 1);
+      st.load(1, plane);
+    }
     __syncthreads();
-#pragma unroll 1
-    for (int g = 0; g < G; ++g) {
-      const char* now = lds + (g & 1) * Stage::kBytes;
-      const typename Op::Weight op[2] = {typename Op::Weight(codes[0]), typename Op::Weight(codes[1])};
+    auto group = [&](auto parity, int g) AWQ_INLINE {
+      constexpr int P = decltype(parity)::value, C = P % kAhead;
+      const char* now = lds + P * Stage::kBytes;
+      const typename Op::Weight op[2] = {typename Op::Weight(codes[C][0]), typename Op::Weight(codes[C][1])};
       float d[2], z[2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) d[q] = half_lo(dz[q]), z[q] = half_lo(dz[q] >> 16);
+      for (int q = 0; q < 2; ++q) d[q] = half_lo(dz[C][q]), z[q] = half_lo(dz[C][q] >> 16);
       if (g + 1 < G) {
-        fetch(g + 1);
-        st.store(lds + (g + 1 & 1) * Stage::kBytes);
+        if constexpr (kAhead == 1) fetch(parity, g + 1);
+        st.store(lds + (1 - P) * Stage::kBytes);
       }
-      if (g + 2 < G) st.load(g + 2, plane);
+      if (g + 2 < G) {
+        if constexpr (kAhead == 2) fetch(parity, g + 2);
+        st.load(g + 2, plane);
+      }
 #pragma unroll
       for (int t = 0; t < USED; ++t) {
         Op x;
@@ -683,6 +696,11 @@ struct TilePass {
         }
       }
       __syncthreads();
+    };
+#pragma unroll 1
+    for (int g = 0; g < G; g += 2) {
+      group(even, g);
+      if (g + 1 < G) group(odd, g + 1);
     }
   }
 };
@@ -783,8 +801,8 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
 }
 
 // Units of a block's run: blocks for one round of the card's CUs, `waves` being a sixteenth of a CU each: about 512 of eight
-// waves where two share a CU, 256 otherwise.  (37 fp32 tokens, 16 experts of 1280 x 896: 27.9 us, 33.1 in two rounds; 4 tokens,
-// 8 of 128 experts, 32.4, with twice the blocks 39.2.)
+// waves where two share a CU, 256 otherwise.  (37 fp32 tokens, 16 experts of 1280 x 896: 26.8 us, 31.4 in two rounds; 4 tokens,
+// 8 of 128 experts, 30.9, with twice the blocks 37.3.)
 int units_per_block(int slots, int units, int waves) {
   const int total = 4096 / waves, blocks = (total + slots - 1) / slots;
   const int per = (units + blocks - 1) / blocks;
@@ -818,9 +836,11 @@ void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
   else down_with<T, 1, 16, 2>(a, slots, st);
 }
 
-// More than ten tokens an expert run in tiles of 64 (32), fewer stream past sixteen at a time.  us, stream / tiles: 64
-// experts, 6 tokens each 79 / 93, 12 98 / 85, 16 103 / 90, 31 158 / 118; 8 experts of 4096 x 14336, 8 tokens 168 / 233.
-bool in_tiles(int64_t M, int k, int E) { return M * k > 10 * E; }
+// Ten tokens an expert and more run in tiles of 64 (32), fewer stream past sixteen at a time: from there on some expert has
+// more than sixteen.  us, stream / tiles: 64 experts of 2048 x 1024, 8 tokens each 58 / 71, 10 87 / 76, 12 99 / 82, 16 103 /
+// 85, 31 157 / 103; 16 of 4096 x 4096, 8 104 / 119, 12 142 / 121; 8 of 4096 x 14336, 8 167 / 237, 12 229 / 268, 16 297 / 297;
+// 16 of 1280 x 896 in fp32, too few tiles for the card, 9 27 / 34, 12 26 / 32; 16 of 4096 x 4096 in fp32, 16 573 / 227.
+bool in_tiles(int64_t M, int k, int E) { return M * k >= 10 * E; }
 
 // Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
 unsigned tile_depth(const MoeArgs& a, int tokens) {
