@@ -29,7 +29,7 @@ extern "C" {
  *   base   [M, N] of y_dtype, row stride ldb
  *   Y      [M, N] of y_dtype (F32, BF16), row stride ldy; may be base itself (ldy = ldb)
  *   ws     device memory of at least awq_lora_workspace_bytes bytes, 16-byte aligned; nothing in it has to start at
- *          zero, and calls that may run at the same time need one each
+ *          zero, one laid out for M tokens serves fewer, and calls that may run at the same time need one each
  * Products are exact in the matrix cores (an F32 X as three bf16 terms), sums fp32.  scale (A x) is formed in fp32 and
  * handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  A row's result does not
  * depend on which rows stand beside it, but for the order of the sums over K, which the sizes alone decide: equal calls

@@ -753,6 +753,6 @@ def lora(X, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, base: torch.Ten
     X [M, K] is float32, bfloat16 or an ``Act8``; A bfloat16 [adapters, R, K], B bfloat16 [adapters, N, R]; K and R multiples
     of 8, R at most 256.  ``ranks`` int32 [adapters]: the rows of A and columns of B that count (all without it); ``scale``
     fp32 [adapters].
-    ``workspace``: ``lora_workspace_bytes`` for (M, K, N, R), allocated here when not given; calls that may run at the same
-    time (two streams, two graphs) need one each."""
+    ``workspace``: ``lora_workspace_bytes`` for (M, K, N, R) or a larger M, allocated here when not given; calls that may run
+    at the same time (two streams, two graphs) need one each."""
     return _on(X[0] if isinstance(X, tuple) else X, (_a8 or _bound()).lora, X, A, B, ids, base, scale, ranks, out, workspace)

@@ -24,7 +24,12 @@ bool lora_sizes(int64_t M, int64_t K, int64_t N, int64_t R) {
 extern "C" {
 
 AWQ_API size_t awq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R) {
-  return lora_sizes(M, K, N, R) ? (size_t)(awq::lora_splits(M, K, R) * M * R * 4) : 0;
+  if (!lora_sizes(M, K, N, R)) return 0;
+  // What no batch of up to M tokens exceeds, so that one workspace serves them all: lora_splits gives at most min(16, K / 512)
+  // splits, and more than one only up to 512 blocks, of at most sixteen tokens each: splits M <= M + 511 * 16.
+  const int64_t most = K / 512 < 1 ? 1 : K / 512 < 16 ? K / 512 : 16;
+  const int64_t rows = M * most < M + 8192 ? M * most : M + 8192;
+  return (size_t)(rows * R * 4);
 }
 
 AWQ_API int awq_lora(const void* X, int x_dtype, const float* xscale, int64_t M, int64_t K, int64_t ldx, const void* A,

@@ -237,3 +237,18 @@ def test_lora_beside_the_packed_projection(awq):
                 got[i] = layer(*data[i])
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_lora_workspace_of_the_largest_batch_serves_all(awq):
+    """One workspace, laid out for the largest batch, for batches of every split of K; its guard stays as it was."""
+    rng = rng_of(7177)
+    K, N, R, n, most = 4096, 512, 48, 3, 700
+    A, B = adapters(rng, n, K, N, R)
+    need = awq.lora_workspace_bytes(most, K, N, R)
+    ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    for M in (1, 15, 64, 65, 256, 257, most):
+        x, x64 = activations(rng, M, K, BF16)
+        ids = rng.integers(-1, n, M).astype(np.int32)
+        base = torch.from_numpy(rng.standard_normal((M, N))).to(BF16).to(DEV)
+        check_lora(awq, x, x64, A, B, ids, base, workspace=ws[:need])
+        assert (ws[need:] == 0xA5).all()

@@ -131,6 +131,13 @@ def test_lora_workspace(L):
         assert ws(*bad) == 0
 
 
+@pytest.mark.parametrize("K,N,R", [(512, 100, 8), (1000, 64, 8), (4096, 14336, 16), (5120, 11008, 32), (28672, 4096, 256)])
+def test_lora_workspace_of_a_larger_batch_serves_a_smaller_one(L, K, N, R):
+    sizes = [L.awq_lora_workspace_bytes(M, K, N, R) for M in range(1, 9000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert L.awq_lora_workspace_bytes(1 << 20, K, N, R) <= ((1 << 20) + 8192) * R * 4  # no splits where the tokens fill the card
+
+
 def test_python_refuses_host_tensors_and_unknown_names():
     from post_weight_quantization_mean_amd import awq
     x, l = torch.zeros(2, 128), torch.zeros(2, 8)
