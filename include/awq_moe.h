@@ -48,11 +48,11 @@ AWQ_API int awq_moe_route(const void* logits, int l_dtype, int64_t M, int64_t E,
  *   act      AWQ_ACT_SILU or AWQ_ACT_GELU
  *   Y        [M, H] of y_dtype (F32, BF16), row stride ldy; a token without an expert here gets 0
  *   ws       device memory of at least awq_moe_workspace_bytes bytes, 256-byte aligned; nothing in it has to start at
- *            zero, and calls that may run at the same time need one each
+ *            zero, one laid out for M tokens serves fewer, and calls that may run at the same time need one each
  * H and I are multiples of 128 up to 2^20, M is at most 2^24, E 1024, k 32, 2 I E and H E 2^27 (AWQ_ERR_SHAPE; the
- * workspace's size is then 0).  Zero points are whole numbers, as awq_pack writes them.  Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms), sums fp32;
- * act(gate) * up is formed in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is
- * rounded once.  The order of the sums depends on the sizes alone: equal calls give equal bits.
+ * workspace's size is then 0).  Zero points are whole numbers, as awq_pack writes them.
+ * Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms), sums fp32; act(gate) * up is formed
+ * in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  The order of the sums depends on the sizes alone: equal calls give equal bits.
  * Y and ws overlap no input and not each other (an exact start is checked: AWQ_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_moe_workspace_bytes(int64_t M, int64_t E, int32_t k, int64_t H, int64_t I);

@@ -704,8 +704,7 @@ def moe_weight(qweight: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
                out: Optional[torch.Tensor] = None) -> MoEWeight:
     """The artefacts of ``pack`` of E experts (qweight int32 [E, N, K/8], scales and zeros fp16 [E, N, K/128], N a multiple
     of 16, zero points whole numbers as ``pack`` writes them) laid out for ``moe``, once per layer.  For the gate/up weight
-    N = 2 I: gate rows, then up rows.  ``out``: uint8
-    of at least ``w4a8_weight_bytes(E * N, K)``, 256-byte aligned."""
+    N = 2 I: gate rows, then up rows.  ``out``: uint8 of at least ``w4a8_weight_bytes(E * N, K)``, 256-byte aligned."""
     if qweight.dim() != 3 or not qweight.is_contiguous():
         raise ValueError("qweight must be a contiguous int32 [E, N, K/8] device tensor")
     E, N, K = qweight.shape[0], qweight.shape[1], qweight.shape[2] * 8
@@ -731,8 +730,8 @@ def moe(X, routing, gate_up: MoEWeight, down: MoEWeight, act: str = "silu", *, k
     X [M, H] is float32, bfloat16 or an ``Act8``, its rows 16-byte aligned; ``gate_up`` E experts of [2 I, H] and ``down``
     of [H, I], from ``moe_weight``; ``act`` "silu" or "gelu".  Y [M, H] is float32 (the default) or bfloat16, all sums in
     fp32.  Made for decode batches and short prompts; more than 2048 / k tokens run in passes that each read the weights.
-    ``workspace``: ``moe_workspace_bytes`` for (M, E, k, H, I), allocated here when not given; calls that may run at the
-    same time (two streams, two graphs) need one each."""
+    ``workspace``: ``moe_workspace_bytes`` for (M, E, k, H, I) or a larger M, allocated here when not given; calls that may run
+    at the same time (two streams, two graphs) need one each."""
     code = _ACTS.get(act)
     if code is None or code == ACT_NONE:
         raise ValueError("act must be silu or gelu")

@@ -131,6 +131,12 @@ def test_lora_workspace(L):
         assert ws(*bad) == 0
 
 
+@pytest.mark.parametrize("E,k,H,I", [(4, 1, 512, 128), (64, 8, 2048, 1024), (9, 7, 256, 384), (40, 32, 128, 128)])
+def test_moe_workspace_of_a_larger_batch_serves_a_smaller_one(L, E, k, H, I):
+    sizes = [L.awq_moe_workspace_bytes(M, E, k, H, I) for M in range(1, 5000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 @pytest.mark.parametrize("K,N,R", [(512, 100, 8), (1000, 64, 8), (4096, 14336, 16), (5120, 11008, 32), (28672, 4096, 256)])
 def test_lora_workspace_of_a_larger_batch_serves_a_smaller_one(L, K, N, R):
     sizes = [L.awq_lora_workspace_bytes(M, K, N, R) for M in range(1, 9000)]
