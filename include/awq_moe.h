@@ -5,7 +5,9 @@
  * The conventions of awq.h hold (device memory owned by the caller, argument errors returned synchronously, every call
  * asynchronous on `stream`, nothing allocated, no state kept).  Activations are F32, BF16, or I8 / E4M3 codes with a
  * scale per row (awq_a8.h).  No data-error flags: a token whose activations hold NaN or Inf, or whose row scale is NaN,
- * has a result that is not finite, and no other token's result changes.
+ * has a result that is not finite, and no other token's result changes.  Finite activations up to the largest number give
+ * a finite result where the definition's sums of magnitudes, sum |x| D |q - z|, stay inside fp32 (in channels whose largest
+ * step D is 2^-11 or more; below, that much sooner).
  */
 #ifndef AWQ_MOE_H
 #define AWQ_MOE_H
@@ -51,8 +53,11 @@ AWQ_API int awq_moe_route(const void* logits, int l_dtype, int64_t M, int64_t E,
  *            zero, one laid out for M tokens serves fewer, and calls that may run at the same time need one each
  * H and I are multiples of 128 up to 2^20, M is at most 2^24, E 1024, k 32, 2 I E and H E 2^27 (AWQ_ERR_SHAPE; the
  * workspace's size is then 0).  Zero points are whole numbers, as awq_pack writes them.
- * Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms), sums fp32; act(gate) * up is formed
- * in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  The order of the sums depends on the sizes alone: equal calls give equal bits.
+ * Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms; exact from 2^-90 up), sums fp32;
+ * act(gate) * up is formed in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly, from 2^-90 up)
+ * for F32; Y is rounded once.  I8 sums are exact in a group; the others round by the magnitude of |x| D (16 + q / 2) and
+ * |x| D (16 + z / 2), not of |x| D |q - z|: an activation with q = z takes 2^-20 of itself from the small ones in its group.
+ * The order of the sums depends on the sizes alone: equal calls give equal bits.
  * Y and ws overlap no input and not each other (an exact start is checked: AWQ_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_moe_workspace_bytes(int64_t M, int64_t E, int32_t k, int64_t H, int64_t I);

@@ -7,7 +7,10 @@
 //
 // A weight code becomes a bf16 operand exactly, as 8 + q / 2 (a nibble moved into the mantissa of 8.0: one instruction per
 // code and no conversion).  A group's sum x (q - z) / 2 is sum x (8 + q / 2) - (8 + z / 2) sum x in fp32 sums of exact
-// products, then multiplied with the group's step in fp32.  int8 activations take the integer products instead, whose sums are exact.
+// products, then multiplied with the group's step in fp32.  The operands hold 2^-20 of these values, and the channel's power of
+// two the rest: 128 products with 8 + q / 2 reach 2^11 |x|, and the layout's steps are 2^10 times the channel's largest, so that
+// an x of 3e37 took the sums out of fp32 where the result stayed inside.  Now only the result's own magnitude does, where the
+// largest step is 2^-11 or more.  int8 activations take the integer products instead, whose sums are exact.
 #include "moe_internal.h"
 #include "x_operand.h"
 
@@ -130,15 +133,17 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const RouteArgs p, bool 
 // ---- operands of a group of 128 channels -------------------------------------------------------------
 // The weight's layout gives lane l, of channel l % 16, the codes of k = 16 (l / 16) .. + 15 and 64 further on; step s of
 // four takes eight of them, of both operands.
+constexpr float kSmall = 0x1p-20f;
 struct W16 {
-  bf16x8 h[4];  // 8 + q / 2
+  bf16x8 h[4];  // 2^-20 (8 + q / 2)
   __device__ __forceinline__ explicit W16(const u32x4 w) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const uint32_t lo = w[s] << 3 & 0x78787878u, hi = w[s] >> 1 & 0x78787878u;
-      constexpr uint32_t k41 = 0x41414141u;  // the upper bytes of 8.0 .. 15.5 in bf16
-      h[s] = __builtin_bit_cast(bf16x8, (u32x4){__builtin_amdgcn_perm(lo, k41, 0x00050004), __builtin_amdgcn_perm(lo, k41, 0x00070006),
-                                                __builtin_amdgcn_perm(hi, k41, 0x00050004), __builtin_amdgcn_perm(hi, k41, 0x00070006)});
+      constexpr uint32_t kUpper = 0x37373737u;  // the upper bytes of 2^-20 times 8.0 .. 15.5 in bf16
+      h[s] = __builtin_bit_cast(
+          bf16x8, (u32x4){__builtin_amdgcn_perm(lo, kUpper, 0x00050004), __builtin_amdgcn_perm(lo, kUpper, 0x00070006),
+                          __builtin_amdgcn_perm(hi, kUpper, 0x00050004), __builtin_amdgcn_perm(hi, kUpper, 0x00070006)});
     }
   }
 };
@@ -160,11 +165,11 @@ __device__ __forceinline__ bf16x8 constant8(uint32_t two) { return __builtin_bit
 template <int T>
 struct Terms {
   using Weight = W16;
-  static constexpr float kUnit = 2.0f;  // of sum()
+  static constexpr float kUnit = 2.0f / kSmall;  // of sum()
   bf16x8 t[T][4];
-  // sum x of the group, for the zero points
+  // 2^-20 sum x of the group, for the zero points
   __device__ __forceinline__ f32x4 ones() const {
-    const bf16x8 one = constant8(0x3f803f80u);
+    const bf16x8 one = constant8(pack_cut(kSmall, kSmall));
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = T - 1; k >= 0; --k)
@@ -172,7 +177,7 @@ struct Terms {
       for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], one, r, 0, 0, 0);
     return r;
   }
-  // sum x (q - z) / 2.  INNER: every 32 products with 8 + q / 2 are followed by 32 with -(8 + z / 2), so that no sum grows past
+  // 2^-20 sum x (q - z) / 2.  INNER: every 32 products with 8 + q / 2 are followed by 32 with -(8 + z / 2), so that no sum grows past
   // those 32 (a sum of 128 rounds at 12 sqrt(128) sigma for a result of 3 sqrt(128) sigma); z is a whole number.  For an fp32
   // result, whose error was up to 1.3e-6 of its norm without (20 tokens, 129 experts of 768 x 512); a bf16 result rounds a
   // thousand times that, and takes the half of the products.
@@ -180,7 +185,7 @@ struct Terms {
   __device__ __forceinline__ f32x4 sum(const W16& w, float z, const f32x4 sx) const {
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (INNER) {
-      const float m = fmaf(z, -0.5f, -8.0f);
+      const float m = fmaf(z, -0.5f * kSmall, -8.0f * kSmall);
       const bf16x8 mz = constant8(pack_cut(m, m));
 #pragma unroll
       for (int k = T - 1; k >= 0; --k)
