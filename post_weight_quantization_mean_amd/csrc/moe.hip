@@ -12,6 +12,7 @@
 // an x of 3e37 took the sums out of fp32 where the result stayed inside.  Now only the result's own magnitude does, where the
 // largest step is 2^-11 or more.  int8 activations take the integer products instead, whose sums are exact.
 #include "moe_internal.h"
+#include "moe_plan.h"
 #include "x_operand.h"
 
 namespace awq {
@@ -805,18 +806,9 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs p) {
   }
 }
 
-// Units of a block's run: blocks for one round of the card's CUs, `waves` being a sixteenth of a CU each: about 512 of eight
-// waves where two share a CU, 256 otherwise.  (37 fp32 tokens, 16 experts of 1280 x 896: 26.8 us, 31.4 in two rounds; 4 tokens,
-// 8 of 128 experts, 30.9, with twice the blocks 37.3.)
-int units_per_block(int slots, int units, int waves) {
-  const int total = 4096 / waves, blocks = (total + slots - 1) / slots;
-  const int per = (units + blocks - 1) / blocks;
-  return per < 1 ? 1 : per;
-}
-
 template <int XT, int NG, int WV, bool INNER>
 void up_with(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots, hipStream_t st) {
-  const int per = units_per_block((int)slots, a.I / 16, WV * 4 / waves_per_simd(sizeof(typename Source<XT>::Operand) * NG));
+  const int per = units_per_block((int)slots, a.I / 16, WV, waves_per_simd(sizeof(typename Source<XT>::Operand) * NG));
   const dim3 grid((unsigned)((a.I / 16 + per - 1) / per), slots);
   if (r != nullptr) moe_up_kernel<XT, NG, WV, INNER, true><<<grid, 64 * WV, 0, st>>>(a, *r, l_type == kBf16, per);
   else moe_up_kernel<XT, NG, WV, INNER, false><<<grid, 64 * WV, 0, st>>>(a, RouteArgs{}, false, per);
@@ -831,7 +823,7 @@ void launch_up(const MoeArgs& a, const RouteArgs* r, int l_type, unsigned slots,
 
 template <int T, int NG, int WV, int PC>
 void down_with(const MoeArgs& a, unsigned slots, hipStream_t st) {
-  const int per = units_per_block((int)slots, a.H / 32, WV * 4 / waves_per_simd(sizeof(Terms<T>) * NG));
+  const int per = units_per_block((int)slots, a.H / 32, WV, waves_per_simd(sizeof(Terms<T>) * NG));
   moe_down_kernel<T, NG, WV, PC><<<dim3((unsigned)((a.H / 32 + per - 1) / per), slots), 64 * WV, 0, st>>>(a, per);
 }
 template <int T>
@@ -841,25 +833,13 @@ void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
   else down_with<T, 1, 16, 2>(a, slots, st);
 }
 
-// Ten tokens an expert and more run in tiles of 64 (32), fewer stream past sixteen at a time: from there on some expert has
-// more than sixteen.  us, stream / tiles: 64 experts of 2048 x 1024, 8 tokens each 58 / 71, 10 87 / 76, 12 99 / 82, 16 103 /
-// 85, 31 157 / 103; 16 of 4096 x 4096, 8 104 / 119, 12 142 / 121; 8 of 4096 x 14336, 8 167 / 237, 12 229 / 268, 16 297 / 297;
-// 16 of 1280 x 896 in fp32, too few tiles for the card, 9 27 / 34, 12 26 / 32; 16 of 4096 x 4096 in fp32, 16 573 / 227.
-bool in_tiles(int64_t M, int k, int E) { return M * k >= 10 * E; }
-
-// Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
-unsigned tile_depth(const MoeArgs& a, int tokens) {
-  const int depth = a.M * a.k * 3 / (2 * a.E * tokens) + 1;
-  return (unsigned)(depth < 8 ? depth : 8);
-}
-
 template <int XT, int TM, bool INNER>
 void up_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a, 16 * TM)), 512, 0, st>>>(a);
+  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM)), 512, 0, st>>>(a);
 }
 template <int T, int TM>
 void down_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a, 16 * TM)), 512, 0, st>>>(a);
+  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM)), 512, 0, st>>>(a);
 }
 
 template <int XT, bool INNER>
