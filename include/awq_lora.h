@@ -31,11 +31,11 @@ extern "C" {
  *   ws     device memory of at least awq_lora_workspace_bytes bytes, 16-byte aligned; nothing in it has to start at
  *          zero, one laid out for M tokens serves fewer, and calls that may run at the same time need one each
  * Products are exact in the matrix cores (an F32 X as three bf16 terms), sums fp32.  scale (A x) is formed in fp32 and
- * handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  A row's result does not
- * depend on which rows stand beside it, but for the order of the sums over K, which the sizes alone decide: equal calls
- * give equal bits.
- * M is below 2^24, N below 2^22, K and adapters below 2^31, ceil(M / 16) ceil(N / 256) below 2^23 (AWQ_ERR_SHAPE; the workspace's
- * size is then 0).  Apart from Y = base, Y and ws overlap no input and not each other (an exact start is
+ * handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly) for F32; Y is rounded once.  A row's result does
+ * not depend on which rows stand beside it, but for the order of the sums over K, which the sizes alone decide: equal
+ * calls give equal bits.
+ * M is below 2^24, N below 2^22, K and adapters below 2^31, ceil(M / 16) ceil(N / 256) below 2^23 (AWQ_ERR_SHAPE; the
+ * workspace's size is then 0).  Apart from Y = base, Y and ws overlap no input and not each other (an exact start is
  * checked: AWQ_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------- */
 AWQ_API size_t awq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R);

@@ -41,8 +41,8 @@ AWQ_API int awq_moe_route(const void* logits, int l_dtype, int64_t M, int64_t E,
  *   Y[m] = sum_j weights[m, j] D_e (act(G_e x[m]) * (U_e x[m])),  e = ids[m, j]
  *   X        [M, H] of x_dtype (F32, BF16, I8, E4M3), row stride ldx, 16-byte aligned rows
  *   xscale   fp32 [M] for I8 and E4M3, else ignored
- *   ids      int32 [M, k]; a value outside 0 .. E-1 is skipped (an expert that another device holds, or none); the same
- *            expert may stand more than once in a row
+ *   ids      int32 [M, k]; a value outside 0 .. E-1 is skipped (an expert that another device holds, or none), but
+ *            counts where the kernels are chosen by M k / E; the same expert may stand more than once in a row
  *   weights  fp32 [M, k]
  *   gate_up  as written by awq_w4a8_weight for N = 2 I E and K = H: expert e's gate rows from 2 I e on, its up rows I
  *            further
@@ -55,8 +55,8 @@ AWQ_API int awq_moe_route(const void* logits, int l_dtype, int64_t M, int64_t E,
  * workspace's size is then 0).  Zero points are whole numbers, as awq_pack writes them.
  * Products are exact in the matrix cores (codes, and an F32 X as three bf16 terms; exact from 2^-90 up), sums fp32;
  * act(gate) * up is formed in fp32 and handed on in two bf16 terms (2^-17) for a BF16 Y, in three (exactly, from 2^-90 up)
- * for F32; Y is rounded once.  I8 sums are exact in a group; the others round by the magnitude of |x| D (16 + q / 2) and
- * |x| D (16 + z / 2), not of |x| D |q - z|: an activation with q = z takes 2^-20 of itself from the small ones in its group.
+ * for F32; Y is rounded once.  I8 sums are exact in a group; the others are rounded by the magnitudes |x| D (16 + q) and
+ * |x| D (16 + z), not |x| D |q - z|: an activation with q = z beside small ones costs their sum up to 2^-19 D of its size.
  * The order of the sums depends on the sizes alone: equal calls give equal bits.
  * Y and ws overlap no input and not each other (an exact start is checked: AWQ_ERR_INVALID_ARG).
  * ------------------------------------------------------------------------------------- */

@@ -1,7 +1,7 @@
 // Python binding of the 8-bit activation calls (awq_a8.h), the mixture of experts (awq_moe.h) and the low-rank adapters
-// (awq_lora.h): argument marshalling only.  These calls run once per layer and token, where the checks and the output's allocation, made in Python, would take longer than
-// the kernel; the rest of the library is bound with ctypes.  The library's functions are handed in as
-// addresses (bind), so that this module does not load it.
+// (awq_lora.h): argument marshalling only.  These calls run once per layer and token, where the checks and the output's
+// allocation, made in Python, would take longer than the kernel; the rest of the library is bound with ctypes.  The
+// library's functions are handed in as addresses (bind), so that this module does not load it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -305,7 +305,8 @@ constexpr int up_runs(bool bf16, int held) { return bf16 && held == 1 ? 2 : 1; }
 
 template <int T, bool YB, int HELD>
 __global__ __launch_bounds__(512) void lora_up_rows_kernel(const LoraArgs p) {
-  constexpr int RUNS = up_runs(YB, HELD), C = 512 * RUNS, kSize = YB ? 2 : 4, kUnit = 16 / kSize;  // channels of a block, of 16 bytes
+  constexpr int RUNS = up_runs(YB, HELD), C = 512 * RUNS;         // channels of a block
+  constexpr int kSize = YB ? 2 : 4, kUnit = 16 / kSize;           // channels of 16 bytes
   constexpr int kTurns = 16 * C / kUnit / 512;                    // units of a thread
   static_assert(C / kUnit % 64 == 0, "a wave's units are one row's");
   constexpr int kRow = C + 4;                                     // sixteen rows' same 16 bytes: all banks

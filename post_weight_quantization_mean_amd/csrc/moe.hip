@@ -7,10 +7,10 @@
 //
 // A weight code becomes a bf16 operand exactly, as 8 + q / 2 (a nibble moved into the mantissa of 8.0: one instruction per
 // code and no conversion).  A group's sum x (q - z) / 2 is sum x (8 + q / 2) - (8 + z / 2) sum x in fp32 sums of exact
-// products, then multiplied with the group's step in fp32.  The operands hold 2^-20 of these values, and the channel's power of
-// two the rest: 128 products with 8 + q / 2 reach 2^11 |x|, and the layout's steps are 2^10 times the channel's largest, so that
-// an x of 3e37 took the sums out of fp32 where the result stayed inside.  Now only the result's own magnitude does, where the
-// largest step is 2^-11 or more.  int8 activations take the integer products instead, whose sums are exact.
+// products, then multiplied with the group's step in fp32.  The operands hold 2^-20 of these values and the channel's power of
+// two the rest: 128 products with 8 + q / 2 reach 2^11 |x|, and the layout's steps are scaled to 2^10 and more, so that an x
+// of 3e37 would take the sums out of fp32 where the result stays inside.  This way only the result's own magnitude does, in
+// channels whose largest step is 2^-11 or more.  int8 activations take the integer products instead, whose sums are exact.
 #include "moe_internal.h"
 #include "moe_plan.h"
 #include "x_operand.h"
@@ -178,10 +178,10 @@ struct Terms {
       for (int s = 0; s < 4; ++s) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[k][s], one, r, 0, 0, 0);
     return r;
   }
-  // 2^-20 sum x (q - z) / 2.  INNER: every 32 products with 8 + q / 2 are followed by 32 with -(8 + z / 2), so that no sum grows past
-  // those 32 (a sum of 128 rounds at 12 sqrt(128) sigma for a result of 3 sqrt(128) sigma); z is a whole number.  For an fp32
-  // result, whose error was up to 1.3e-6 of its norm without (20 tokens, 129 experts of 768 x 512); a bf16 result rounds a
-  // thousand times that, and takes the half of the products.
+  // 2^-20 sum x (q - z) / 2.  INNER: every 32 products with 8 + q / 2 are followed by 32 with -(8 + z / 2), so that no sum
+  // grows past those 32 (a sum of 128 rounds at 12 sqrt(128) sigma for a result of 3 sqrt(128) sigma); z is a whole number.
+  // For an fp32 result, whose error was up to 1.3e-6 of its norm without (20 tokens, 129 experts of 768 x 512); a bf16 result
+  // rounds a thousand times that, and takes the half of the products.
   template <bool INNER>
   __device__ __forceinline__ f32x4 sum(const W16& w, float z, const f32x4 sx) const {
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -346,7 +346,9 @@ __device__ __forceinline__ int expert_pairs(const int32_t* ids, int P, int e, ui
   return total;
 }
 
-// Waves per SIMD that a kernel is built for: four (two blocks of eight waves on a CU) where its operands leave room.
+// Waves per SIMD that a kernel is built for, by its tokens' operands: four (two blocks of eight waves on a CU) up to 128 bytes
+// of them, else two.  It bounds the registers and sizes the grid; what a kernel then needs may be less (fp32 X, one group a
+// wave: 124 registers) or just above what lets a second block in (down in three terms, one group a wave: 130).
 constexpr int waves_per_simd(size_t operands) { return operands <= 128 ? 4 : 2; }
 
 // The expert of a slot: experts, where there are at least as many pairs as experts, else the expert of the pair of that
@@ -581,8 +583,8 @@ __global__ __launch_bounds__(64 * WV, waves_per_simd(sizeof(Terms<T>) * NG)) voi
 // ---- many tokens an expert: tiles ---------------------------------------------------------------------------
 // A block of eight waves: an expert's tokens 16 TM at a time with 256 channels of the weight (up: 128 gate rows and the up
 // rows beside them), all groups one after the other.  A wave has all the tokens and two channel tiles, whose codes come
-// straight into registers a group or two ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.  Nothing
-// is summed across waves, and a code is unpacked once for 16 TM tokens.
+// straight into registers a group or two ahead; the tokens come into LDS, two groups in turn, requested two groups ahead.
+// Nothing is summed across waves, and a code is unpacked once for 16 TM tokens.
 // Rows in LDS hold their 16-byte pieces at piece ^ swizzle(row): the reads of sixteen rows' same piece use every bank once.
 template <int SRC, int TM>
 struct TileStage {
@@ -648,8 +650,8 @@ struct TilePass {
   // ahead / two / as here: 16 experts of 4096 x 4096, 16 tokens each, 163 / 134 / 135; 8 of 4096 x 14336, 32 tokens each,
   // 384 / 365 / 343; 64 of 2048 x 1024, 31 tokens each, 107 / 108 / 106.
   template <int USED>
-  static __device__ __forceinline__ void groups(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st, int64_t plane,
-                                                char* lds, int lane, f32x4 (&tot)[TM][2]) {
+  static __device__ __forceinline__ void groups(const ExpertWeights& w, const int64_t (&tile)[2], int G, Stage& st,
+                                                int64_t plane, char* lds, int lane, f32x4 (&tot)[TM][2]) {
     const int c = lane & 15, j = lane >> 4;
     constexpr int kAhead = TM == 4 && USED <= 2 ? 2 : 1;
     u32x4 codes[kAhead][2];
@@ -835,11 +837,13 @@ void launch_down(const MoeArgs& a, unsigned slots, hipStream_t st) {
 
 template <int XT, int TM, bool INNER>
 void up_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_up_tile_kernel<XT, TM, INNER><<<dim3((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM)), 512, 0, st>>>(a);
+  const dim3 grid((unsigned)(a.I / 128), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM));
+  moe_up_tile_kernel<XT, TM, INNER><<<grid, 512, 0, st>>>(a);
 }
 template <int T, int TM>
 void down_tiles(const MoeArgs& a, hipStream_t st) {
-  moe_down_tile_kernel<T, TM><<<dim3((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM)), 512, 0, st>>>(a);
+  const dim3 grid((unsigned)((a.H + 255) / 256), (unsigned)a.E, tile_depth(a.M, a.k, a.E, 16 * TM));
+  moe_down_tile_kernel<T, TM><<<grid, 512, 0, st>>>(a);
 }
 
 template <int XT, bool INNER>

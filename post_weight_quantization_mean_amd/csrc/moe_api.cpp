@@ -11,6 +11,8 @@ namespace {
 
 using namespace awq::api;
 
+static_assert(awq::kSoftmax == AWQ_MOE_SOFTMAX && awq::kSigmoid == AWQ_MOE_SIGMOID, "the ABI's scores");
+
 // A launch takes fewer than 2^32 threads: 64 per token (router); a quarter per result of 2048 pairs (sum).
 constexpr int64_t kMaxTokens = 1 << 24, kMaxWidth = 1 << 20;
 

@@ -5,11 +5,14 @@
 
 namespace awq {
 
-// Ten tokens an expert and more run in tiles of 64 (32), fewer stream past sixteen at a time: from there on some expert has
-// more than sixteen.  us, stream / tiles: 64 experts of 2048 x 1024, 8 tokens each 58 / 71, 10 87 / 76, 12 99 / 82, 16 103 /
-// 85, 31 157 / 103; 16 of 4096 x 4096, 8 104 / 119, 12 142 / 121; 8 of 4096 x 14336, 8 167 / 237, 12 229 / 268, 16 297 / 297;
-// in fp32 (X and Y) 64 of 2048 x 2048, 8 149 / 174, 10 258 / 208; 16 of 4096 x 4096, 8 217 / 167, 10 290 / 191, 16 381 / 265;
-// 16 of 1280 x 896, too few tiles for the card, 9 28 / 35, 12 29 / 35.
+// Ten tokens an expert and more run in tiles of 64 (32), fewer stream past sixteen at a time: from there on, with experts
+// chosen evenly, some expert has more than sixteen.  us, stream / tiles: 64 experts of 2048 x 1024, 8 tokens each 58 / 71, 10
+// 87 / 76, 12 99 / 82, 16 103 / 85, 31 157 / 103; 16 of 4096 x 4096, 8 104 / 119, 12 142 / 121; 8 of 4096 x 14336, 8 167 /
+// 237, 12 229 / 268, 16 297 / 297; in fp32 (X and Y) 64 of 2048 x 2048, 8 149 / 174, 10 258 / 208; 16 of 4096 x 4096, 8 217 /
+// 167, 10 290 / 191, 16 381 / 265; 16 of 1280 x 896, too few tiles for the card, 9 28 / 35, 12 29 / 35.
+// All M k pairs count, also those whose expert is on another device, which the host cannot tell: with an eighth of the
+// experts here tiles begin at one or two tokens for each of them (8 of 64 experts of 2048 x 1024, k 8: 8 tokens stream in 21,
+// 10 take 28 in tiles).
 inline bool in_tiles(int64_t M, int k, int E) { return M * k >= 10 * E; }
 
 // Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
