@@ -12,7 +12,8 @@ namespace awq {
 // 167, 10 290 / 191, 16 381 / 265; 16 of 1280 x 896, too few tiles for the card, 9 28 / 35, 12 29 / 35.
 // All M k pairs count, also those whose expert is on another device, which the host cannot tell: with an eighth of the
 // experts here tiles begin at one or two tokens for each of them (8 of 64 experts of 2048 x 1024, k 8: 8 tokens stream in 21,
-// 10 take 28 in tiles).
+// 10 take 28 in tiles).  Nor does the rule ask whether the tiles fill the card: few small experts would stream faster also
+// beyond (4 of 2048 x 1024, 10 tokens each 15 / 30, 32 each 27 / 45; 8 of 2048 x 1408, 16 each 32 / 42).
 inline bool in_tiles(int64_t M, int k, int E) { return M * k >= 10 * E; }
 
 // Blocks for an expert's token tiles: half as many again as it has on average, at most eight; they take more in turn.
